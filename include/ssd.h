@@ -9,8 +9,10 @@
  *   ssm_decode_update   device: single/speculative-token decode state update
  *
  * Next to them: the depthwise causal conv1d that produces x, B and C
- * (ssd_conv1d_varlen / ssd_conv1d_update) and the Mamba1 selective scan with
- * per-channel states (mamba1_scan_varlen / mamba1_state_update).
+ * (ssd_conv1d_varlen / ssd_conv1d_update), the Mamba1 selective scan with
+ * per-channel states (mamba1_scan_varlen / mamba1_state_update), and the
+ * attention layers of a hybrid model (kv_block_tables, kv_qk_norm_rope,
+ * kv_tree_attention, kv_commit_tokens).
  *
  * The recurrence (per head h, group g = h / (nheads / ngroups)):
  *   delta_t = clamp(softplus(dt[t,h] + dt_bias[h]), dt_min, dt_max)
@@ -24,7 +26,8 @@
  * "[vllm] vLLM Mamba2 SSD 커널 웜업", section "mamba_mixer2.py 변경 사항 (핵심)".
  *
  * Conventions shared by every call
- *   - All tensors are dense and row-major (last index fastest).
+ *   - All tensors are dense and row-major (last index fastest), but for the
+ *     rows and blocks that the kv_ calls take a stride for.
  *   - "device" pointers are CUDA global memory of the current device;
  *     "host" pointers are ordinary CPU memory.  The caller owns every buffer.
  *   - Device calls are asynchronous on the given stream.  They launch CUDA
@@ -77,6 +80,7 @@ typedef enum { SSD_F32 = 0, SSD_BF16 = 1 } ssd_dtype_t;
 #define SSD_DEVERR_COLUMN 0x4u   /* num_accepted_tokens outside [0, state_indices_cols) */
 #define SSD_DEVERR_TIMEOUT 0x8u  /* a bounded device-side wait gave up */
 #define SSD_DEVERR_INTERNAL 0x10u /* launch configuration not as the kernel requires (bug) */
+#define SSD_DEVERR_BLOCKS 0x20u /* kv_block_tables: more blocks needed than are free, or than a table row holds */
 
 /* Human-readable name of a status code (static string). */
 SSD_API const char *ssd_status_string(ssd_status_t status);
@@ -516,6 +520,222 @@ SSD_API ssd_status_t mamba1_scan_varlen(const mamba1_args *args, ssd_stream_t st
  * plus tokens_per_req >= 1 and state_indices_cols >= tokens_per_req.  One kernel.
  */
 SSD_API ssd_status_t mamba1_state_update(const mamba1_args *args, ssd_stream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * The attention layers of a hybrid model (device)
+ *
+ * A hybrid model puts a few attention layers between its state-space ones
+ * ("vLLM v0.20.0 하이브리드 SSM 모델을 위한 분산 서빙 추가": one block pool
+ * holds the attention layers' key/value blocks beside the SSM states), and
+ * both see the same step: packed requests, each with the tokens already
+ * computed and 1 + num_spec new ones ("MetadataBuilder 초기화").  Four calls
+ * run an attention layer's part of such a step:
+ *
+ *   kv_block_tables    blocks for the step's tokens, their slots and positions
+ *   kv_qk_norm_rope    per-head norms of q and k, rotation, keys/values to the cache
+ *   kv_tree_attention  the new tokens' attention over cache and one another
+ *   kv_commit_tokens   accepted tokens' keys/values to the cache
+ *
+ * Keys and values live in pages: k_cache and v_cache are
+ * [num_blocks, block_size, kv_heads, headdim] in the token dtype, each block
+ * contiguous, blocks cache_block_stride elements apart (so both may be views
+ * of one allocation).  A token's slot is block * block_size + offset.  The new
+ * tokens of a step need not be in the cache while the step attends: they are
+ * passed on their own, and a step that drafts a tree writes only the tokens
+ * that were accepted.  Query head h reads key head h / (nheads / kv_heads).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * kv_block_tables -- for S requests with context_lens[r] tokens computed and
+ * new_lens[r] to run, let t = context + new, held = ceil(reserved_lens[r] / b)
+ * and need = max(held, ceil(t / b)) with b = block_size.  The need - held
+ * missing blocks of each request, in request order, are taken from the ring of
+ * free block ids, which starts at entry ring_in[0] and holds ring_in[1] ids:
+ *   block_table[r, held + i] = free_ring[(ring_in[0] + taken before r + i) mod free_capacity],
+ * and for new token j of request r at packed row cu_seqlens[r] + j
+ *   positions = context + j
+ *   slots     = block_table[r, positions / b] * b + positions mod b
+ *   token_req = r.
+ * Rows from cu_seqlens[S] to max_tokens are padding: slot -1, position 0,
+ * token_req -1.  A token whose table entry is null_block_id, or (with
+ * SSD_DEVERR_SLOT) outside [0, num_blocks), gets slot -1.  The caller returns
+ * ids of finished requests by writing them behind the ring's last one.
+ *
+ * All or nothing: SSD_DEVERR_METADATA (a negative length, or more than
+ * max_tokens tokens) or SSD_DEVERR_BLOCKS (fewer free blocks than needed, or a
+ * row of more than table_cols) leaves table and ring as they were and gives an
+ * empty step: cu_seqlens all 0, every row padding, seq_lens = context_lens,
+ * reserved_out = reserved_lens, ring_out = ring_in.
+ * Inputs and outputs must not overlap (ring_out is not ring_in, reserved_out
+ * not reserved_lens).  Host checks: sizes, pointers,
+ * num_blocks * block_size < 2^31 (slots are 32 bits wide).  One kernel.
+ */
+typedef struct kv_tables_args {
+    int32_t num_reqs;      /* S */
+    int32_t block_size;    /* b, tokens of a block (>= 1) */
+    int32_t table_cols;    /* columns of a block_table row */
+    int32_t free_capacity; /* entries of free_ring */
+    int32_t max_tokens;    /* rows of the per-token outputs */
+    int32_t num_blocks;    /* valid block ids are [0, num_blocks) */
+    int32_t null_block_id;
+    /* device pointers */
+    const int32_t *context_lens;  /* [S] */
+    const int32_t *new_lens;      /* [S] (0: the request runs nothing in this step) */
+    const int32_t *reserved_lens; /* [S] tokens r's table row has blocks for (the last call's reserved_out) */
+    int32_t *block_table;         /* [S, table_cols], new entries written */
+    const int32_t *free_ring;     /* [free_capacity] */
+    const int32_t *ring_in;       /* [2] first entry in use, ids in the ring */
+    int32_t *ring_out;            /* [2] the same after this call */
+    int32_t *cu_seqlens;          /* [S+1] */
+    int32_t *seq_lens;            /* [S] context + new */
+    int32_t *reserved_out;        /* [S] max(reserved_lens, context + new) */
+    int32_t *slots;               /* [max_tokens] */
+    int32_t *positions;           /* [max_tokens] */
+    int32_t *token_req;           /* [max_tokens] or NULL */
+    uint32_t *err_word;           /* device word or NULL */
+} kv_tables_args;
+SSD_API ssd_status_t kv_block_tables(const kv_tables_args *args, ssd_stream_t stream);
+
+/*
+ * kv_qk_norm_rope -- per token t and head, with D = headdim, R = rotary_dim:
+ *   n = x * w / sqrt(mean(x^2) + eps)       (w NULL: n = x, no norm)
+ *   pairs (i, i + R/2), i < R/2 (interleaved: pairs (2i, 2i + 1)) are rotated:
+ *     n[a] <- n[a] * cos_i - n[b] * sin_i,  n[b] <- n[b] * cos_i + n[a] * sin_i
+ *   with cos_i = cos_sin[positions[t], i], sin_i = cos_sin[positions[t], R/2 + i];
+ *   entries from R on are n as it is.
+ * q goes to q_out, k to k_out and, where slots[t] >= 0, with v (copied) to the
+ * cache.  Arithmetic in fp32, one rounding at the end.  q, k and v rows may be
+ * views of one packed projection (q_stride, k_stride, v_stride elements from
+ * token to token); q_out may be q itself when q is dense, k_out likewise.
+ * A position outside [0, max_position) sets SSD_DEVERR_METADATA and nothing of
+ * that token is written; a slot of num_blocks * block_size or more sets
+ * SSD_DEVERR_SLOT and the cache is not written for it.  Slots must be distinct.
+ * Host checks: sizes, headdim a multiple of 8 up to 256, rotary_dim even and
+ * at most headdim, strides a multiple of 16 bytes, pointers and alignments
+ * (16 bytes; positions, slots 4).  One kernel.
+ */
+typedef struct kv_qk_args {
+    int32_t total_tokens; /* T */
+    int32_t nheads;       /* query heads */
+    int32_t kv_heads;     /* key/value heads */
+    int32_t headdim;      /* D */
+    int32_t rotary_dim;   /* R (0: no rotation) */
+    int32_t interleaved;
+    int32_t max_position; /* rows of cos_sin */
+    int32_t dtype;        /* ssd_dtype_t of q, k, v, the outputs and the cache */
+    int32_t block_size, num_blocks; /* cache pages (used with k_cache) */
+    float eps;
+    int64_t q_stride, k_stride, v_stride; /* elements from one token to the next */
+    int64_t cache_block_stride;           /* elements from one block to the next */
+    /* device pointers */
+    const void *q, *k;        /* [T, nheads, D], [T, kv_heads, D] */
+    const void *v;            /* [T, kv_heads, D]; only read for the cache */
+    const float *q_weight;    /* [D] or NULL */
+    const float *k_weight;    /* [D] or NULL */
+    const float *cos_sin;     /* [max_position, R] (NULL when R is 0) */
+    const int32_t *positions; /* [T] (NULL when R is 0) */
+    const int32_t *slots;     /* [T], negative: not cached; NULL with k_cache NULL */
+    void *q_out;              /* [T, nheads, D] dense */
+    void *k_out;              /* [T, kv_heads, D] dense, or NULL */
+    void *k_cache, *v_cache;  /* pages, or both NULL */
+    uint32_t *err_word;       /* device word or NULL */
+} kv_qk_args;
+SSD_API ssd_status_t kv_qk_norm_rope(const kv_qk_args *args, ssd_stream_t stream);
+
+/*
+ * kv_tree_attention -- the new tokens of every request attend to its
+ * context_lens[r] cached tokens (positions 0 .. context-1, through
+ * block_table) and to its own new tokens: token i sees new token j when bit j
+ * of its mask row is set (bit j mod 32 of word j / 32), or, without a mask,
+ * when j <= i (a chain: prompts, single-token decode, draft chains).
+ *   s = scale * q . k;  out = sum softmax(s) v;  lse = log(sum exp(s))
+ * over what it sees; a token that sees nothing gets out = 0, lse = -inf.  What
+ * is not seen does not enter the result whatever it holds (NaN in stale page
+ * rows, in rejected drafts).  Softmax statistics and sums are fp32.
+ * bf16 with headdim 64 or 128, at most 128 query heads to a key head, block_size a
+ * multiple of 8 and 16-byte strides runs on the tensor cores, its probabilities
+ * rounded to bf16; everything else, fp32 above all, on the CUDA cores in fp32.
+ *
+ * Work is cut into equal shares over the GPU along requests, heads, query
+ * tiles and keys, from lengths the kernel reads on the device; a share that
+ * ends inside a tile's keys leaves its sums in the workspace and a second
+ * kernel joins them.  Results do not depend on timing: the same call gives the
+ * same bits.
+ * Errors on the device: SSD_DEVERR_METADATA for cu_seqlens entries that decrease or
+ * leave [0, T], a context beyond the table row, or more new tokens than mask
+ * bits (that request's rows are left unwritten); SSD_DEVERR_SLOT for a block
+ * id outside [0, num_blocks) (its keys and values count as zeros);
+ * SSD_DEVERR_TIMEOUT as for the prefill.
+ * Host checks: sizes, nheads a multiple of kv_heads, headdim a multiple of 8
+ * up to 256, strides of 16 bytes, pointers and alignments, finite scale.
+ */
+typedef struct kv_attention_args {
+    int32_t total_tokens; /* T, rows of q */
+    int32_t num_seqs;     /* S */
+    int32_t nheads, kv_heads, headdim;
+    int32_t dtype;        /* ssd_dtype_t of q, k_new, v_new, the cache and out */
+    int32_t block_size, num_blocks, table_cols;
+    int32_t max_new_tokens; /* most new tokens of a request: sizes the tiles, results do not depend on it */
+    int32_t mask_words;     /* 32-bit words of a tree_mask row (0 with tree_mask NULL) */
+    float scale;
+    int64_t q_stride, k_stride, v_stride; /* elements from one token to the next */
+    int64_t cache_block_stride;           /* elements from one block to the next */
+    int64_t wait_limit_cycles;            /* as ssd_prefill_args.wait_limit_cycles */
+    /* device pointers */
+    const void *q;              /* [T, nheads, D] */
+    const void *k_new, *v_new;  /* [T, kv_heads, D] */
+    const void *k_cache, *v_cache;
+    const int32_t *cu_seqlens;   /* [S+1] */
+    const int32_t *context_lens; /* [S] */
+    const int32_t *block_table;  /* [S, table_cols] */
+    const uint32_t *tree_mask;   /* [T, mask_words] or NULL (chain) */
+    void *out;                   /* [T, nheads, D] dense */
+    float *lse;                  /* [T, nheads] or NULL */
+    uint32_t *err_word;          /* device word or NULL */
+} kv_attention_args;
+
+/* Bytes of device workspace kv_tree_attention needs (sizes only are read) on
+ * the current device; 0 on invalid sizes or an empty call. */
+SSD_API size_t kv_tree_attention_workspace_size(const kv_attention_args *args);
+/* workspace: 256-byte aligned, caller-owned, no initial contents required, not
+ * shared with a concurrent call. */
+SSD_API ssd_status_t kv_tree_attention(const kv_attention_args *args, void *workspace, size_t workspace_bytes,
+                                       ssd_stream_t stream);
+
+/*
+ * kv_commit_tokens -- keys and values of accepted tokens to the cache: with
+ * n = path_lens[r] (path NULL: all new tokens of r, in order),
+ *   cache[slots[cu_seqlens[r] + i]] = new[cu_seqlens[r] + path[r, i]],  i < n
+ * (an accepted path of a drafted tree closes up to the positions behind the
+ * context), and context_out[r] = context_lens[r] + n.  Negative slots are
+ * skipped.  SSD_DEVERR_METADATA: n outside [0, max_path], more than the
+ * request's new tokens, or a path entry that is none of them;
+ * SSD_DEVERR_SLOT: a slot of num_blocks * block_size or more.  The rows
+ * concerned are not copied; context_out is context_lens where n is refused.
+ * Slots written must be distinct.  Host checks: sizes, kv_heads * headdim a multiple
+ * of 16 bytes, strides of 16 bytes, pointers and alignments.  One kernel.
+ */
+typedef struct kv_commit_args {
+    int32_t total_tokens; /* T, rows of k_new, v_new and slots */
+    int32_t num_seqs;     /* S */
+    int32_t kv_heads, headdim;
+    int32_t dtype;
+    int32_t block_size, num_blocks;
+    int32_t max_path;     /* columns of path (0 with path NULL) */
+    int64_t k_stride, v_stride;  /* elements from one token to the next */
+    int64_t cache_block_stride;  /* elements from one block to the next */
+    /* device pointers */
+    const void *k_new, *v_new;   /* [T, kv_heads, D] */
+    const int32_t *slots;        /* [T] */
+    const int32_t *cu_seqlens;   /* [S+1] */
+    const int32_t *path;         /* [S, max_path] or NULL */
+    const int32_t *path_lens;    /* [S] (NULL with path NULL) */
+    const int32_t *context_lens; /* [S] or NULL */
+    int32_t *context_out;        /* [S] or NULL (both or neither) */
+    void *k_cache, *v_cache;
+    uint32_t *err_word;          /* device word or NULL */
+} kv_commit_args;
+SSD_API ssd_status_t kv_commit_tokens(const kv_commit_args *args, ssd_stream_t stream);
 
 #ifdef __cplusplus
 }

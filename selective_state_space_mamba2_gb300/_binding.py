@@ -18,17 +18,20 @@ LIB_PATH = os.path.join(_PKG, "libssd_gb300.so")
 
 SSD_OK, SSD_ERR_INVALID_ARG, SSD_ERR_UNSUPPORTED, SSD_ERR_WORKSPACE, SSD_ERR_CUDA = range(5)
 SSD_F32, SSD_BF16 = 0, 1
-DEVERR_SLOT, DEVERR_METADATA, DEVERR_COLUMN, DEVERR_TIMEOUT, DEVERR_INTERNAL = 1, 2, 4, 8, 16
+DEVERR_SLOT, DEVERR_METADATA, DEVERR_COLUMN, DEVERR_TIMEOUT, DEVERR_INTERNAL, DEVERR_BLOCKS = 1, 2, 4, 8, 16, 32
 
 EXPORTED_SYMBOLS = ("ssd_status_string", "ssd_abi_version", "ssd_max_chunks", "ssd_chunk_metadata",
                     "ssd_prefill_workspace_size", "ssd_prefill_kernel_count", "ssd_prefill_varlen",
                     "ssd_prefill_varlen_marked", "ssd_prefill_varlen_noalloc", "ssm_decode_update", "ssd_mixed_step",
                     "ssd_conv1d_varlen",
                     "ssd_conv1d_update",
-                    "mamba1_scan_varlen", "mamba1_state_update")
+                    "mamba1_scan_varlen", "mamba1_state_update",
+                    "kv_block_tables", "kv_qk_norm_rope", "kv_tree_attention_workspace_size", "kv_tree_attention",
+                    "kv_commit_tokens")
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
 _f32 = ctypes.c_float
 
 
@@ -72,6 +75,44 @@ class Mamba1Args(ctypes.Structure):
                 ("dt_bias", _vp), ("cu_seqlens", _vp), ("cu_chunk_seqlens", _vp), ("last_chunk_indices", _vp),
                 ("init_slot", _vp), ("chunk_slot", _vp), ("state_indices", _vp), ("num_accepted_tokens", _vp),
                 ("state_cache", _vp), ("y", _vp), ("err_word", _vp)]
+
+
+class TablesArgs(ctypes.Structure):
+    _fields_ = [("num_reqs", _i32), ("block_size", _i32), ("table_cols", _i32), ("free_capacity", _i32),
+                ("max_tokens", _i32), ("num_blocks", _i32), ("null_block_id", _i32),
+                ("context_lens", _vp), ("new_lens", _vp), ("reserved_lens", _vp), ("block_table", _vp),
+                ("free_ring", _vp), ("ring_in", _vp), ("ring_out", _vp), ("cu_seqlens", _vp), ("seq_lens", _vp),
+                ("reserved_out", _vp), ("slots", _vp), ("positions", _vp), ("token_req", _vp), ("err_word", _vp)]
+
+
+class QkArgs(ctypes.Structure):
+    _fields_ = [("total_tokens", _i32), ("nheads", _i32), ("kv_heads", _i32), ("headdim", _i32),
+                ("rotary_dim", _i32), ("interleaved", _i32), ("max_position", _i32), ("dtype", _i32),
+                ("block_size", _i32), ("num_blocks", _i32), ("eps", _f32),
+                ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64), ("cache_block_stride", _i64),
+                ("q", _vp), ("k", _vp), ("v", _vp), ("q_weight", _vp), ("k_weight", _vp), ("cos_sin", _vp),
+                ("positions", _vp), ("slots", _vp), ("q_out", _vp), ("k_out", _vp), ("k_cache", _vp),
+                ("v_cache", _vp), ("err_word", _vp)]
+
+
+class AttentionArgs(ctypes.Structure):
+    _fields_ = [("total_tokens", _i32), ("num_seqs", _i32), ("nheads", _i32), ("kv_heads", _i32),
+                ("headdim", _i32), ("dtype", _i32), ("block_size", _i32), ("num_blocks", _i32),
+                ("table_cols", _i32), ("max_new_tokens", _i32), ("mask_words", _i32), ("scale", _f32),
+                ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64), ("cache_block_stride", _i64),
+                ("wait_limit_cycles", _i64),
+                ("q", _vp), ("k_new", _vp), ("v_new", _vp), ("k_cache", _vp), ("v_cache", _vp),
+                ("cu_seqlens", _vp), ("context_lens", _vp), ("block_table", _vp), ("tree_mask", _vp),
+                ("out", _vp), ("lse", _vp), ("err_word", _vp)]
+
+
+class CommitArgs(ctypes.Structure):
+    _fields_ = [("total_tokens", _i32), ("num_seqs", _i32), ("kv_heads", _i32), ("headdim", _i32),
+                ("dtype", _i32), ("block_size", _i32), ("num_blocks", _i32), ("max_path", _i32),
+                ("k_stride", _i64), ("v_stride", _i64), ("cache_block_stride", _i64),
+                ("k_new", _vp), ("v_new", _vp), ("slots", _vp), ("cu_seqlens", _vp), ("path", _vp),
+                ("path_lens", _vp), ("context_lens", _vp), ("context_out", _vp), ("k_cache", _vp),
+                ("v_cache", _vp), ("err_word", _vp)]
 
 
 class SSDError(RuntimeError):
@@ -121,6 +162,13 @@ def lib():
         for fn in ("mamba1_scan_varlen", "mamba1_state_update"):
             getattr(L, fn).restype = ctypes.c_int
             getattr(L, fn).argtypes = [ctypes.POINTER(Mamba1Args), _vp]
+        for fn, st in (("kv_block_tables", TablesArgs), ("kv_qk_norm_rope", QkArgs), ("kv_commit_tokens", CommitArgs)):
+            getattr(L, fn).restype = ctypes.c_int
+            getattr(L, fn).argtypes = [ctypes.POINTER(st), _vp]
+        L.kv_tree_attention_workspace_size.restype = ctypes.c_size_t
+        L.kv_tree_attention_workspace_size.argtypes = [ctypes.POINTER(AttentionArgs)]
+        L.kv_tree_attention.restype = ctypes.c_int
+        L.kv_tree_attention.argtypes = [ctypes.POINTER(AttentionArgs), _vp, ctypes.c_size_t, _vp]
         _lib = L
     return _lib
 
@@ -523,3 +571,229 @@ def mamba1_state_update(x, dt, A, B, C, state_cache, state_indices, num_accepted
     if rc != SSD_OK:
         raise SSDError("mamba1_state_update", rc)
     return out
+
+
+# ------------------------------------------- attention layers of a hybrid model --
+
+def _i32v(t, name, shape, required=True):
+    """Pointer of a device int32 tensor of that shape."""
+    p = _dev(t, name, torch.int32, required)
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError("%s must be int32 of shape %s" % (name, list(shape)))
+    return p
+
+
+def _rows(t, name, shape, dtype):
+    """Pointer and token stride (elements) of a device tensor [T, heads, D] whose tokens are dense rows."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if tuple(t.shape) != shape or t.dtype != dtype:
+        raise ValueError("%s must be %s of shape %s" % (name, dtype, list(shape)))
+    T, H, D = shape
+    if T == 0:
+        return t.data_ptr(), H * D
+    s = t.stride()
+    if s[2] != 1 or (H > 1 and s[1] != D):
+        raise ValueError("the rows of %s must be dense" % name)
+    return t.data_ptr(), (s[0] if T > 1 else H * D)
+
+
+def _pages(k_cache, v_cache, H, D, dtype):
+    """Pointers, sizes and block stride of k_cache and v_cache ([num_blocks, block_size, H, D])."""
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % name)
+        if t.dim() != 4 or t.dtype != dtype or tuple(t.shape[2:]) != (H, D) or t.shape != k_cache.shape:
+            raise ValueError("%s must be %s [num_blocks, block_size, %d, %d]" % (name, dtype, H, D))
+        s = t.stride()
+        if s[3] != 1 or (H > 1 and s[2] != D) or (t.shape[1] > 1 and s[1] != H * D):
+            raise ValueError("the blocks of %s must be dense" % name)
+    nb, bs = k_cache.shape[:2]
+    stride = k_cache.stride(0) if nb > 1 else bs * H * D
+    if nb > 1 and v_cache.stride(0) != stride:
+        raise ValueError("k_cache and v_cache must have the same block stride")
+    return k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, stride
+
+
+def kv_block_tables(context_lens, new_lens, reserved_lens, block_table, free_ring, ring_state, block_size, num_blocks,
+                    max_tokens, null_block_id=0, out=None, err_word=None, stream=None):
+    """Blocks, slots and positions of a step's tokens, from the requests' lengths on the device (see
+    ``kv_block_tables`` in ssd.h).  ``block_table`` [S, cols] is extended in place with ids from ``free_ring``,
+    whose ``ring_state`` is (first entry, ids in it).  Returns a dict of int32 device tensors: cu_seqlens [S+1],
+    seq_lens [S], reserved_lens [S] and ring_state [2] (for the next call), slots, positions and token_req
+    [max_tokens].  ``out``: such a dict from an earlier call to write to instead (not the one whose
+    reserved_lens or ring_state this call reads)."""
+    S = context_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != S:
+        raise ValueError("block_table must be int32 [%d, cols]" % S)
+    if out is None:
+        i32 = dict(dtype=torch.int32, device=context_lens.device)
+        out = dict(cu_seqlens=torch.empty(S + 1, **i32), seq_lens=torch.empty(S, **i32),
+                   reserved_lens=torch.empty(S, **i32), ring_state=torch.empty(2, **i32),
+                   slots=torch.empty(max_tokens, **i32), positions=torch.empty(max_tokens, **i32),
+                   token_req=torch.empty(max_tokens, **i32))
+    a = TablesArgs()
+    a.num_reqs, a.block_size, a.table_cols = S, int(block_size), block_table.shape[1]
+    a.free_capacity, a.max_tokens, a.num_blocks = free_ring.numel(), int(max_tokens), int(num_blocks)
+    a.null_block_id = int(null_block_id)
+    a.context_lens = _i32v(context_lens, "context_lens", (S,))
+    a.new_lens = _i32v(new_lens, "new_lens", (S,))
+    a.reserved_lens = _i32v(reserved_lens, "reserved_lens", (S,))
+    a.block_table = _dev(block_table, "block_table", torch.int32)
+    a.free_ring = _dev(free_ring, "free_ring", torch.int32)
+    a.ring_in = _i32v(ring_state, "ring_state", (2,))
+    a.ring_out = _i32v(out["ring_state"], "out ring_state", (2,))
+    a.cu_seqlens = _i32v(out["cu_seqlens"], "out cu_seqlens", (S + 1,))
+    a.seq_lens = _i32v(out["seq_lens"], "out seq_lens", (S,))
+    a.reserved_out = _i32v(out["reserved_lens"], "out reserved_lens", (S,))
+    a.slots = _i32v(out["slots"], "out slots", (max_tokens,))
+    a.positions = _i32v(out["positions"], "out positions", (max_tokens,))
+    a.token_req = _i32v(out.get("token_req"), "out token_req", (max_tokens,), required=False)
+    a.err_word = _dev(err_word, "err_word", required=False)
+    rc = lib().kv_block_tables(ctypes.byref(a), _stream(stream))
+    if rc != SSD_OK:
+        raise SSDError("kv_block_tables", rc)
+    return out
+
+
+def kv_qk_norm_rope(q, k, positions=None, cos_sin=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                    v=None, k_cache=None, v_cache=None, slots=None, q_out=None, k_out=None, err_word=None,
+                    stream=None):
+    """Per-head norms of q [T, H, D] and k [T, Hkv, D] (``q_weight``, ``k_weight`` float32 [D], or None for no norm)
+    and their rotation by the rows ``positions`` of ``cos_sin`` (float32 [max_position, rotary_dim], cosines then
+    sines; None for none), in one pass; with ``k_cache``, ``v_cache`` and ``slots`` the keys and ``v`` go to the
+    cache too.  q, k and v may be views of one packed projection.  Returns (q_out, k_out)."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [T, heads, D]")
+    T, H, D = q.shape
+    Hkv = k.shape[1]
+    if q_out is None:
+        q_out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty((T, Hkv, D), dtype=q.dtype, device=q.device)
+    a = QkArgs()
+    a.total_tokens, a.nheads, a.kv_heads, a.headdim, a.dtype = T, H, Hkv, D, _dtype_code(q)
+    a.interleaved, a.eps = int(bool(interleaved)), float(eps)
+    a.q, a.q_stride = _rows(q, "q", (T, H, D), q.dtype)
+    a.k, a.k_stride = _rows(k, "k", (T, Hkv, D), q.dtype)
+    for name, t, heads in (("q_out", q_out, H), ("k_out", k_out, Hkv)):
+        if tuple(t.shape) != (T, heads, D) or t.dtype != q.dtype:
+            raise ValueError("%s must be %s of shape %s" % (name, q.dtype, [T, heads, D]))
+    a.q_out, a.k_out = _dev(q_out, "q_out"), _dev(k_out, "k_out")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and tuple(w.shape) != (D,):
+            raise ValueError("%s must be float32 [%d]" % (name, D))
+    a.q_weight = _dev(q_weight, "q_weight", torch.float32, required=False)
+    a.k_weight = _dev(k_weight, "k_weight", torch.float32, required=False)
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
+        a.max_position, a.rotary_dim = cos_sin.shape
+        a.cos_sin = _dev(cos_sin, "cos_sin", torch.float32)
+        a.positions = _i32v(positions, "positions", (T,))
+    if k_cache is not None or v_cache is not None or slots is not None:
+        a.k_cache, a.v_cache, a.num_blocks, a.block_size, a.cache_block_stride = _pages(k_cache, v_cache, Hkv, D, q.dtype)
+        a.v, a.v_stride = _rows(v, "v", (T, Hkv, D), q.dtype)
+        a.slots = _i32v(slots, "slots", (T,))
+    a.err_word = _dev(err_word, "err_word", required=False)
+    rc = lib().kv_qk_norm_rope(ctypes.byref(a), _stream(stream))
+    if rc != SSD_OK:
+        raise SSDError("kv_qk_norm_rope", rc)
+    return q_out, k_out
+
+
+def attention_args(q, k_new, v_new, k_cache, v_cache, cu_seqlens, context_lens, block_table, out, max_new_tokens,
+                   tree_mask=None, scale=None, lse=None, err_word=None, wait_limit_cycles=0):
+    """Fills an ``AttentionArgs`` from device tensors (validating shapes and dtypes)."""
+    if q.dim() != 3 or k_new.dim() != 3:
+        raise ValueError("q and k_new must be [T, heads, D]")
+    T, H, D = q.shape
+    Hkv = k_new.shape[1]
+    S = cu_seqlens.numel() - 1
+    if block_table.dim() != 2 or block_table.shape[0] != S:
+        raise ValueError("block_table must be int32 [%d, cols]" % S)
+    if tuple(out.shape) != (T, H, D) or out.dtype != q.dtype:
+        raise ValueError("out must be %s of shape %s" % (q.dtype, [T, H, D]))
+    a = AttentionArgs()
+    a.total_tokens, a.num_seqs, a.nheads, a.kv_heads, a.headdim, a.dtype = T, S, H, Hkv, D, _dtype_code(q)
+    a.table_cols, a.max_new_tokens = block_table.shape[1], int(max_new_tokens)
+    a.scale = float(D ** -0.5 if scale is None else scale)
+    a.wait_limit_cycles = int(wait_limit_cycles)
+    a.q, a.q_stride = _rows(q, "q", (T, H, D), q.dtype)
+    a.k_new, a.k_stride = _rows(k_new, "k_new", (T, Hkv, D), q.dtype)
+    a.v_new, a.v_stride = _rows(v_new, "v_new", (T, Hkv, D), q.dtype)
+    a.k_cache, a.v_cache, a.num_blocks, a.block_size, a.cache_block_stride = _pages(k_cache, v_cache, Hkv, D, q.dtype)
+    a.cu_seqlens = _i32v(cu_seqlens, "cu_seqlens", (S + 1,))
+    a.context_lens = _i32v(context_lens, "context_lens", (S,))
+    a.block_table = _dev(block_table, "block_table", torch.int32)
+    if tree_mask is not None:
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != T:
+            raise ValueError("tree_mask must be int32 [%d, words]" % T)
+        a.tree_mask, a.mask_words = _dev(tree_mask, "tree_mask", torch.int32), tree_mask.shape[1]
+    a.out = _dev(out, "out")
+    if lse is not None:
+        if tuple(lse.shape) != (T, H):
+            raise ValueError("lse must be float32 of shape %s" % [T, H])
+        a.lse = _dev(lse, "lse", torch.float32)
+    a.err_word = _dev(err_word, "err_word", required=False)
+    return a
+
+
+def kv_tree_attention_workspace_size(args):
+    return int(lib().kv_tree_attention_workspace_size(ctypes.byref(args)))
+
+
+def kv_tree_attention(q, k_new, v_new, k_cache, v_cache, cu_seqlens, context_lens, block_table, max_new_tokens,
+                      tree_mask=None, scale=None, out=None, lse=None, return_lse=False, workspace=None,
+                      err_word=None, stream=None, wait_limit_cycles=0):
+    """Attention of every request's new tokens (packed, ``cu_seqlens``) over its ``context_lens`` cached ones and
+    one another: bit j of a row of ``tree_mask`` (int32 [T, words]) lets the token see its request's new token j;
+    without a mask the new tokens are a chain.  ``scale`` defaults to D ** -0.5.  Returns ``out`` [T, H, D], or
+    (out, lse [T, H] float32) with ``return_lse`` or ``lse``."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    a = attention_args(q, k_new, v_new, k_cache, v_cache, cu_seqlens, context_lens, block_table, out, max_new_tokens,
+                       tree_mask, scale, lse, err_word, wait_limit_cycles)
+    if workspace is None:
+        workspace = torch.empty(max(kv_tree_attention_workspace_size(a), 1), dtype=torch.uint8, device=q.device)
+    rc = lib().kv_tree_attention(ctypes.byref(a), workspace.data_ptr(), workspace.numel(), _stream(stream))
+    if rc != SSD_OK:
+        raise SSDError("kv_tree_attention", rc)
+    return out if lse is None else (out, lse)
+
+
+def kv_commit_tokens(k_new, v_new, k_cache, v_cache, slots, cu_seqlens=None, context_lens=None, path=None,
+                     path_lens=None, context_out=None, err_word=None, stream=None):
+    """Keys and values of accepted tokens to the cache: step i of request r's ``path`` ([S, max_path], the index of
+    a new token; None: all of them in order) goes to the slot of its new token i.  Returns the new context
+    lengths, or None without ``context_lens``."""
+    if k_new.dim() != 3:
+        raise ValueError("k_new must be [T, heads, D]")
+    T, H, D = k_new.shape
+    S = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
+    a = CommitArgs()
+    a.total_tokens, a.num_seqs, a.kv_heads, a.headdim, a.dtype = T, S, H, D, _dtype_code(k_new)
+    a.k_new, a.k_stride = _rows(k_new, "k_new", (T, H, D), k_new.dtype)
+    a.v_new, a.v_stride = _rows(v_new, "v_new", (T, H, D), k_new.dtype)
+    a.k_cache, a.v_cache, a.num_blocks, a.block_size, a.cache_block_stride = _pages(k_cache, v_cache, H, D, k_new.dtype)
+    a.slots = _dev(slots, "slots", torch.int32)
+    if slots.numel() < T:  # a step's slot map may be padded beyond its tokens
+        raise ValueError("slots must have an entry for each of the %d tokens" % T)
+    a.cu_seqlens = _dev(cu_seqlens, "cu_seqlens", torch.int32, required=path is not None or context_lens is not None)
+    if path is not None:
+        if path.dim() != 2 or path.shape[0] != S or path.shape[1] == 0:
+            raise ValueError("path must be int32 [%d, max_path]" % S)
+        a.path, a.max_path = _dev(path, "path", torch.int32), path.shape[1]
+        a.path_lens = _i32v(path_lens, "path_lens", (S,))
+    if context_lens is not None:
+        if context_out is None:
+            context_out = torch.empty_like(context_lens)
+        a.context_lens = _i32v(context_lens, "context_lens", (S,))
+        a.context_out = _i32v(context_out, "context_out", (S,))
+    a.err_word = _dev(err_word, "err_word", required=False)
+    rc = lib().kv_commit_tokens(ctypes.byref(a), _stream(stream))
+    if rc != SSD_OK:
+        raise SSDError("kv_commit_tokens", rc)
+    return context_out

@@ -1,0 +1,309 @@
+// kv_tree_attention on the CUDA cores, in fp32: every type, head size, group and page size the
+// tensor-core kernel does not take, and the kernel that joins the parts of cut items.
+//
+// Online softmax over key tiles of 32 for 16 query rows a CTA: keys and values of a tile are
+// staged in shared memory as fp32, a thread owns one row's 4 scores of a tile and an eighth of
+// its output.  Bound by shared-memory reads (one 16-byte read for 4 multiply-adds); its use is
+// fp32 decode, where few rows meet each key.
+#include "kv_sched.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kRowTile = 16;
+constexpr int kKeyTile = 32;
+constexpr int kMinUnits = 4;
+constexpr int kCtasPerSm = 4;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+constexpr int smem_bytes(int D) { return (kRowTile * (D + 4) + 2 * kKeyTile * (D + 4) + kRowTile * (kKeyTile + 1)) * 4; }
+
+template <typename T> __device__ __forceinline__ void load8(float (&f)[8], const T *p);
+template <> __device__ __forceinline__ void load8<float>(float (&f)[8], const float *p) {
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+template <> __device__ __forceinline__ void load8<__nv_bfloat16>(float (&f)[8], const __nv_bfloat16 *p) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+// NV: 32-float pieces of a row a thread group covers, headdim <= 32 NV
+template <typename T, int NV>
+__global__ void __launch_bounds__(kThreads) kv_attention_simt_kernel(const kv_attention_args a, const kvs::Parts parts) {
+    extern __shared__ __align__(16) float smem[];
+    __shared__ kvs::FindSmem find;
+    const int D = a.headdim, group = a.nheads / a.kv_heads, pitch = D + 4;
+    float *sq = smem, *sk = sq + kRowTile * pitch, *sv = sk + kKeyTile * pitch, *sp = sv + kKeyTile * pitch;
+    const int tid = threadIdx.x, row = tid >> 3, sub = tid & 7;
+
+    kvs::Walk w;
+    if (!kvs::find_run(a, group, kRowTile, kKeyTile, kMinUnits, find, parts.borders, w)) return;
+    const float c = a.scale * kLog2e;
+    const int pieces = D / 8;
+    bool more = true;
+    while (more) {
+        const int rows = (int)min((int64_t)kRowTile, (int64_t)w.q.n * group - (int64_t)w.m * kRowTile);
+        // query rows
+        __syncthreads();
+        for (int i = tid; i < kRowTile * pieces; i += kThreads) {
+            const int r = i / pieces, e = (i % pieces) * 8;
+            float f[8] = {};
+            if (r < rows) {
+                const int64_t flat = (int64_t)w.m * kRowTile + r;
+                const int64_t tok = w.q.q0 + flat / group;
+                load8(f, static_cast<const T *>(a.q) + tok * a.q_stride + (w.h * group + flat % group) * D + e);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sq[r * pitch + e + j] = f[j];
+        }
+        const int64_t my_flat = (int64_t)w.m * kRowTile + row;
+        const int32_t my_tok = row < rows ? (int32_t)(my_flat / group) : -1;
+        const uint32_t *mask = a.tree_mask && my_tok >= 0 ? a.tree_mask + (int64_t)(w.q.q0 + my_tok) * a.mask_words : nullptr;
+
+        float top = -INFINITY, sum = 0.f, acc[NV][4] = {};
+        for (int t = w.t0; t < w.t1; ++t) {
+            const bool cached = t < w.cached_tiles;
+            const int32_t base = (cached ? t : t - w.cached_tiles) * kKeyTile;
+            const int32_t limit = cached ? w.q.c : w.new_seen;  // keys from here on do not exist
+            __syncthreads();
+            for (int i = tid; i < kKeyTile * pieces; i += kThreads) {
+                const int key = i / pieces, e = (i % pieces) * 8;
+                const int32_t pos = base + key;
+                float fk[8] = {}, fv[8] = {};
+                if (pos < limit) {
+                    if (cached) {
+                        const int32_t col = pos / a.block_size;
+                        const int32_t id = a.block_table[(int64_t)w.r * a.table_cols + col];
+                        if (id >= 0 && id < a.num_blocks) {
+                            const int64_t at = (int64_t)id * a.cache_block_stride +
+                                               ((int64_t)(pos - col * a.block_size) * a.kv_heads + w.h) * D + e;
+                            load8(fk, static_cast<const T *>(a.k_cache) + at);
+                            load8(fv, static_cast<const T *>(a.v_cache) + at);
+                        } else if (e == 0) {
+                            report(a.err_word, SSD_DEVERR_SLOT);
+                        }
+                    } else {
+                        const int64_t tok = w.q.q0 + pos;
+                        load8(fk, static_cast<const T *>(a.k_new) + tok * a.k_stride + w.h * D + e);
+                        load8(fv, static_cast<const T *>(a.v_new) + tok * a.v_stride + w.h * D + e);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    sk[key * pitch + e + j] = fk[j];
+                    sv[key * pitch + e + j] = fv[j];
+                }
+            }
+            __syncthreads();
+            // scores of keys sub + 8 j
+            float s[4] = {};
+            for (int e = 0; e < D; e += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(sq + row * pitch + e);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 y = *reinterpret_cast<const float4 *>(sk + (sub + 8 * j) * pitch + e);
+                    s[j] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s[j]))));
+                }
+            }
+            float best = -INFINITY;
+            bool sees[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int32_t pos = base + sub + 8 * j;
+                sees[j] = pos < limit && my_tok >= 0;
+                if (!cached && sees[j])
+                    sees[j] = mask ? (mask[pos >> 5] >> (pos & 31)) & 1u : pos <= my_tok;
+                s[j] = sees[j] ? s[j] * c : -INFINITY;
+                best = s[j] > best || s[j] != s[j] ? s[j] : best;
+            }
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) {
+                const float v = __shfl_xor_sync(~0u, best, o);
+                best = v > best || v != v ? v : best;
+            }
+            const float now = best > top || best != best ? best : top;
+            const float from = now == -INFINITY ? 0.f : now;  // nothing seen yet: weights are exp2(-inf) = 0
+            const float shrink = exp2f(top - from);
+            top = now;
+            sum *= shrink;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = exp2f(s[j] - from);
+                sp[row * (kKeyTile + 1) + sub + 8 * j] = sees[j] ? p : 0.f;
+                sum += sees[j] ? p : 0.f;
+            }
+            __syncwarp();  // a row's weights are written and read by the same warp
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[v][j] *= shrink;
+            for (int key = 0; key < kKeyTile; ++key) {
+                const float p = sp[row * (kKeyTile + 1) + key];
+                if (p == 0.f) continue;  // not seen: its value stays out, whatever it is
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const int e = 32 * v + 4 * sub;
+                    if (e < D) {
+                        const float4 y = *reinterpret_cast<const float4 *>(sv + key * pitch + e);
+                        acc[v][0] = fmaf(p, y.x, acc[v][0]);
+                        acc[v][1] = fmaf(p, y.y, acc[v][1]);
+                        acc[v][2] = fmaf(p, y.z, acc[v][2]);
+                        acc[v][3] = fmaf(p, y.w, acc[v][3]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        if (my_tok >= 0) {
+            if (w.whole()) {
+                const int64_t out_row = (int64_t)(w.q.q0 + my_tok) * a.nheads + w.h * group + my_flat % group;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that saw nothing: zeros
+                T *out = static_cast<T *>(a.out) + out_row * D;
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const int e = 32 * v + 4 * sub;
+                    if (e < D)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) out[e + j] = from_f32<T>(acc[v][j] * inv);
+                }
+                if (a.lse && sub == 0) a.lse[out_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+            } else {
+                const int64_t part = ((int64_t)blockIdx.x * 2 + (w.t0 > 0 ? 0 : 1)) * kRowTile + row;
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const int e = 32 * v + 4 * sub;
+                    if (e < D) *reinterpret_cast<float4 *>(parts.sums + part * D + e) =
+                        make_float4(acc[v][0], acc[v][1], acc[v][2], acc[v][3]);
+                }
+                if (sub == 0) parts.stats[part] = make_float2(top, sum);
+            }
+        }
+        more = w.next(a, group, kRowTile, kKeyTile);
+    }
+}
+
+// ---- joining the parts of a cut item -----------------------------------------------
+//
+// CTA b looks at the border before CTA b's run.  If it cuts an item and is the first border in
+// it, this CTA adds up the item's parts: the one of CTA b - 1 (begun there) and those of b and
+// the CTAs after it while their runs start inside the item.  out = sum_i 2^(m_i - m) O_i / L.
+constexpr int kJoinThreads = 128;
+constexpr int kJoinRows = 4;  // rows of an item joined by one CTA, a warp each
+
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const kv_attention_args a, const kvs::Parts parts,
+                                                               const int row_tile) {
+    const int b = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ctas = parts.borders[0].ctas;
+    if (b >= ctas) return;
+    const kvs::Border me = parts.borders[b];
+    if (me.item0 == me.lo || parts.borders[b - 1].lo > me.item0) return;  // not cut here, or joined by an earlier one
+    const int D = a.headdim, group = a.nheads / a.kv_heads;
+    const kvs::Request q = kvs::request(a, me.r, false);
+    const int row = blockIdx.y * kJoinRows + warp;
+    const int64_t flat = (int64_t)me.m * row_tile + row;
+    if (row >= row_tile || flat >= (int64_t)q.n * group) return;
+    int last = b;  // last CTA with a part
+    while (last + 1 < ctas && parts.borders[last + 1].lo < me.item1) ++last;
+    auto part_row = [&](int cta) { return ((int64_t)cta * 2 + (cta == b - 1 ? 1 : 0)) * row_tile + row; };
+    float top = -INFINITY;
+    for (int i = b - 1 + lane; i <= last; i += 32) {
+        const float m = parts.stats[part_row(i)].x;
+        top = m > top || m != m ? m : top;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float m = __shfl_xor_sync(~0u, top, o);
+        top = m > top || m != m ? m : top;
+    }
+    const float from = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, acc[8] = {};  // headdim <= 256: 8 entries a lane
+    for (int i = b - 1; i <= last; ++i) {
+        const int64_t pr = part_row(i);
+        const float2 st = parts.stats[pr];
+        const float f = exp2f(st.x - from);
+        sum = fmaf(f, st.y, sum);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int e = 128 * j + 4 * lane;
+            if (e < D) {
+                const float4 v = *reinterpret_cast<const float4 *>(parts.sums + pr * D + e);
+                acc[4 * j] = fmaf(f, v.x, acc[4 * j]);
+                acc[4 * j + 1] = fmaf(f, v.y, acc[4 * j + 1]);
+                acc[4 * j + 2] = fmaf(f, v.z, acc[4 * j + 2]);
+                acc[4 * j + 3] = fmaf(f, v.w, acc[4 * j + 3]);
+            }
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t out_row = (int64_t)(q.q0 + flat / group) * a.nheads + me.h * group + flat % group;
+    T *out = static_cast<T *>(a.out) + out_row * D;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int e = 128 * j + 4 * lane;
+        if (e < D)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[e + i] = from_f32<T>(acc[4 * j + i] * inv);
+    }
+    if (a.lse && lane == 0) a.lse[out_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+int device_sms() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 152;
+    return sms;
+}
+
+int simt_grid(const kv_attention_args &a) {
+    return kvs::grid_of(a, kRowTile, kKeyTile, kMinUnits, kCtasPerSm * device_sms());
+}
+
+template <typename T, int NV>
+cudaError_t launch(const kv_attention_args &a, void *ws, cudaStream_t s) {
+    const int grid = simt_grid(a);
+    const kvs::Parts parts = kvs::parts_at(ws, grid, kRowTile, a.headdim);
+    const int smem = smem_bytes(a.headdim);
+    cudaError_t e = cudaFuncSetAttribute(kv_attention_simt_kernel<T, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kv_attention_simt_kernel<T, NV><<<grid, kThreads, smem, s>>>(a, parts);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : kvs::join_launch(a, parts, grid, kRowTile, s);
+}
+
+template <typename T> cudaError_t launch_dim(const kv_attention_args &a, void *ws, cudaStream_t s) {
+    if (a.headdim <= 64) return launch<T, 2>(a, ws, s);
+    if (a.headdim <= 128) return launch<T, 4>(a, ws, s);
+    return launch<T, 8>(a, ws, s);
+}
+
+}  // namespace
+
+cudaError_t kvs::join_launch(const kv_attention_args &a, const Parts &p, int grid, int row_tile, cudaStream_t s) {
+    if (grid < 2) return cudaSuccess;
+    const dim3 g((unsigned)(grid - 1), (unsigned)((row_tile + kJoinRows - 1) / kJoinRows));
+    if (a.dtype == SSD_BF16)
+        kv_join_kernel<__nv_bfloat16><<<g, kJoinThreads, 0, s>>>(a, p, row_tile);
+    else
+        kv_join_kernel<float><<<g, kJoinThreads, 0, s>>>(a, p, row_tile);
+    return cudaGetLastError();
+}
+
+size_t kv_attention_simt_workspace(const kv_attention_args &a) {
+    return kvs::parts_bytes(simt_grid(a), kRowTile, a.headdim);
+}
+
+cudaError_t kv_attention_simt_launch(const kv_attention_args &a, void *ws, cudaStream_t s) {
+    return a.dtype == SSD_BF16 ? launch_dim<__nv_bfloat16>(a, ws, s) : launch_dim<float>(a, ws, s);
+}
+
+}  // namespace ssd

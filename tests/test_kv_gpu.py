@@ -1,0 +1,524 @@
+"""The attention-side calls (kv_block_tables, kv_qk_norm_rope, kv_tree_attention, kv_commit_tokens) on
+the GPU against plain 64-bit forms, with NaN in every cache row, page and draft that must not count."""
+import numpy as np
+import pytest
+import torch
+
+import selective_state_space_mamba2_gb300 as ssd
+from tests import kv_forms as F
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    ssd.build()
+    torch.cuda.init()
+
+
+def _i(v):
+    return torch.tensor(np.asarray(v), dtype=torch.int32, device=DEV)
+
+
+def _err():
+    return torch.zeros(1, dtype=torch.int32, device=DEV)
+
+
+# ------------------------------------------------------------------ tables --
+
+def _tables(ctx, new, reserved, b, cols, max_tokens, free, head, null=0, spare_ring=3, seed=0, mangle=None):
+    rng = np.random.default_rng(seed)
+    table, total, ids = F.rand_pages(reserved, b, cols, free, rng)
+    if mangle:
+        mangle(table)
+    cap = free + spare_ring
+    ring = np.full(cap, -7, np.int32)
+    for i in range(free):
+        ring[(head + i) % cap] = ids[i]
+    ok, want = F.block_tables(ctx, new, reserved, table, ring, (head, free), b, total, max_tokens, null)
+    t, r, err = _i(table), _i(ring), _err()
+    got = ssd.kv_block_tables(_i(ctx), _i(new), _i(reserved), t, r, _i([head, free]), b, total, max_tokens,
+                              null_block_id=null, err_word=err)
+    torch.cuda.synchronize()
+    for key in ("cu_seqlens", "seq_lens", "reserved_lens", "ring_state", "slots", "positions", "token_req"):
+        assert got[key].tolist() == list(want[key]), key
+    assert np.array_equal(t.cpu().numpy(), want["table"])
+    assert np.array_equal(r.cpu().numpy(), ring)
+    return ok, want, int(err.item())
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_tables_random_batches(seed):
+    """Ragged batches: empty requests, contexts inside and at block ends, rows with blocks to spare, a context beyond
+    what is reserved, a ring that wraps, padding rows; more requests than a CTA has threads."""
+    rng = np.random.default_rng(100 + seed)
+    S = [1, 7, 256, 257, 600, 33][seed]
+    b = [16, 1, 64, 5, 16, 256][seed]
+    top = [40, 9, 130, 30, 20, 3000][seed]
+    ctx = rng.integers(0, top, S)
+    new = rng.integers(0, top, S) * (rng.random(S) < 0.8)
+    reserved = np.maximum(0, ctx + rng.integers(-b, 3 * b, S))
+    cols = int((ctx + new).max() // b + 5)
+    free = int(sum(-(-(c + n) // b) for c, n in zip(ctx, new))) + 2
+    ok, _, err = _tables(ctx.tolist(), new.tolist(), reserved.tolist(), b, cols, int(new.sum()) + 11, free,
+                         head=free + 1, seed=seed)
+    assert ok and err == 0
+
+
+def test_tables_long_prompts_beside_decodes():
+    """Requests over several token tiles beside single tokens, and a request that ends exactly with the output."""
+    new = [1, 5000, 1, 0, 1024, 9, 8, 1, 2048]
+    ctx = [17, 3, 0, 5, 64, 0, 7, 16, 100]
+    b = 16
+    free = sum(-(-(c + n) // b) for c, n in zip(ctx, new))
+    ok, _, err = _tables(ctx, new, ctx, b, 400, sum(new), free, head=0)
+    assert ok and err == 0
+
+
+@pytest.mark.parametrize("case,bit", [("blocks", 32), ("cols", 32), ("tokens", 2), ("negative", 2), ("ring", 2)])
+def test_tables_refuse_as_a_whole(case, bit):
+    """A step that cannot be served changes nothing and comes back empty."""
+    ctx, new, reserved, b, cols, top, free = [10, 20, 5], [30, 1, 2], [10, 20, 5], 8, 8, 64, 20
+    head = 2
+    if case == "blocks":
+        free = 2
+    elif case == "cols":
+        cols = 4
+    elif case == "tokens":
+        top = 32
+    elif case == "negative":
+        new = [30, -1, 2]
+    elif case == "ring":
+        head = 23  # free + spare_ring entries: none at 23
+    rng = np.random.default_rng(0)
+    table, total, ids = F.rand_pages(reserved, b, cols, 20, rng)
+    ring = np.concatenate([ids[:20], np.full(3, -7, np.int32)])
+    t, r, err, state = _i(table), _i(ring), _err(), _i([head, free])
+    got = ssd.kv_block_tables(_i(ctx), _i(new), _i(reserved), t, r, state, b, total, top, err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == bit
+    assert np.array_equal(t.cpu().numpy(), table) and np.array_equal(r.cpu().numpy(), ring)
+    assert got["cu_seqlens"].tolist() == [0] * 4 and got["slots"].tolist() == [-1] * top
+    assert got["token_req"].tolist() == [-1] * top and got["positions"].tolist() == [0] * top
+    assert got["seq_lens"].tolist() == ctx and got["reserved_lens"].tolist() == reserved
+    assert got["ring_state"].tolist() == [head, free]
+
+
+def test_tables_null_and_bad_entries():
+    """A held entry that is the null block gives slot -1; one that is no block does too, and is reported."""
+    def null(t):
+        t[0, 1] = 9999
+
+    def none(t):
+        t[0, 1] = 0
+    ok, want, err = _tables([10, 3], [4, 2], [16, 8], 8, 4, 9, 3, 0, mangle=none)
+    assert ok and err == 0 and want["slots"][:4] == [-1] * 4
+    ok, want, err = _tables([10, 3], [4, 2], [16, 8], 8, 4, 9, 3, 0, mangle=null)
+    assert ok and want["bad_slot"] and err == 1
+
+
+def test_tables_steps_chain_on_another_stream():
+    """Two steps, each reading what the one before it wrote, on a stream of the caller's."""
+    s = torch.cuda.Stream()
+    b, S = 4, 3
+    table, ring, state = _i(np.zeros((S, 6))), _i([5, 6, 7, 8, 9, 1, 2, 3]), _i([6, 8])
+    ctx, new, zero = _i([0, 0, 0]), _i([3, 5, 0]), _i([0, 0, 0])
+    s.wait_stream(torch.cuda.current_stream())
+    one = ssd.kv_block_tables(ctx, new, zero, table, ring, state, b, 10, 8, stream=s)
+    two = ssd.kv_block_tables(one["seq_lens"], _i([2, 0, 1]), one["reserved_lens"], table, ring, one["ring_state"], b,
+                              10, 8, stream=s)
+    s.synchronize()
+    # ring from entry 6: 2, 3, 5, 6, 7 ...: request 0 takes 2; request 1 takes 3 and 5; then 0 takes 6 and 2 takes 7
+    assert table[0, :2].tolist() == [2, 6] and table[1, :2].tolist() == [3, 5] and table[2, 0].item() == 7
+    assert two["slots"].tolist() == [2 * 4 + 3, 6 * 4, 7 * 4, -1, -1, -1, -1, -1]
+    assert two["ring_state"].tolist() == [3, 3]
+
+
+def test_tables_without_requests():
+    got = ssd.kv_block_tables(_i([]), _i([]), _i([]), _i(np.zeros((0, 3))), _i([1, 2]), _i([1, 1]), 8, 4, 5)
+    torch.cuda.synchronize()
+    assert got["cu_seqlens"].tolist() == [0] and got["slots"].tolist() == [-1] * 5
+    assert got["ring_state"].tolist() == [1, 1]
+
+
+# -------------------------------------------------------------------- rope --
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,rot,inter", [(128, 128, False), (64, 32, False), (80, 40, False), (8, 2, False), (8, 8, True),
+                                         (256, 64, True), (112, 112, False), (256, 256, False), (40, 6, True),
+                                         (128, 0, False)])
+@pytest.mark.parametrize("H,Hkv,T", [(5, 1, 7), (32, 8, 3), (2, 2, 1)])
+def test_norm_rope(dtype, D, rot, inter, H, Hkv, T):
+    """Head sizes, rotated parts that end inside a lane's entries, both pairings; q, k and v as views of one packed
+    projection; tokens without a slot; rows of the cache that are not written keep their bits."""
+    g = torch.Generator(device=DEV).manual_seed(D * 31 + rot + T)
+    qkv = torch.randn(T, (H + 2 * Hkv) * D + 8, generator=g, device=DEV).to(dtype)
+    q = qkv[:, :H * D].view(T, H, D) if T == 1 else qkv[:, :H * D].unflatten(1, (H, D))
+    k = qkv[:, H * D:(H + Hkv) * D].unflatten(1, (Hkv, D))
+    v = qkv[:, (H + Hkv) * D:(H + 2 * Hkv) * D].unflatten(1, (Hkv, D))
+    qw = torch.randn(D, generator=g, device=DEV)
+    kw = torch.randn(D, generator=g, device=DEV)
+    cs = torch.randn(50, rot, generator=g, device=DEV) if rot else None
+    pos = _i(np.arange(T) * 7 % 50) if rot else None
+    kv = F.poison((6, 2, 3, Hkv, D), dtype, DEV)  # keys and values of a block side by side
+    kc, vc = kv[:, 0], kv[:, 1]
+    slots = _i([(5 * t + 4) % 18 if t != 1 else -1 for t in range(T)])
+    err = _err()
+    qo, ko = ssd.kv_qk_norm_rope(q, k, pos, cs, qw, kw, 1e-5, inter, v, kc, vc, slots, err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    for got, x, w in ((qo, q, qw), (ko, k, kw)):
+        want, mag = F.norm_rope(x, w, cs, pos, 1e-5, inter)
+        assert ((got.double().cpu() - want).abs() <= F.rope_bound(want, mag, D, dtype)).all()
+    used = torch.zeros(18, dtype=torch.bool)
+    for t, s in enumerate(slots.tolist()):
+        if s >= 0:
+            used[s] = True
+            assert torch.equal(kc[s // 3, s % 3], ko[t]) and torch.equal(vc[s // 3, s % 3], v[t])
+    rest = kv.transpose(1, 2).reshape(18, 2, Hkv, D)[~used.to(DEV)]
+    assert torch.isnan(rest).all()
+
+
+@pytest.mark.parametrize("rot", [64, 40])
+def test_norm_rope_in_place_and_without_norm(rot):
+    T, H, Hkv, D = 9, 3, 3, 64
+    g = torch.Generator(device=DEV).manual_seed(5)
+    q = torch.randn(T, H, D, generator=g, device=DEV)
+    k = torch.randn(T, Hkv, D, generator=g, device=DEV)
+    cs = torch.randn(20, rot, generator=g, device=DEV)
+    pos = _i(np.arange(T) + 3)
+    wq, mq = F.norm_rope(q, None, cs, pos, 0, False)
+    wk, mk = F.norm_rope(k, None, cs, pos, 0, False)
+    a, b = ssd.kv_qk_norm_rope(q, k, pos, cs, q_out=q, k_out=k)
+    torch.cuda.synchronize()
+    assert a is q and ((a.double().cpu() - wq).abs() <= F.rope_bound(wq, mq, D, F32)).all()
+    assert b is k and ((b.double().cpu() - wk).abs() <= F.rope_bound(wk, mk, D, F32)).all()
+
+
+def test_norm_rope_reports_bad_positions_and_slots():
+    T, H, D = 4, 2, 64
+    q = torch.randn(T, H, D, device=DEV)
+    cs = torch.randn(10, D, device=DEV)
+    kc, vc = F.poison((2, 4, H, D), F32, DEV), F.poison((2, 4, H, D), F32, DEV)
+    qo, ko, err = F.poison((T, H, D), F32, DEV), F.poison((T, H, D), F32, DEV), _err()
+    ssd.kv_qk_norm_rope(q, q, _i([0, 10, -1, 9]), cs, v=q, k_cache=kc, v_cache=vc, slots=_i([0, 1, 2, 8]), q_out=qo,
+                        k_out=ko, err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 3
+    assert torch.isnan(qo[1:3]).all() and torch.isfinite(qo[0]).all() and torch.isfinite(qo[3]).all()
+    assert torch.isfinite(kc[0, 0]).all() and torch.isnan(kc.flatten(0, 1)[1:]).all() and torch.isnan(vc.flatten(0, 1)[1:]).all()
+
+
+def test_norm_rope_zero_row_and_large_values():
+    """An all-zero head stays zero (eps keeps the root finite); values near fp32's square root of the largest number."""
+    q = torch.zeros(2, 1, 64, device=DEV)
+    q[1] = 1e18
+    qo, _ = ssd.kv_qk_norm_rope(q, q.clone(), q_weight=torch.ones(64, device=DEV))
+    torch.cuda.synchronize()
+    assert (qo[0] == 0).all() and torch.allclose(qo[1], torch.ones(1, 64, device=DEV), rtol=1e-5)
+
+
+# --------------------------------------------------------------- attention --
+
+def _tree(rng, n, words):
+    rows, bits = [], []
+    for i in range(n):
+        up = bits[rng.integers(max(0, i - 5), i)] if i else 0
+        bits.append(up | 1 << i)
+    for m in bits:
+        rows.append([(m >> 32 * w) & 0xFFFFFFFF for w in range(words)])
+    return np.array(rows, np.uint32).reshape(n, words)
+
+
+def _attn(dtype, H, Hkv, D, b, new, ctx, tree, seed=0, empty_rows=(), poison_new=(), scale=None, qk_gain=1.0,
+          max_new=None, pack=True, extra_words=0):
+    """Inputs with NaN in every page row that holds no cached token, and in front of and behind the packed tokens."""
+    rng = np.random.default_rng(seed)
+    g = torch.Generator(device=DEV).manual_seed(seed + 77)
+    S, T = len(new), sum(new)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    cols = max(-(-max(ctx) // b), 1) + 1
+    table, total, _ = F.rand_pages(ctx, b, cols, 2, rng)
+    table[table == 0] = 10 ** 6  # entries behind the context are never read
+    kc, vc = F.poison((total, b, Hkv, D), dtype, DEV), F.poison((total, b, Hkv, D), dtype, DEV)
+    for r in range(S):
+        for j in range(-(-ctx[r] // b)):
+            n = min(b, ctx[r] - j * b)
+            kc[int(table[r, j]), :n] = torch.randn(n, Hkv, D, generator=g, device=DEV).to(dtype)
+            vc[int(table[r, j]), :n] = torch.randn(n, Hkv, D, generator=g, device=DEV).to(dtype)
+    pad = 3
+    qkv = F.poison((T + 2 * pad, (H + 2 * Hkv) * D), dtype, DEV)
+    qkv[pad:pad + T] = torch.randn(T, (H + 2 * Hkv) * D, generator=g, device=DEV).to(dtype)
+    qkv[:, :H * D] *= qk_gain
+    part = qkv[pad:pad + T]
+    q = part[:, :H * D].unflatten(1, (H, D))
+    k = part[:, H * D:(H + Hkv) * D].unflatten(1, (Hkv, D))
+    v = part[:, (H + Hkv) * D:].unflatten(1, (Hkv, D))
+    if not pack:
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+    mask = None
+    if tree:
+        words = -(-max(max(new), 1) // 32) + extra_words
+        mask = np.concatenate([_tree(rng, n, words) for n in new])
+        for r, i in empty_rows:
+            mask[cu[r] + i] = 0
+        for r, i in poison_new:  # nobody but itself may see it
+            t = cu[r] + i
+            k[t], v[t] = float("nan"), float("nan")
+            for j in range(new[r]):
+                if j != i:
+                    mask[cu[r] + j, i // 32] &= ~np.uint32(1 << i % 32)
+    sc = D ** -0.5 if scale is None else scale
+    return dict(q=q, k=k, v=v, kc=kc, vc=vc, cu=cu, ctx=ctx, table=table, mask=mask, scale=sc, new=new,
+                max_new=max(new) if max_new is None else max_new)
+
+
+def _run(c, err, **kw):
+    mask = None if c["mask"] is None else torch.from_numpy(c["mask"].view(np.int32)).to(DEV)
+    return ssd.kv_tree_attention(c["q"], c["k"], c["v"], c["kc"], c["vc"], _i(c["cu"]), _i(c["ctx"]), _i(c["table"]),
+                                 c["max_new"], tree_mask=mask, scale=c["scale"], return_lse=True, err_word=err, **kw)
+
+
+def _near(c, out, rows):
+    """The output rows (a slice) are inside the bound."""
+    want, wlse, mag, big, keys = F.attention(c["q"], c["k"], c["v"], c["kc"], c["vc"], c["cu"], c["ctx"], c["table"],
+                                             c["mask"], c["scale"])
+    tol, _ = F.attention_bound(want, wlse, mag, big, keys, c["q"].shape[2], c["q"].dtype)
+    return bool(((out.double().cpu() - want).abs() <= tol)[rows].all())
+
+
+def _check(c, nan_rows=()):
+    err = _err()
+    out, lse = _run(c, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    dtype, D = c["q"].dtype, c["q"].shape[2]
+    want, wlse, mag, big, keys = F.attention(c["q"], c["k"], c["v"], c["kc"], c["vc"], c["cu"], c["ctx"], c["table"],
+                                             c["mask"], c["scale"])
+    tol, ltol = F.attention_bound(want, wlse, mag, big, keys, D, dtype)
+    out, lse = out.double().cpu(), lse.double().cpu()
+    live = torch.ones(out.shape[0], dtype=torch.bool)
+    for t in nan_rows:
+        live[t] = False
+        assert torch.isnan(out[t]).all()
+    bad = ((out - want).abs() > tol)[live]
+    assert not torch.isnan(out[live]).any() and not bad.any(), float(((out - want).abs() / tol)[live].max())
+    none = keys == 0
+    assert (out[none] == 0).all() and torch.isneginf(lse[none]).all()
+    some = live & ~none
+    assert ((lse - wlse).abs() <= ltol)[some].all(), float(((lse - wlse).abs() / ltol)[some].max())
+    return out
+
+
+LAYOUTS = [  # dtype, query heads, key heads, head size, block size
+    (BF, 8, 2, 128, 16), (BF, 4, 4, 64, 8), (BF, 8, 1, 128, 48), (BF, 10, 2, 64, 256), (BF, 5, 1, 128, 32),
+    (BF, 16, 1, 128, 64), (BF, 40, 1, 128, 128), (BF, 128, 1, 64, 16),
+    (F32, 8, 2, 128, 16), (F32, 4, 4, 64, 5), (F32, 3, 1, 256, 1), (F32, 20, 1, 40, 24),
+    (BF, 8, 2, 128, 20), (BF, 2, 1, 256, 16), (BF, 6, 2, 96, 16), (BF, 130, 1, 64, 16),
+]
+
+
+@pytest.mark.parametrize("dtype,H,Hkv,D,b", LAYOUTS)
+@pytest.mark.parametrize("tree", [False, True])
+def test_attention_layouts(dtype, H, Hkv, D, b, tree):
+    """Every kernel, head size, group and page size on a ragged batch: no context, contexts of one token, at and around
+    page and tile ends, requests without new tokens, single tokens and several; stale page rows are NaN."""
+    new = [1, 3, 0, 7, 2, 5, 1, 4]
+    ctx = [0, 1, 40, 63, 64, 65, 300, b]
+    _check(_attn(dtype, H, Hkv, D, b, new, ctx, tree, seed=D + H))
+
+
+@pytest.mark.parametrize("dtype,D,group", [(BF, 128, 4), (BF, 64, 1), (BF, 128, 5), (BF, 128, 16), (F32, 64, 2)])
+@pytest.mark.parametrize("n", [1, 15, 31, 33, 64, 65, 129])
+def test_attention_tree_sizes(dtype, D, group, n):
+    """Trees up to several mask words and key tiles; rows that see nothing at all and rows that see no draft."""
+    c = _attn(dtype, group, 1, D, 16, [n, max(1, n // 2)], [0, 100], True, seed=n, extra_words=n % 2,
+              empty_rows=[(0, n - 1), (1, 0)])
+    _check(c)
+
+
+@pytest.mark.parametrize("dtype,D", [(BF, 128), (BF, 64), (F32, 64)])
+@pytest.mark.parametrize("new,ctx", [([200], [0]), ([1], [0]), ([130, 1, 67], [70, 2000, 0]), ([257], [129])])
+def test_attention_prompts(dtype, D, new, ctx):
+    """Chains over several query tiles, behind a prefix or none."""
+    _check(_attn(dtype, 4, 2, D, 16, new, ctx, False, seed=3))
+
+
+@pytest.mark.parametrize("dtype,H,Hkv,D", [(BF, 8, 2, 128), (BF, 32, 1, 64), (F32, 4, 1, 128)])
+def test_attention_long_caches_are_split(dtype, H, Hkv, D):
+    """One long request beside short ones: its keys are cut over many CTAs and joined."""
+    _check(_attn(dtype, H, Hkv, D, 16, [1, 2, 1], [20011, 5, 700], False, seed=9))
+
+
+@pytest.mark.parametrize("dtype,D", [(BF, 128), (BF, 64), (F32, 64)])
+def test_attention_nan_drafts_stay_out(dtype, D):
+    """A draft whose key and value are NaN touches nobody but itself."""
+    c = _attn(dtype, 4, 1, D, 16, [9, 40], [33, 0], True, seed=4, poison_new=[(0, 4), (1, 0), (1, 35)])
+    _check(c, nan_rows=[int(c["cu"][0]) + 4, int(c["cu"][1]), int(c["cu"][1]) + 35])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_infinite_values(dtype):
+    """An infinite value that is seen gives infinity (or NaN against its opposite) in its column, and only there."""
+    c = _attn(dtype, 4, 1, 64, 16, [6], [20], True, seed=8)
+    c["v"][2, 0, 5] = float("inf")
+    c["v"][3, 0, 9] = float("-inf")
+    out, _ = _run(c, _err())
+    torch.cuda.synchronize()
+    bits = c["mask"][:, 0]
+    for i in range(6):
+        row = out[i]
+        for col, j, inf in ((5, 2, float("inf")), (9, 3, float("-inf"))):
+            if bits[i] >> j & 1:
+                assert (row[:, col] == inf).all()
+            else:
+                assert torch.isfinite(row[:, col]).all()
+        keep = [e for e in range(64) if e not in (5, 9)]
+        assert torch.isfinite(row[:, keep]).all()
+
+
+@pytest.mark.parametrize("dtype,gain", [(BF, 60.0), (F32, 60.0), (BF, 0.0), (F32, 1e-3)])
+def test_attention_score_ranges(dtype, gain):
+    """Peaked scores (hundreds apart, so running maxima jump), and equal ones."""
+    _check(_attn(dtype, 8, 2, 128, 16, [4, 1, 33], [500, 1000, 77], False, seed=6, qk_gain=gain))
+
+
+def test_attention_does_not_depend_on_the_hint():
+    """max_new_tokens sizes the tiles; every value of it gives a result inside the bound."""
+    for hint in (0, 1, 10, 33, 1000):
+        _check(_attn(BF, 4, 1, 128, 16, [40, 3, 1], [50, 200, 0], True, seed=12, max_new=hint))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_is_repeatable_and_stream_ordered(dtype):
+    """The same bits every time, on another stream, and with a workspace full of NaN."""
+    c = _attn(dtype, 8, 2, 128, 16, [2, 1, 30], [3000, 40, 900], False, seed=21)
+    a, la = _run(c, _err())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    ws = torch.full((1 << 28,), 255, dtype=torch.uint8, device=DEV)
+    s.wait_stream(torch.cuda.current_stream())
+    b, lb = _run(c, _err(), stream=s, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_reports_bad_metadata(dtype):
+    """A context beyond the table, more drafts than mask bits, decreasing offsets: the request's rows stay unwritten and
+    the others come out right.  A block id that is none reads as zeros."""
+    def case(new=(2, 3)):
+        return _attn(dtype, 4, 2, 64, 16, list(new), [30, 50], True, seed=2)
+
+    c, good = case(), case()
+    c["ctx"] = [30, 16 * c["table"].shape[1] + 1]
+    out, err = F.poison(c["q"].shape, dtype, DEV), _err()
+    _run(c, err, out=out)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 2 and _near(good, out, slice(0, 2)) and torch.isnan(out[2:]).all()
+
+    c, good = case((2, 40)), case((2, 40))
+    c["mask"] = c["mask"][:, :1].copy()
+    out, err = F.poison(c["q"].shape, dtype, DEV), _err()
+    _run(c, err, out=out)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 2 and _near(good, out, slice(0, 2)) and torch.isnan(out[2:]).all()
+
+    c = case()
+    c["cu"] = np.array([0, 9, 5], np.int32)
+    out, err = F.poison(c["q"].shape, dtype, DEV), _err()
+    _run(c, err, out=out)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 2 and torch.isnan(out).all()
+
+    c = case()
+    c["table"][1, 1] = -5
+    err = _err()
+    out, _ = _run(c, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 1
+    c["kc"] = torch.cat([c["kc"], torch.zeros_like(c["kc"][:1])])
+    c["vc"] = torch.cat([c["vc"], torch.zeros_like(c["vc"][:1])])
+    c["table"][1, 1] = c["kc"].shape[0] - 1
+    assert _near(c, out, slice(0, 5))
+
+
+def test_attention_cache_views_and_far_blocks():
+    """Keys and values interleaved block by block, with a block stride that puts the last blocks beyond 2^31
+    elements."""
+    c = _attn(BF, 4, 1, 128, 16, [3, 1], [100, 40], False, seed=5)
+    nb, b, H, D = c["kc"].shape
+    stride = (1 << 32) // nb // 8 * 8
+    big = torch.empty(stride * (nb - 1) + 2 * b * H * D, dtype=BF, device=DEV)
+    kc = big.as_strided((nb, b, H, D), (stride, H * D, D, 1), 0)
+    vc = big.as_strided((nb, b, H, D), (stride, H * D, D, 1), b * H * D)
+    kc.copy_(c["kc"])
+    vc.copy_(c["vc"])
+    c["kc"], c["vc"] = kc, vc
+    _check(c)
+
+
+def test_attention_without_tokens():
+    c = _attn(BF, 4, 1, 128, 16, [0, 0], [100, 40], False, seed=5)
+    out, lse = _run(c, _err())
+    torch.cuda.synchronize()
+    assert out.shape == (0, 4, 128) and lse.shape == (0, 4)
+    # tokens behind the last request: nothing is theirs, nothing is written
+    c = _attn(BF, 4, 1, 128, 16, [5], [100], False, seed=5)
+    c["cu"] = np.array([0, 0], np.int32)
+    out = F.poison((5, 4, 128), BF, DEV)
+    _run(c, _err(), out=out)
+    torch.cuda.synchronize()
+    assert torch.isnan(out).all()
+
+
+# ------------------------------------------------------------------ commit --
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("Hkv,D", [(8, 128), (1, 8), (3, 40)])
+def test_commit_paths(dtype, Hkv, D):
+    g = torch.Generator(device=DEV).manual_seed(1)
+    new = [5, 0, 16, 1, 9]
+    cu = np.concatenate([[0], np.cumsum(new)])
+    T = int(cu[-1])
+    kv = torch.randn(T, 2 * Hkv * D, generator=g, device=DEV).to(dtype)
+    k, v = kv[:, :Hkv * D].unflatten(1, (Hkv, D)), kv[:, Hkv * D:].unflatten(1, (Hkv, D))
+    path = np.array([[0, 2, 4], [9, 9, 9], [1, 7, 15], [0, 5, 5], [8, 8, 8]])
+    lens, ctx = [3, 0, 2, 1, 0], [10, 20, 30, 40, 50]
+    slots = np.random.default_rng(0).permutation(60)[:T]
+    slots[cu[2] + 1] = -1  # a token without a slot
+    kc, vc, err = F.poison((12, 5, Hkv, D), dtype, DEV), F.poison((12, 5, Hkv, D), dtype, DEV), _err()
+    out = ssd.kv_commit_tokens(k, v, kc, vc, _i(slots), _i(cu), _i(ctx), _i(path), _i(lens), err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and out.tolist() == [13, 20, 32, 41, 50]
+    wk, wv = F.poison((60, Hkv, D), dtype, DEV), F.poison((60, Hkv, D), dtype, DEV)
+    for r in range(5):
+        for i in range(lens[r]):
+            s = slots[cu[r] + i]
+            if s >= 0:
+                wk[s], wv[s] = k[cu[r] + path[r, i]], v[cu[r] + path[r, i]]
+    bits = torch.int16 if dtype == BF else torch.int32
+    assert torch.equal(kc.view(60, Hkv, D).view(bits), wk.view(bits))
+    assert torch.equal(vc.view(60, Hkv, D).view(bits), wv.view(bits))
+
+
+def test_commit_all_tokens_and_errors():
+    T, Hkv, D = 11, 2, 64
+    k = torch.randn(T, Hkv, D, device=DEV)
+    kc, vc = F.poison((4, 4, Hkv, D), F32, DEV), F.poison((4, 4, Hkv, D), F32, DEV)
+    slots = _i([15, 3, 2, 1, 0, 4, 5, 6, 7, 8, 9, -1, -1])  # a padded slot map
+    assert ssd.kv_commit_tokens(k, -k, kc, vc, slots) is None
+    torch.cuda.synchronize()
+    assert torch.equal(kc.flatten(0, 1)[15], k[0]) and torch.equal(vc.flatten(0, 1)[9], -k[10])
+    assert torch.isnan(kc.flatten(0, 1)[10:15]).all()
+    kc, vc, err = F.poison((4, 4, Hkv, D), F32, DEV), F.poison((4, 4, Hkv, D), F32, DEV), _err()
+    out = ssd.kv_commit_tokens(k, k, kc, vc, _i([0, 1, 2, 3, 4, 5, 99, 7, 8, 9, 10]), _i([0, 3, 6, 9, 11]), _i([1, 1, 1, 1]),
+                               _i([[0, 1], [0, 3], [0, 1], [1, 0]]), _i([3, 2, 2, 1]), err_word=err)
+    torch.cuda.synchronize()
+    # request 0: more steps than columns; 1: a step that is none of its tokens; 2: a slot that is none
+    assert int(err.item()) == 3 and out.tolist() == [1, 3, 3, 2]
+    flat = kc.flatten(0, 1)
+    assert torch.isnan(flat[:3]).all() and torch.equal(flat[3], k[3]) and torch.isnan(flat[4]).all()
+    assert torch.equal(flat[7], k[7]) and torch.equal(flat[9], k[10])
