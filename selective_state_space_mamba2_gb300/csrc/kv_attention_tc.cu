@@ -1,6 +1,561 @@
+// kv_tree_attention on the tensor cores: bf16, headdim 64 or 128.
+//
+// One item (kv_sched.cuh) is up to 128 query rows (tokens x the query heads of one key head)
+// against its keys in tiles of 64.  Per tile
+//   S = Q K^T          tcgen05, 128 x 64, K = headdim, both K-major from TMA tiles
+//   P = exp2(c S - m)  one row per thread (TMEM lane), written over S in TMEM as bf16
+//   O += P V           tcgen05, 128 x headdim, K = 64, P from TMEM, V MN-major
+// with the running maximum m and the sum of the weights in registers (fp32).  O stays in TMEM; it
+// is only rescaled when a row's maximum grows by more than 2^8 (the weights are then at most
+// 2^8, exact powers of two apart from what they would be, and the sum is kept to the same m).
+// P's rounding to bf16 is that of the product's operand type: V is bf16, and both operands of a
+// product have one type; the sum of the weights takes them before the rounding.
+//
+// Roles (192 threads, two CTAs per SM so that one's softmax runs beside the other's products):
+// warps 0-3 softmax and output, warp 4 TMA loads, warp 5 the products.  Keys and values pass
+// through one ring of 64-row tiles in the order they are used: K0 K1 V0 K2 V1 ...
+//
+// Masked places: a score that must not count is replaced, not added to, so a NaN key is harmless.
+// A value enters the product whatever its weight, so in tiles with rows that are not there or
+// that some query does not see, the rows that are not there are zeroed in shared memory, and
+// values that are not finite are taken out there and added again, to the rows that see them, at
+// the end (which then only decides between infinity and NaN).
+//
+// Waits are bounded: one that gives up marks the CTA, after which no wait of it waits, nothing
+// more is issued, and every loop runs to its (finite) end.
 #include "kv_sched.cuh"
+#include "tc_ptx.cuh"
+#include "tmap.h"
+
 namespace ssd {
-bool kv_attention_tc_supported(const kv_attention_args &a) { return false; }
-size_t kv_attention_tc_workspace(const kv_attention_args &a) { return 0; }
-cudaError_t kv_attention_tc_launch(const kv_attention_args &a, void *, cudaStream_t) { return cudaErrorNotSupported; }
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 128;    // TMEM lanes: query rows of a tile
+constexpr int kKeys = 64;     // keys of a tile
+constexpr int kThreads = 192;
+constexpr int kLoadWarp = 4, kMmaWarp = 5;
+constexpr int kStages = 5;
+constexpr int kMinUnits = 2;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;  // growth of a maximum (base 2) that is let stand
+
+struct TcParams {
+    kv_attention_args a;
+    kvs::Parts parts;
+    int32_t tile_tokens;  // tokens of a row tile
+    int32_t box_rows;     // rows of a page that one copy brings: divides block_size and kKeys
+    long long wait_limit;
+};
+
+enum { Q_FULL, Q_EMPTY, S_FULL0, S_FULL1, P_READY0, P_READY1, O_DONE, FIN, KV_FULL0, KV_EMPTY0 = KV_FULL0 + kStages,
+       NUM_BARS = KV_EMPTY0 + kStages };
+
+template <int D> struct Layout {
+    static constexpr int kQ = kRows * D * 2;
+    static constexpr int kTile = kKeys * D * 2;
+    static constexpr int kRing = kQ;
+    static constexpr int kBars = kRing + kStages * kTile;
+    static constexpr int kMisc = kBars + NUM_BARS * 8;  // TMEM base, dead mark, item with non-finite values
+    static constexpr int kFind = (kMisc + 16 + 15) / 16 * 16;
+    static constexpr int kBytes = kFind + (int)sizeof(kvs::FindSmem);
+};
+
+struct Waiter {
+    volatile int *dead;
+    uint32_t *err;
+    long long limit;
+    __device__ __forceinline__ void operator()(uint64_t *bar, uint32_t parity) const {
+        if (mbar_try_wait(bar, parity)) return;
+        const long long t0 = clock64();
+        while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+            if (*dead) return;
+            if (clock64() - t0 > limit) {
+                *dead = 1;
+                report(err, SSD_DEVERR_TIMEOUT);
+                return;
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
 }
+
+// bits [0, n) set, n clamped to 0 .. 64
+__device__ __forceinline__ unsigned long long low_bits(int64_t n) {
+    return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+
+// which keys of tile t the row of new token `tok` sees (tok < 0: no row)
+__device__ __forceinline__ unsigned long long seen_bits(const kv_attention_args &a, const kvs::Walk &w, int t, int tok) {
+    if (tok < 0) return 0;
+    if (t < w.cached_tiles) return low_bits((int64_t)w.q.c - (int64_t)t * kKeys);
+    const int base = (t - w.cached_tiles) * kKeys;
+    if (!a.tree_mask) return low_bits((int64_t)tok + 1 - base);
+    const uint32_t *m = a.tree_mask + (int64_t)(w.q.q0 + tok) * a.mask_words;
+    const int word = base / 32;  // base < new tokens <= 32 mask_words
+    unsigned long long bits = m[word];
+    if (word + 1 < a.mask_words) bits |= (unsigned long long)m[word + 1] << 32;
+    return bits & low_bits((int64_t)w.q.n - base);
+}
+
+__device__ __forceinline__ uint32_t nonfinite_bf16x2(uint32_t v) {  // mask of the halves whose exponent is all ones
+    const uint32_t lo = (v & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u, hi = (v & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
+    return lo | hi;
+}
+
+// Takes out of value tile `tile` what must not be multiplied (see the top): rows from `limit` on,
+// and, where `fresh`, non-finite values.  True if there were any.  Called by 128 threads.
+template <int D> __device__ __forceinline__ bool clean_values(uint8_t *tile, int limit, bool fresh, int tid) {
+    constexpr int kPieces = D / 16;  // 16-byte pieces of a thread: two threads per row
+    const int row = tid & 63, part = tid >> 6;
+    bool found = false;
+    if (row >= limit || fresh) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int piece = part * kPieces + i;  // of the row's D / 8
+            uint8_t *p = tile + (piece >> 3) * (kKeys * 128) + sw128_offset(row, piece & 7);
+            if (row >= limit) {
+                *reinterpret_cast<uint4 *>(p) = make_uint4(0, 0, 0, 0);
+            } else {
+                uint4 v = *reinterpret_cast<uint4 *>(p);
+                const uint32_t x = nonfinite_bf16x2(v.x), y = nonfinite_bf16x2(v.y), z = nonfinite_bf16x2(v.z),
+                               w = nonfinite_bf16x2(v.w);
+                if (x | y | z | w) {
+                    found = true;
+                    v.x &= ~x, v.y &= ~y, v.z &= ~z, v.w &= ~w;
+                    *reinterpret_cast<uint4 *>(p) = v;
+                }
+            }
+        }
+    }
+    return found;
+}
+
+// The non-finite values that clean_values took out, added to the 32 output columns from `col` of a
+// row that sees their keys.
+__device__ __noinline__ void add_nonfinite(const kv_attention_args &a, const kvs::Walk &w, int tok, int col,
+                                           uint32_t (&o)[32]) {
+    for (int t = max(w.t0, w.cached_tiles); t < w.t1; ++t) {
+        const unsigned long long seen = seen_bits(a, w, t, tok);
+        const int base = (t - w.cached_tiles) * kKeys;
+        for (int j = 0; j < kKeys; ++j) {
+            if (!(seen >> j & 1)) continue;
+            const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v_new) +
+                                     (int64_t)(w.q.q0 + base + j) * a.v_stride + w.h * a.headdim + col;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const float f = to_f32(v[e]);
+                if (!isfinite(f)) o[e] = __float_as_uint(__uint_as_float(o[e]) + f);
+            }
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+    kv_attention_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKc,
+                           const __grid_constant__ CUtensorMap tmVc, const __grid_constant__ CUtensorMap tmKn,
+                           const __grid_constant__ CUtensorMap tmVn, const __grid_constant__ TcParams p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    using L = Layout<D>;
+    constexpr int kHalves = D / 64;
+    constexpr uint32_t kTmemCols = 256;
+    constexpr uint32_t COL_S = 0, COL_O = 128;  // two score tiles of 64 columns, the output
+    const kv_attention_args &a = p.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int group = a.nheads / a.kv_heads, row_tile = p.tile_tokens * group;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + L::kBars);
+    uint32_t *sTmem = reinterpret_cast<uint32_t *>(smem + L::kMisc);
+    volatile int *dead = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
+    volatile int *dirty = reinterpret_cast<volatile int *>(smem + L::kMisc + 8);
+
+    kvs::Walk w;
+    if (!kvs::find_run(a, group, row_tile, kKeys, kMinUnits, *reinterpret_cast<kvs::FindSmem *>(smem + L::kFind),
+                       p.parts.borders, w))
+        return;
+    if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled tiles need a 1024-byte aligned base
+        if (tid == 0) report(a.err_word, SSD_DEVERR_INTERNAL);
+        return;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < NUM_BARS; ++i) mbar_init(&bar[i], i == Q_EMPTY || i == P_READY0 || i == P_READY1 ? 4 : 1);
+        fence_mbar_init();
+        *dead = 0;
+        *dirty = 0;
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(sTmem, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = *sTmem;
+    const Waiter wait{dead, a.err_word, p.wait_limit};
+
+    if (warp == kLoadWarp) {
+        // ---- loads -----------------------------------------------------------------
+        uint32_t slot = 0;  // ring position
+        uint32_t items = 0;
+        const int boxes = kKeys / p.box_rows;
+        const int my_box = lane / kHalves, my_half = lane % kHalves;
+        // this lane's page of cached tile t: block id, or -1 where it has none to load
+        auto page = [&](int t) -> int32_t {
+            if (my_box >= boxes) return -1;
+            const int32_t pos = t * kKeys + my_box * p.box_rows;
+            if (t >= w.cached_tiles || pos >= w.q.c) return -1;
+            const int32_t id = a.block_table[(int64_t)w.r * a.table_cols + pos / a.block_size];
+            if (id < 0 || id >= a.num_blocks) {
+                report(a.err_word, SSD_DEVERR_SLOT);
+                return a.num_blocks;  // outside the tensor: reads as zeros
+            }
+            return id;
+        };
+        auto load = [&](bool value, int t, int32_t id) {
+            const uint32_t st = slot % kStages;
+            wait(&bar[KV_EMPTY0 + st], ((slot / kStages) & 1) ^ 1);
+            ++slot;
+            if (__any_sync(~0u, *dead)) return;
+            uint8_t *dst = smem + L::kRing + st * L::kTile;
+            uint64_t *full = &bar[KV_FULL0 + st];
+            if (t < w.cached_tiles) {
+                const uint32_t n = __popc(__ballot_sync(~0u, id >= 0));
+                if (lane == 0) mbar_arrive_expect_tx(full, n * p.box_rows * 128);
+                __syncwarp();
+                if (id >= 0) {
+                    const int32_t pos = t * kKeys + my_box * p.box_rows;
+                    tma_load_4d(dst + my_half * (kKeys * 128) + my_box * p.box_rows * 128, value ? &tmVc : &tmKc,
+                                my_half * 64, w.h, pos % a.block_size, id, full);
+                }
+            } else {
+                if (lane == 0) mbar_arrive_expect_tx(full, L::kTile);
+                __syncwarp();
+                if (lane < kHalves)
+                    tma_load_3d(dst + lane * (kKeys * 128), value ? &tmVn : &tmKn, lane * 64, w.h,
+                                w.q.q0 + (t - w.cached_tiles) * kKeys, full);
+            }
+        };
+        bool more = true;
+        while (more) {
+            int32_t id = page(w.t0), id_before = -1;
+            wait(&bar[Q_EMPTY], (items & 1) ^ 1);
+            ++items;
+            if (!__any_sync(~0u, *dead)) {
+                if (lane == 0) mbar_arrive_expect_tx(&bar[Q_FULL], kHalves * row_tile * 128);
+                __syncwarp();
+                if (lane < kHalves)
+                    tma_load_3d(smem + lane * (kRows * 128), &tmQ, lane * 64, w.h * group, w.q.q0 + w.m * p.tile_tokens,
+                                &bar[Q_FULL]);
+            }
+            for (int t = w.t0; t < w.t1; ++t) {
+                const int32_t id_next = page(t + 1);  // looked up a tile ahead
+                load(false, t, id);
+                if (t > w.t0) load(true, t - 1, id_before);
+                id_before = id;
+                id = id_next;
+            }
+            load(true, w.t1 - 1, id_before);
+            more = w.next(a, group, row_tile, kKeys);
+        }
+        if (__any_sync(~0u, *dead)) {  // copies in flight land before the CTA may go
+            for (int st = 0; st < kStages; ++st)
+                if (slot > (uint32_t)st) {
+                    const uint32_t last = slot - 1 - (slot - 1 - st) % kStages;
+                    mbar_wait(&bar[KV_FULL0 + st], (last / kStages) & 1, 20000000ll);
+                }
+            mbar_wait(&bar[Q_FULL], (items - 1) & 1, 20000000ll);
+        }
+    } else if (warp == kMmaWarp) {
+        // ---- products --------------------------------------------------------------
+        if (lane == 0) {
+            constexpr uint32_t kIdS = idesc_bf16(kRows, kKeys, 0, 0);
+            constexpr uint32_t kIdO = idesc_bf16(kRows, D, 0, 1);
+            const uint64_t dQ = sw128_desc(smem_u32(smem), 16, 1024);
+            const uint64_t dK = sw128_desc(smem_u32(smem + L::kRing), 16, 1024);
+            const uint64_t dV = sw128_desc(smem_u32(smem + L::kRing), kKeys * 128, 1024);
+            uint32_t slot = 0, tile = 0, items = 0;
+            auto scores = [&]() {  // of tile number `tile`
+                const uint32_t st = slot % kStages;
+                wait(&bar[KV_FULL0 + st], (slot / kStages) & 1);
+                ++slot;
+                if (*dead) return;
+                tc_fence_after();
+                const uint64_t k0 = desc_at(dK, st * L::kTile);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_ss(tm + COL_S + 64 * (tile & 1), desc_at(dQ, (k >> 2) * (kRows * 128) + (k & 3) * 32),
+                           desc_at(k0, (k >> 2) * (kKeys * 128) + (k & 3) * 32), kIdS, k > 0);
+                mma_commit(&bar[KV_EMPTY0 + st]);
+                mma_commit(&bar[S_FULL0 + (tile & 1)]);
+            };
+            auto output = [&](uint32_t g, bool first) {  // of tile number g
+                wait(&bar[P_READY0 + (g & 1)], (g >> 1) & 1);
+                const uint32_t st = slot % kStages;
+                wait(&bar[KV_FULL0 + st], (slot / kStages) & 1);
+                ++slot;
+                if (*dead) return;
+                tc_fence_after();
+                const uint64_t v0 = desc_at(dV, st * L::kTile);
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                    mma_ts(tm + COL_O, tm + COL_S + 64 * (g & 1) + 8 * k, desc_at(v0, 2048 * k), kIdO, !first || k > 0);
+                mma_commit(&bar[KV_EMPTY0 + st]);
+                mma_commit(&bar[O_DONE]);
+            };
+            bool more = true;
+            while (more) {
+                wait(&bar[Q_FULL], items & 1);
+                ++items;
+                for (int t = w.t0; t < w.t1; ++t) {
+                    scores();
+                    if (t > w.t0) output(tile - 1, t - 1 == w.t0);
+                    ++tile;
+                }
+                output(tile - 1, w.t1 - 1 == w.t0);
+                more = w.next(a, group, row_tile, kKeys);
+            }
+            mma_commit(&bar[FIN]);  // everything issued is done before the CTA goes
+            mbar_wait(&bar[FIN], 0, 20000000ll);
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax and output ------------------------------------------------------
+        const float c = a.scale * kLog2e;
+        const uint32_t lane_base = tm + ((uint32_t)(warp * 32) << 16);
+        uint32_t tile = 0, ring = 0;  // tile number, ring positions used by earlier items
+        int item = 0;
+        bool more = true;
+        while (more) {
+            ++item;
+            const int rows = (int)min((int64_t)row_tile, (int64_t)w.q.n * group - (int64_t)w.m * row_tile);
+            const bool warp_live = warp * 32 < rows;
+            const int tok = tid < rows ? w.m * p.tile_tokens + tid / group : -1;
+            const int n_tiles = w.t1 - w.t0;
+            float top = -INFINITY, sum = 0.f;
+            for (int t = w.t0; t < w.t1; ++t, ++tile) {
+                const uint32_t s_col = lane_base + COL_S + 64 * (tile & 1);
+                const bool cached = t < w.cached_tiles;
+                const int limit = cached ? min(kKeys, w.q.c - t * kKeys)
+                                         : min(kKeys, w.q.n - (t - w.cached_tiles) * kKeys);
+                const bool partial = !cached || limit < kKeys;
+                wait(&bar[S_FULL0 + (tile & 1)], (tile >> 1) & 1);
+                __syncwarp();
+                tc_fence_after();
+                if (warp_live) {
+                    uint32_t s[64];
+                    tmem_ld64(s_col, s);
+                    tmem_ld_wait();
+                    if (partial) {
+                        const unsigned long long seen = seen_bits(a, w, t, tok);
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if (!(seen >> j & 1)) s[j] = 0xFF800000u;  // -inf
+                    }
+                    float best = __uint_as_float(s[0]);
+#pragma unroll
+                    for (int j = 1; j < 64; ++j) best = fmaxf(best, __uint_as_float(s[j]));
+                    const float now = best == -INFINITY ? top : fmaxf(top, best * c);
+                    const bool grows = now > top + kSlack;  // the first seen key too: top is -inf then
+                    if (t == w.t0) {
+                        top = now;
+                    } else if (__any_sync(~0u, grows)) {
+                        const float f = grows ? ex2(top - now) : 1.f;
+                        if (grows) top = now;
+                        sum *= f;
+                        wait(&bar[O_DONE], (tile - 1) & 1);  // the product of the tile before
+                        __syncwarp();
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int d = 0; d < D; d += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(lane_base + COL_O + d, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st32(lane_base + COL_O + d, o);
+                        }
+                        tmem_st_wait();
+                    }
+                    const float from = top == -INFINITY ? 0.f : top;
+                    const float2 c2 = make_float2(c, c), m2 = make_float2(-from, -from);
+                    float2 add = make_float2(0.f, 0.f);
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        float2 v = make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+                        v = fma_f2(v, c2, m2);
+                        v.x = ex2(v.x);
+                        v.y = ex2(v.y);
+                        add.x += v.x;
+                        add.y += v.y;
+                        pk[j] = pack_bf16(v.x, v.y);
+                    }
+                    sum += add.x + add.y;
+                    tmem_st32(s_col, pk);
+                    tmem_st_wait();
+                }
+                if (partial) {
+                    // ring position of this tile's values: K0 K1 V0 K2 V1 ... V(n-1)
+                    const int i = t - w.t0;
+                    const uint32_t pos = ring + (i == n_tiles - 1 ? 2 * n_tiles - 1 : 2 * i + 2);
+                    wait(&bar[KV_FULL0 + pos % kStages], (pos / kStages) & 1);
+                    if (clean_values<D>(smem + L::kRing + (pos % kStages) * L::kTile, limit, !cached, tid)) *dirty = item;
+                    fence_proxy_async_smem();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[P_READY0 + (tile & 1)]);
+            }
+            ring += 2 * n_tiles;
+            // the last two products (a parity tells two phases apart, so one after the other; those
+            // before them were done when the last scores were)
+            if (n_tiles > 1) wait(&bar[O_DONE], tile & 1);
+            wait(&bar[O_DONE], (tile - 1) & 1);
+            __syncwarp();
+            tc_fence_after();
+            if (warp_live) {
+                // rows leave through shared memory (the query tile, done with), 32 columns
+                // at a time, so that a warp writes whole runs of each row
+                const bool whole = w.whole();
+                const bool fix = *dirty == item;
+                const float mul = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;  // a row that saw nothing: zeros
+                const int64_t first_row = (int64_t)w.m * row_tile + warp * 32;
+                const int64_t part = ((int64_t)blockIdx.x * 2 + (w.t0 > 0 ? 0 : 1)) * row_tile + warp * 32;
+                const int live = min(32, rows - warp * 32);
+                float *stage = reinterpret_cast<float *>(smem + warp * (32 * 32 * 4));
+#pragma unroll 1
+                for (int d = 0; d < D; d += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(lane_base + COL_O + d, o);
+                    tmem_ld_wait();
+                    if (fix && tok >= 0) add_nonfinite(a, w, tok, d, o);
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float4 v;
+                        v.x = __uint_as_float(o[4 * j]) * mul;
+                        v.y = __uint_as_float(o[4 * j + 1]) * mul;
+                        v.z = __uint_as_float(o[4 * j + 2]) * mul;
+                        v.w = __uint_as_float(o[4 * j + 3]) * mul;
+                        *reinterpret_cast<float4 *>(stage + lane * 32 + ((j ^ (lane & 7)) << 2)) = v;
+                    }
+                    __syncwarp();
+                    for (int r = lane >> 3; r < live; r += 4) {  // 8 lanes a row
+                        const int j = lane & 7;
+                        const float4 v = *reinterpret_cast<const float4 *>(stage + r * 32 + ((j ^ (r & 7)) << 2));
+                        if (whole) {
+                            const int64_t flat = first_row + r;
+                            const int64_t out_row = (w.q.q0 + flat / group) * a.nheads + w.h * group + flat % group;
+                            uint2 b;
+                            b.x = pack_bf16(v.x, v.y);
+                            b.y = pack_bf16(v.z, v.w);
+                            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + out_row * D + d + 4 * j) = b;
+                        } else {
+                            *reinterpret_cast<float4 *>(p.parts.sums + (part + r) * D + d + 4 * j) = v;
+                        }
+                    }
+                }
+                if (tok >= 0) {
+                    if (!whole) {
+                        p.parts.stats[part + lane] = make_float2(top, sum);
+                    } else if (a.lse) {
+                        const int64_t flat = first_row + lane;
+                        a.lse[(w.q.q0 + flat / group) * a.nheads + w.h * group + flat % group] =
+                            sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+                    }
+                }
+            }
+            fence_proxy_async_smem();  // the query tile's next contents come by TMA
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[Q_EMPTY]);
+            more = w.next(a, group, row_tile, kKeys);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tm, kTmemCols);
+    }
+}
+
+int device_sms() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 152;
+    return sms;
+}
+
+struct Shape {
+    int group, tile_tokens, row_tile, grid;
+};
+
+Shape shape_of(const kv_attention_args &a) {
+    Shape s;
+    s.group = a.nheads / a.kv_heads;
+    // tokens of a row tile: as many as fit, but no more than a request is said to have, so that
+    // decode steps load and join few rows
+    s.tile_tokens = kRows / s.group;
+    const int hint = a.max_new_tokens > 0 ? a.max_new_tokens : 1;
+    if (hint < s.tile_tokens) s.tile_tokens = hint;
+    s.row_tile = s.tile_tokens * s.group;
+    s.grid = kvs::grid_of(a, s.row_tile, kKeys, kMinUnits, 2 * device_sms());
+    return s;
+}
+
+template <int D> cudaError_t launch(const kv_attention_args &a, void *ws, cudaStream_t s) {
+    const Shape sh = shape_of(a);
+    TcParams p;
+    p.a = a;
+    p.parts = kvs::parts_at(ws, sh.grid, sh.row_tile, D);
+    p.tile_tokens = sh.tile_tokens;
+    p.box_rows = kKeys;
+    while (a.block_size % p.box_rows) p.box_rows /= 2;
+    p.wait_limit = a.wait_limit_cycles > 0 ? a.wait_limit_cycles : 2000000000ll;
+    const uint64_t H = a.nheads, G = a.kv_heads, T = a.total_tokens;
+    CUtensorMap q, kc, vc, kn, vn;
+    const bool ok =
+        make_tmap_bf16_3d(&q, a.q, D, H, T, D * 2, (uint64_t)a.q_stride * 2, 64, sh.group, sh.tile_tokens) &&
+        make_tmap_bf16_3d(&kn, a.k_new, D, G, T, D * 2, (uint64_t)a.k_stride * 2, 64, 1, kKeys) &&
+        make_tmap_bf16_3d(&vn, a.v_new, D, G, T, D * 2, (uint64_t)a.v_stride * 2, 64, 1, kKeys) &&
+        make_tmap_16bit_4d(&kc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.k_cache, D, G, a.block_size, a.num_blocks, D * 2,
+                           G * D * 2, (uint64_t)a.cache_block_stride * 2, 64, 1, p.box_rows) &&
+        make_tmap_16bit_4d(&vc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.v_cache, D, G, a.block_size, a.num_blocks, D * 2,
+                           G * D * 2, (uint64_t)a.cache_block_stride * 2, 64, 1, p.box_rows);
+    if (!ok) return cudaErrorInvalidValue;
+    constexpr int smem = Layout<D>::kBytes;
+    cudaError_t e = cudaFuncSetAttribute(kv_attention_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kv_attention_tc_kernel<D><<<sh.grid, kThreads, smem, s>>>(q, kc, vc, kn, vn, p);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : kvs::join_launch(a, p.parts, sh.grid, sh.row_tile, s);
+}
+
+}  // namespace
+
+// A rule on sizes alone: what the TMA boxes and the two products take.  A negative scale would
+// turn the maximum of the scores into that of their opposites.
+bool kv_attention_tc_supported(const kv_attention_args &a) {
+    return a.dtype == SSD_BF16 && (a.headdim == 64 || a.headdim == 128) && a.nheads / a.kv_heads <= kRows &&
+           a.block_size % 8 == 0 && a.scale >= 0.f && a.cache_block_stride < (int64_t{1} << 38) &&
+           a.q_stride < (int64_t{1} << 38) && a.k_stride < (int64_t{1} << 38) && a.v_stride < (int64_t{1} << 38);
+}
+
+size_t kv_attention_tc_workspace(const kv_attention_args &a) {
+    const Shape sh = shape_of(a);
+    return kvs::parts_bytes(sh.grid, sh.row_tile, a.headdim);
+}
+
+cudaError_t kv_attention_tc_launch(const kv_attention_args &a, void *ws, cudaStream_t s) {
+    return a.headdim == 64 ? launch<64>(a, ws, s) : launch<128>(a, ws, s);
+}
+
+}  // namespace ssd

@@ -460,6 +460,18 @@ def test_attention_cache_views_and_far_blocks():
     _check(c)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_waits_are_bounded(D):
+    """With a limit of a few cycles the tensor-core kernel's waits give up: the call returns, the timeout is reported and
+    the next call on the same context is right."""
+    c = _attn(BF, 8, 2, D, 16, [2, 1, 30], [3000, 40, 900], False, seed=22)
+    err = _err()
+    _run(c, err, wait_limit_cycles=20)
+    torch.cuda.synchronize()
+    assert int(err.item()) == ssd.DEVERR_TIMEOUT
+    _check(c)
+
+
 def test_attention_without_tokens():
     c = _attn(BF, 4, 1, 128, 16, [0, 0], [100, 40], False, seed=5)
     out, lse = _run(c, _err())
