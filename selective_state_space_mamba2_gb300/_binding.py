@@ -574,45 +574,78 @@ def mamba1_state_update(x, dt, A, B, C, state_cache, state_indices, num_accepted
 
 
 # ------------------------------------------- attention layers of a hybrid model --
+#
+# Decode steps make these calls every few microseconds of GPU time, so the checks below are one
+# expression per tensor on the way through; only a failed one looks for what to say.
 
-def _i32v(t, name, shape, required=True):
-    """Pointer of a device int32 tensor of that shape."""
-    p = _dev(t, name, torch.int32, required)
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError("%s must be int32 of shape %s" % (name, list(shape)))
-    return p
+_INT32, _FLOAT32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+_TYPE_CODES = {torch.bfloat16: SSD_BF16, torch.float32: SSD_F32}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _kv_stream(stream, like):
+    """The caller's stream, or the current one of the tensors' device, as a pointer."""
+    if stream is not None:
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if _raw_stream is not None:
+        return _raw_stream(like.get_device())
+    return torch.cuda.current_stream(like.device).cuda_stream
+
+
+def _dense(t, name, shape, dtype):
+    """Pointer of a dense device tensor of that shape and type."""
+    try:
+        if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, name, dtype)
+    raise ValueError("%s must be %s of shape %s" % (name, dtype, list(shape)))
 
 
 def _rows(t, name, shape, dtype):
     """Pointer and token stride (elements) of a device tensor [T, heads, D] whose tokens are dense rows."""
+    try:
+        if t.shape == shape and t.dtype is dtype and t.is_cuda:
+            T, H, D = shape
+            s = t.stride()
+            if T == 0:
+                return t.data_ptr(), H * D
+            if (s[2] == 1 or D == 1) and (s[1] == D or H == 1):
+                return t.data_ptr(), (s[0] if T > 1 else H * D)
+            raise ValueError("the rows of %s must be dense" % name)
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if tuple(t.shape) != shape or t.dtype != dtype:
-        raise ValueError("%s must be %s of shape %s" % (name, dtype, list(shape)))
-    T, H, D = shape
-    if T == 0:
-        return t.data_ptr(), H * D
-    s = t.stride()
-    if s[2] != 1 or (H > 1 and s[1] != D):
-        raise ValueError("the rows of %s must be dense" % name)
-    return t.data_ptr(), (s[0] if T > 1 else H * D)
+    raise ValueError("%s must be %s of shape %s" % (name, dtype, list(shape)))
 
 
 def _pages(k_cache, v_cache, H, D, dtype):
     """Pointers, sizes and block stride of k_cache and v_cache ([num_blocks, block_size, H, D])."""
+    try:
+        shape = k_cache.shape
+        if (k_cache.dtype is dtype and v_cache.dtype is dtype and k_cache.is_cuda and v_cache.is_cuda and
+                len(shape) == 4 and shape == v_cache.shape and shape[2] == H and shape[3] == D):
+            nb, bs = shape[0], shape[1]
+            sk, sv = k_cache.stride(), v_cache.stride()
+            for s in (sk, sv) if sk != sv else (sk,):
+                if (s[3] != 1 and D > 1) or (s[2] != D and H > 1) or (s[1] != H * D and bs > 1):
+                    raise ValueError("the blocks of k_cache and v_cache must be dense")
+            if nb > 1 and sk[0] != sv[0]:
+                raise ValueError("k_cache and v_cache must have the same block stride")
+            return k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, (sk[0] if nb > 1 else bs * H * D)
+    except AttributeError:
+        pass
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError("%s must be a CUDA tensor" % name)
-        if t.dim() != 4 or t.dtype != dtype or tuple(t.shape[2:]) != (H, D) or t.shape != k_cache.shape:
-            raise ValueError("%s must be %s [num_blocks, block_size, %d, %d]" % (name, dtype, H, D))
-        s = t.stride()
-        if s[3] != 1 or (H > 1 and s[2] != D) or (t.shape[1] > 1 and s[1] != H * D):
-            raise ValueError("the blocks of %s must be dense" % name)
-    nb, bs = k_cache.shape[:2]
-    stride = k_cache.stride(0) if nb > 1 else bs * H * D
-    if nb > 1 and v_cache.stride(0) != stride:
-        raise ValueError("k_cache and v_cache must have the same block stride")
-    return k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, stride
+    raise ValueError("k_cache and v_cache must be %s [num_blocks, block_size, %d, %d]" % (dtype, H, D))
+
+
+def _code(t):
+    code = _TYPE_CODES.get(t.dtype)
+    return _dtype_code(t) if code is None else code
 
 
 def kv_block_tables(context_lens, new_lens, reserved_lens, block_table, free_ring, ring_state, block_size, num_blocks,
@@ -624,33 +657,36 @@ def kv_block_tables(context_lens, new_lens, reserved_lens, block_table, free_rin
     [max_tokens].  ``out``: such a dict from an earlier call to write to instead (not the one whose
     reserved_lens or ring_state this call reads)."""
     S = context_lens.numel()
+    one, tokens = (S,), (max_tokens,)
+    p_ctx = _dense(context_lens, "context_lens", one, _INT32)
     if block_table.dim() != 2 or block_table.shape[0] != S:
         raise ValueError("block_table must be int32 [%d, cols]" % S)
+    cols = block_table.shape[1]
     if out is None:
-        i32 = dict(dtype=torch.int32, device=context_lens.device)
-        out = dict(cu_seqlens=torch.empty(S + 1, **i32), seq_lens=torch.empty(S, **i32),
-                   reserved_lens=torch.empty(S, **i32), ring_state=torch.empty(2, **i32),
-                   slots=torch.empty(max_tokens, **i32), positions=torch.empty(max_tokens, **i32),
-                   token_req=torch.empty(max_tokens, **i32))
-    a = TablesArgs()
-    a.num_reqs, a.block_size, a.table_cols = S, int(block_size), block_table.shape[1]
-    a.free_capacity, a.max_tokens, a.num_blocks = free_ring.numel(), int(max_tokens), int(num_blocks)
-    a.null_block_id = int(null_block_id)
-    a.context_lens = _i32v(context_lens, "context_lens", (S,))
-    a.new_lens = _i32v(new_lens, "new_lens", (S,))
-    a.reserved_lens = _i32v(reserved_lens, "reserved_lens", (S,))
-    a.block_table = _dev(block_table, "block_table", torch.int32)
-    a.free_ring = _dev(free_ring, "free_ring", torch.int32)
-    a.ring_in = _i32v(ring_state, "ring_state", (2,))
-    a.ring_out = _i32v(out["ring_state"], "out ring_state", (2,))
-    a.cu_seqlens = _i32v(out["cu_seqlens"], "out cu_seqlens", (S + 1,))
-    a.seq_lens = _i32v(out["seq_lens"], "out seq_lens", (S,))
-    a.reserved_out = _i32v(out["reserved_lens"], "out reserved_lens", (S,))
-    a.slots = _i32v(out["slots"], "out slots", (max_tokens,))
-    a.positions = _i32v(out["positions"], "out positions", (max_tokens,))
-    a.token_req = _i32v(out.get("token_req"), "out token_req", (max_tokens,), required=False)
-    a.err_word = _dev(err_word, "err_word", required=False)
-    rc = lib().kv_block_tables(ctypes.byref(a), _stream(stream))
+        empty, dev = torch.empty, context_lens.device
+        cu, seq, res = (empty(S + 1, dtype=_INT32, device=dev), empty(S, dtype=_INT32, device=dev),
+                        empty(S, dtype=_INT32, device=dev))
+        ring, slots = empty(2, dtype=_INT32, device=dev), empty(max_tokens, dtype=_INT32, device=dev)
+        pos, req = empty(max_tokens, dtype=_INT32, device=dev), empty(max_tokens, dtype=_INT32, device=dev)
+        out = {"cu_seqlens": cu, "seq_lens": seq, "reserved_lens": res, "ring_state": ring, "slots": slots,
+               "positions": pos, "token_req": req}
+        outs = (ring.data_ptr(), cu.data_ptr(), seq.data_ptr(), res.data_ptr(), slots.data_ptr(), pos.data_ptr(),
+                req.data_ptr())
+    else:
+        outs = (_dense(out["ring_state"], "out ring_state", (2,), _INT32),
+                _dense(out["cu_seqlens"], "out cu_seqlens", (S + 1,), _INT32),
+                _dense(out["seq_lens"], "out seq_lens", one, _INT32),
+                _dense(out["reserved_lens"], "out reserved_lens", one, _INT32),
+                _dense(out["slots"], "out slots", tokens, _INT32),
+                _dense(out["positions"], "out positions", tokens, _INT32),
+                None if out.get("token_req") is None else _dense(out["token_req"], "out token_req", tokens, _INT32))
+    a = TablesArgs(S, block_size, cols, free_ring.numel(), max_tokens, num_blocks, null_block_id, p_ctx,
+                   _dense(new_lens, "new_lens", one, _INT32), _dense(reserved_lens, "reserved_lens", one, _INT32),
+                   _dense(block_table, "block_table", (S, cols), _INT32),
+                   _dense(free_ring, "free_ring", (free_ring.numel(),), _INT32),
+                   _dense(ring_state, "ring_state", (2,), _INT32), *outs,
+                   None if err_word is None else _dev(err_word, "err_word"))
+    rc = lib().kv_block_tables(ctypes.byref(a), _kv_stream(stream, context_lens))
     if rc != SSD_OK:
         raise SSDError("kv_block_tables", rc)
     return out
@@ -665,38 +701,41 @@ def kv_qk_norm_rope(q, k, positions=None, cos_sin=None, q_weight=None, k_weight=
     cache too.  q, k and v may be views of one packed projection.  Returns (q_out, k_out)."""
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q and k must be [T, heads, D]")
-    T, H, D = q.shape
+    qs = q.shape
+    T, H, D = qs
     Hkv = k.shape[1]
+    ks = (T, Hkv, D)
+    dtype = q.dtype
+    code = _code(q)
+    p_q, s_q = _rows(q, "q", qs, dtype)
+    p_k, s_k = _rows(k, "k", ks, dtype)
     if q_out is None:
-        q_out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+        q_out = torch.empty(qs, dtype=dtype, device=q.device)
+        p_qo = q_out.data_ptr()
+    else:
+        p_qo = _dense(q_out, "q_out", qs, dtype)
     if k_out is None:
-        k_out = torch.empty((T, Hkv, D), dtype=q.dtype, device=q.device)
-    a = QkArgs()
-    a.total_tokens, a.nheads, a.kv_heads, a.headdim, a.dtype = T, H, Hkv, D, _dtype_code(q)
-    a.interleaved, a.eps = int(bool(interleaved)), float(eps)
-    a.q, a.q_stride = _rows(q, "q", (T, H, D), q.dtype)
-    a.k, a.k_stride = _rows(k, "k", (T, Hkv, D), q.dtype)
-    for name, t, heads in (("q_out", q_out, H), ("k_out", k_out, Hkv)):
-        if tuple(t.shape) != (T, heads, D) or t.dtype != q.dtype:
-            raise ValueError("%s must be %s of shape %s" % (name, q.dtype, [T, heads, D]))
-    a.q_out, a.k_out = _dev(q_out, "q_out"), _dev(k_out, "k_out")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and tuple(w.shape) != (D,):
-            raise ValueError("%s must be float32 [%d]" % (name, D))
-    a.q_weight = _dev(q_weight, "q_weight", torch.float32, required=False)
-    a.k_weight = _dev(k_weight, "k_weight", torch.float32, required=False)
+        k_out = torch.empty(ks, dtype=dtype, device=q.device)
+        p_ko = k_out.data_ptr()
+    else:
+        p_ko = _dense(k_out, "k_out", ks, dtype)
+    p_cs = p_pos = p_v = p_slots = p_kc = p_vc = None
+    top = rot = nb = bs = s_v = block = 0
     if cos_sin is not None:
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
-        a.max_position, a.rotary_dim = cos_sin.shape
-        a.cos_sin = _dev(cos_sin, "cos_sin", torch.float32)
-        a.positions = _i32v(positions, "positions", (T,))
+        top, rot = cos_sin.shape
+        p_cs = _dense(cos_sin, "cos_sin", cos_sin.shape, _FLOAT32)
+        p_pos = _dense(positions, "positions", (T,), _INT32)
     if k_cache is not None or v_cache is not None or slots is not None:
-        a.k_cache, a.v_cache, a.num_blocks, a.block_size, a.cache_block_stride = _pages(k_cache, v_cache, Hkv, D, q.dtype)
-        a.v, a.v_stride = _rows(v, "v", (T, Hkv, D), q.dtype)
-        a.slots = _i32v(slots, "slots", (T,))
-    a.err_word = _dev(err_word, "err_word", required=False)
-    rc = lib().kv_qk_norm_rope(ctypes.byref(a), _stream(stream))
+        p_kc, p_vc, nb, bs, block = _pages(k_cache, v_cache, Hkv, D, dtype)
+        p_v, s_v = _rows(v, "v", ks, dtype)
+        p_slots = _dense(slots, "slots", (T,), _INT32)
+    a = QkArgs(T, H, Hkv, D, rot, 1 if interleaved else 0, top, code, bs, nb, eps, s_q, s_k, s_v, block, p_q, p_k, p_v,
+               None if q_weight is None else _dense(q_weight, "q_weight", (D,), _FLOAT32),
+               None if k_weight is None else _dense(k_weight, "k_weight", (D,), _FLOAT32), p_cs, p_pos, p_slots, p_qo,
+               p_ko, p_kc, p_vc, None if err_word is None else _dev(err_word, "err_word"))
+    rc = lib().kv_qk_norm_rope(ctypes.byref(a), _kv_stream(stream, q))
     if rc != SSD_OK:
         raise SSDError("kv_qk_norm_rope", rc)
     return q_out, k_out
@@ -707,36 +746,33 @@ def attention_args(q, k_new, v_new, k_cache, v_cache, cu_seqlens, context_lens, 
     """Fills an ``AttentionArgs`` from device tensors (validating shapes and dtypes)."""
     if q.dim() != 3 or k_new.dim() != 3:
         raise ValueError("q and k_new must be [T, heads, D]")
-    T, H, D = q.shape
+    qs = q.shape
+    T, H, D = qs
     Hkv = k_new.shape[1]
+    ks = (T, Hkv, D)
+    dtype = q.dtype
+    code = _code(q)
     S = cu_seqlens.numel() - 1
     if block_table.dim() != 2 or block_table.shape[0] != S:
         raise ValueError("block_table must be int32 [%d, cols]" % S)
-    if tuple(out.shape) != (T, H, D) or out.dtype != q.dtype:
-        raise ValueError("out must be %s of shape %s" % (q.dtype, [T, H, D]))
-    a = AttentionArgs()
-    a.total_tokens, a.num_seqs, a.nheads, a.kv_heads, a.headdim, a.dtype = T, S, H, Hkv, D, _dtype_code(q)
-    a.table_cols, a.max_new_tokens = block_table.shape[1], int(max_new_tokens)
-    a.scale = float(D ** -0.5 if scale is None else scale)
-    a.wait_limit_cycles = int(wait_limit_cycles)
-    a.q, a.q_stride = _rows(q, "q", (T, H, D), q.dtype)
-    a.k_new, a.k_stride = _rows(k_new, "k_new", (T, Hkv, D), q.dtype)
-    a.v_new, a.v_stride = _rows(v_new, "v_new", (T, Hkv, D), q.dtype)
-    a.k_cache, a.v_cache, a.num_blocks, a.block_size, a.cache_block_stride = _pages(k_cache, v_cache, Hkv, D, q.dtype)
-    a.cu_seqlens = _i32v(cu_seqlens, "cu_seqlens", (S + 1,))
-    a.context_lens = _i32v(context_lens, "context_lens", (S,))
-    a.block_table = _dev(block_table, "block_table", torch.int32)
+    table = block_table.shape
+    p_q, s_q = _rows(q, "q", qs, dtype)
+    p_k, s_k = _rows(k_new, "k_new", ks, dtype)
+    p_v, s_v = _rows(v_new, "v_new", ks, dtype)
+    p_kc, p_vc, nb, bs, block = _pages(k_cache, v_cache, Hkv, D, dtype)
+    p_mask, words = None, 0
     if tree_mask is not None:
         if tree_mask.dim() != 2 or tree_mask.shape[0] != T:
             raise ValueError("tree_mask must be int32 [%d, words]" % T)
-        a.tree_mask, a.mask_words = _dev(tree_mask, "tree_mask", torch.int32), tree_mask.shape[1]
-    a.out = _dev(out, "out")
-    if lse is not None:
-        if tuple(lse.shape) != (T, H):
-            raise ValueError("lse must be float32 of shape %s" % [T, H])
-        a.lse = _dev(lse, "lse", torch.float32)
-    a.err_word = _dev(err_word, "err_word", required=False)
-    return a
+        words = tree_mask.shape[1]
+        p_mask = _dense(tree_mask, "tree_mask", tree_mask.shape, _INT32)
+    return AttentionArgs(T, S, H, Hkv, D, code, bs, nb, table[1], max_new_tokens, words,
+                         D ** -0.5 if scale is None else scale, s_q, s_k, s_v, block, wait_limit_cycles, p_q, p_k, p_v,
+                         p_kc, p_vc, _dense(cu_seqlens, "cu_seqlens", (S + 1,), _INT32),
+                         _dense(context_lens, "context_lens", (S,), _INT32),
+                         _dense(block_table, "block_table", table, _INT32), p_mask, _dense(out, "out", qs, dtype),
+                         None if lse is None else _dense(lse, "lse", (T, H), _FLOAT32),
+                         None if err_word is None else _dev(err_word, "err_word"))
 
 
 def kv_tree_attention_workspace_size(args):
@@ -753,12 +789,15 @@ def kv_tree_attention(q, k_new, v_new, k_cache, v_cache, cu_seqlens, context_len
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if lse is None and return_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        lse = torch.empty(q.shape[:2], dtype=_FLOAT32, device=q.device)
     a = attention_args(q, k_new, v_new, k_cache, v_cache, cu_seqlens, context_lens, block_table, out, max_new_tokens,
                        tree_mask, scale, lse, err_word, wait_limit_cycles)
+    L = lib()
+    ref = ctypes.byref(a)
     if workspace is None:
-        workspace = torch.empty(max(kv_tree_attention_workspace_size(a), 1), dtype=torch.uint8, device=q.device)
-    rc = lib().kv_tree_attention(ctypes.byref(a), workspace.data_ptr(), workspace.numel(), _stream(stream))
+        need = L.kv_tree_attention_workspace_size(ref)
+        workspace = torch.empty(need or 1, dtype=torch.uint8, device=q.device)
+    rc = L.kv_tree_attention(ref, workspace.data_ptr(), workspace.numel(), _kv_stream(stream, q))
     if rc != SSD_OK:
         raise SSDError("kv_tree_attention", rc)
     return out if lse is None else (out, lse)
@@ -767,33 +806,43 @@ def kv_tree_attention(q, k_new, v_new, k_cache, v_cache, cu_seqlens, context_len
 def kv_commit_tokens(k_new, v_new, k_cache, v_cache, slots, cu_seqlens=None, context_lens=None, path=None,
                      path_lens=None, context_out=None, err_word=None, stream=None):
     """Keys and values of accepted tokens to the cache: step i of request r's ``path`` ([S, max_path], the index of
-    a new token; None: all of them in order) goes to the slot of its new token i.  Returns the new context
-    lengths, or None without ``context_lens``."""
+    a new token; None: all of them in order) goes to the slot of its new token i.  ``slots`` may be padded beyond
+    the tokens.  Returns the new context lengths, or None without ``context_lens``."""
     if k_new.dim() != 3:
         raise ValueError("k_new must be [T, heads, D]")
-    T, H, D = k_new.shape
-    S = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
-    a = CommitArgs()
-    a.total_tokens, a.num_seqs, a.kv_heads, a.headdim, a.dtype = T, S, H, D, _dtype_code(k_new)
-    a.k_new, a.k_stride = _rows(k_new, "k_new", (T, H, D), k_new.dtype)
-    a.v_new, a.v_stride = _rows(v_new, "v_new", (T, H, D), k_new.dtype)
-    a.k_cache, a.v_cache, a.num_blocks, a.block_size, a.cache_block_stride = _pages(k_cache, v_cache, H, D, k_new.dtype)
-    a.slots = _dev(slots, "slots", torch.int32)
-    if slots.numel() < T:  # a step's slot map may be padded beyond its tokens
+    shape = k_new.shape
+    T, H, D = shape
+    dtype = k_new.dtype
+    code = _code(k_new)
+    p_k, s_k = _rows(k_new, "k_new", shape, dtype)
+    p_v, s_v = _rows(v_new, "v_new", shape, dtype)
+    p_kc, p_vc, nb, bs, block = _pages(k_cache, v_cache, H, D, dtype)
+    p_slots = _dense(slots, "slots", (slots.numel(),), _INT32)
+    if slots.numel() < T:
         raise ValueError("slots must have an entry for each of the %d tokens" % T)
-    a.cu_seqlens = _dev(cu_seqlens, "cu_seqlens", torch.int32, required=path is not None or context_lens is not None)
+    S, width = 0, 0
+    p_cu = p_path = p_lens = p_ctx = p_out = None
+    if cu_seqlens is not None:
+        S = cu_seqlens.numel() - 1
+        p_cu = _dense(cu_seqlens, "cu_seqlens", (S + 1,), _INT32)
+    elif path is not None or context_lens is not None:
+        raise ValueError("cu_seqlens is required")
     if path is not None:
         if path.dim() != 2 or path.shape[0] != S or path.shape[1] == 0:
             raise ValueError("path must be int32 [%d, max_path]" % S)
-        a.path, a.max_path = _dev(path, "path", torch.int32), path.shape[1]
-        a.path_lens = _i32v(path_lens, "path_lens", (S,))
+        width = path.shape[1]
+        p_path = _dense(path, "path", path.shape, _INT32)
+        p_lens = _dense(path_lens, "path_lens", (S,), _INT32)
     if context_lens is not None:
+        p_ctx = _dense(context_lens, "context_lens", (S,), _INT32)
         if context_out is None:
-            context_out = torch.empty_like(context_lens)
-        a.context_lens = _i32v(context_lens, "context_lens", (S,))
-        a.context_out = _i32v(context_out, "context_out", (S,))
-    a.err_word = _dev(err_word, "err_word", required=False)
-    rc = lib().kv_commit_tokens(ctypes.byref(a), _stream(stream))
+            context_out = torch.empty(S, dtype=_INT32, device=k_new.device)
+            p_out = context_out.data_ptr()
+        else:
+            p_out = _dense(context_out, "context_out", (S,), _INT32)
+    a = CommitArgs(T, S, H, D, code, bs, nb, width, s_k, s_v, block, p_k, p_v, p_slots, p_cu, p_path, p_lens, p_ctx,
+                   p_out, p_kc, p_vc, None if err_word is None else _dev(err_word, "err_word"))
+    rc = lib().kv_commit_tokens(ctypes.byref(a), _kv_stream(stream, k_new))
     if rc != SSD_OK:
         raise SSDError("kv_commit_tokens", rc)
     return context_out

@@ -12,7 +12,9 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kRowTile = 16;
-constexpr int kKeyTile = 32;
+constexpr int kKeyShift = 5;
+constexpr int kKeyTile = 1 << kKeyShift;
+constexpr int kOverhead = 1;  // of an item, in key tiles
 constexpr int kMinUnits = 4;
 constexpr int kCtasPerSm = 4;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -37,7 +39,8 @@ template <> __device__ __forceinline__ void load8<__nv_bfloat16>(float (&f)[8], 
 
 // NV: 32-float pieces of a row a thread group covers, headdim <= 32 NV
 template <typename T, int NV>
-__global__ void __launch_bounds__(kThreads) kv_attention_simt_kernel(const kv_attention_args a, const kvs::Parts parts) {
+__global__ void __launch_bounds__(kThreads) kv_attention_simt_kernel(const kv_attention_args a, const kvs::Parts parts,
+                                                                  const kvs::Tiling g) {
     extern __shared__ __align__(16) float smem[];
     __shared__ kvs::FindSmem find;
     const int D = a.headdim, group = a.nheads / a.kv_heads, pitch = D + 4;
@@ -45,27 +48,26 @@ __global__ void __launch_bounds__(kThreads) kv_attention_simt_kernel(const kv_at
     const int tid = threadIdx.x, row = tid >> 3, sub = tid & 7;
 
     kvs::Walk w;
-    if (!kvs::find_run(a, group, kRowTile, kKeyTile, kMinUnits, find, parts.borders, w)) return;
+    if (!kvs::find_run(a, g, kMinUnits, find, parts.borders, w)) return;
     const float c = a.scale * kLog2e;
     const int pieces = D / 8;
     bool more = true;
     while (more) {
-        const int rows = (int)min((int64_t)kRowTile, (int64_t)w.q.n * group - (int64_t)w.m * kRowTile);
+        const int heads = w.heads(g, group), rows = w.tokens(g) * heads, head0 = w.h * group + w.part * g.heads;
+        const int token0 = w.first_token(g);
         // query rows
         __syncthreads();
         for (int i = tid; i < kRowTile * pieces; i += kThreads) {
             const int r = i / pieces, e = (i % pieces) * 8;
             float f[8] = {};
             if (r < rows) {
-                const int64_t flat = (int64_t)w.m * kRowTile + r;
-                const int64_t tok = w.q.q0 + flat / group;
-                load8(f, static_cast<const T *>(a.q) + tok * a.q_stride + (w.h * group + flat % group) * D + e);
+                const int64_t tok = w.q.q0 + token0 + r / heads;
+                load8(f, static_cast<const T *>(a.q) + tok * a.q_stride + (head0 + r % heads) * D + e);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) sq[r * pitch + e + j] = f[j];
         }
-        const int64_t my_flat = (int64_t)w.m * kRowTile + row;
-        const int32_t my_tok = row < rows ? (int32_t)(my_flat / group) : -1;
+        const int32_t my_tok = row < rows ? token0 + row / heads : -1;
         const uint32_t *mask = a.tree_mask && my_tok >= 0 ? a.tree_mask + (int64_t)(w.q.q0 + my_tok) * a.mask_words : nullptr;
 
         float top = -INFINITY, sum = 0.f, acc[NV][4] = {};
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(kThreads) kv_attention_simt_kernel(const kv_at
         for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
         if (my_tok >= 0) {
             if (w.whole()) {
-                const int64_t out_row = (int64_t)(w.q.q0 + my_tok) * a.nheads + w.h * group + my_flat % group;
+                const int64_t out_row = (int64_t)(w.q.q0 + my_tok) * a.nheads + head0 + row % heads;
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that saw nothing: zeros
                 T *out = static_cast<T *>(a.out) + out_row * D;
 #pragma unroll
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) kv_attention_simt_kernel(const kv_at
                 }
                 if (a.lse && sub == 0) a.lse[out_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
             } else {
-                const int64_t part = ((int64_t)blockIdx.x * 2 + (w.t0 > 0 ? 0 : 1)) * kRowTile + row;
+                const int64_t part = ((int64_t)blockIdx.x * 2 + (w.t0 > 0 ? 0 : 1)) * g.rows + row;
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
                     const int e = 32 * v + 4 * sub;
@@ -187,37 +189,42 @@ __global__ void __launch_bounds__(kThreads) kv_attention_simt_kernel(const kv_at
                 if (sub == 0) parts.stats[part] = make_float2(top, sum);
             }
         }
-        more = w.next(a, group, kRowTile, kKeyTile);
+        more = w.next(a, g);
     }
 }
 
 // ---- joining the parts of a cut item -----------------------------------------------
 //
-// CTA b looks at the border before CTA b's run.  If it cuts an item and is the first border in
-// it, this CTA adds up the item's parts: the one of CTA b - 1 (begun there) and those of b and
-// the CTAs after it while their runs start inside the item.  out = sum_i 2^(m_i - m) O_i / L.
+// CTA b looks at the border before CTA b's run.  If it cuts an item's key tiles and is the first
+// border to do so, this CTA adds up the item's parts: the one of CTA b - 1 (begun there) and those
+// of b and the CTAs after it while their runs start inside the item:
+//   out = sum_i 2^(m_i - m) O_i / L,  L = sum_i 2^(m_i - m) l_i,  m = max_i m_i.
+// A warp per row; the parts' factors are worked out a lane each, so that the loads of the sums
+// depend on nothing but one another's order in the sum.
 constexpr int kJoinThreads = 128;
 constexpr int kJoinRows = 4;  // rows of an item joined by one CTA, a warp each
 
-template <typename T>
+template <typename T, int NV>  // NV: 128-float pieces of a row
 __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const kv_attention_args a, const kvs::Parts parts,
-                                                               const int row_tile) {
+                                                               const kvs::Tiling g) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are complete
     const int b = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ctas = parts.borders[0].ctas;
     if (b >= ctas) return;
     const kvs::Border me = parts.borders[b];
-    if (me.item0 == me.lo || parts.borders[b - 1].lo > me.item0) return;  // not cut here, or joined by an earlier one
-    const int D = a.headdim, group = a.nheads / a.kv_heads;
-    const kvs::Request q = kvs::request(a, me.r, false);
+    const long long tile0 = me.item0 + g.overhead;  // unit of the item's first key tile
+    if (kvs::run_start(me.total, b, ctas) <= tile0 || kvs::run_start(me.total, b - 1, ctas) > tile0) return;
     const int row = blockIdx.y * kJoinRows + warp;
-    const int64_t flat = (int64_t)me.m * row_tile + row;
-    if (row >= row_tile || flat >= (int64_t)q.n * group) return;
-    int last = b;  // last CTA with a part
-    while (last + 1 < ctas && parts.borders[last + 1].lo < me.item1) ++last;
-    auto part_row = [&](int cta) { return ((int64_t)cta * 2 + (cta == b - 1 ? 1 : 0)) * row_tile + row; };
+    if (row >= me.tokens * me.heads) return;
+    // the last CTA with a part: the last one whose run starts before the item's end
+    int last = (int)min((long long)ctas - 1, me.item1 * ctas / me.total + 1);
+    while (kvs::run_start(me.total, last, ctas) >= me.item1) --last;
+    const int D = a.headdim, n = last - b + 2;
+    // part k: of CTA b - 1 + k
+    auto part_row = [&](int k) { return ((int64_t)(b - 1 + k) * 2 + (k == 0 ? 1 : 0)) * g.rows + row; };
     float top = -INFINITY;
-    for (int i = b - 1 + lane; i <= last; i += 32) {
-        const float m = parts.stats[part_row(i)].x;
+    for (int k = lane; k < n; k += 32) {
+        const float m = parts.stats[part_row(k)].x;
         top = m > top || m != m ? m : top;
     }
 #pragma unroll
@@ -226,58 +233,79 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const kv_attentio
         top = m > top || m != m ? m : top;
     }
     const float from = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, acc[8] = {};  // headdim <= 256: 8 entries a lane
-    for (int i = b - 1; i <= last; ++i) {
-        const int64_t pr = part_row(i);
-        const float2 st = parts.stats[pr];
-        const float f = exp2f(st.x - from);
-        sum = fmaf(f, st.y, sum);
+    float sum = 0.f, acc[NV][4] = {};
+    for (int k0 = 0; k0 < n; k0 += 32) {
+        float f = 0.f;
+        if (k0 + lane < n) {
+            const float2 st = parts.stats[part_row(k0 + lane)];
+            f = exp2f(st.x - from);
+            sum = fmaf(f, st.y, sum);
+        }
+        const int here = min(32, n - k0);
+#pragma unroll 8
+        for (int k = 0; k < here; ++k) {
+            const float fk = __shfl_sync(~0u, f, k);
+            const float *src = parts.sums + part_row(k0 + k) * D;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int e = 128 * j + 4 * lane;
-            if (e < D) {
-                const float4 v = *reinterpret_cast<const float4 *>(parts.sums + pr * D + e);
-                acc[4 * j] = fmaf(f, v.x, acc[4 * j]);
-                acc[4 * j + 1] = fmaf(f, v.y, acc[4 * j + 1]);
-                acc[4 * j + 2] = fmaf(f, v.z, acc[4 * j + 2]);
-                acc[4 * j + 3] = fmaf(f, v.w, acc[4 * j + 3]);
+            for (int j = 0; j < NV; ++j) {
+                const int e = 128 * j + 4 * lane;
+                if (e < D) {
+                    const float4 v = *reinterpret_cast<const float4 *>(src + e);
+                    acc[j][0] = fmaf(fk, v.x, acc[j][0]);
+                    acc[j][1] = fmaf(fk, v.y, acc[j][1]);
+                    acc[j][2] = fmaf(fk, v.z, acc[j][2]);
+                    acc[j][3] = fmaf(fk, v.w, acc[j][3]);
+                }
             }
         }
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t out_row = (int64_t)(q.q0 + flat / group) * a.nheads + me.h * group + flat % group;
+    const int64_t out_row = (int64_t)(me.token0 + row / me.heads) * a.nheads + me.head0 + row % me.heads;
     T *out = static_cast<T *>(a.out) + out_row * D;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < NV; ++j) {
         const int e = 128 * j + 4 * lane;
         if (e < D)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) out[e + i] = from_f32<T>(acc[4 * j + i] * inv);
+            for (int i = 0; i < 4; ++i) out[e + i] = from_f32<T>(acc[j][i] * inv);
     }
     if (a.lse && lane == 0) a.lse[out_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
-int device_sms() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 152;
-    return sms;
+template <typename T, int NV>
+cudaError_t launch_join(const kv_attention_args &a, const kvs::Parts &p, int grid, const kvs::Tiling &g, cudaStream_t s) {
+    // a programmatic dependent of the attention kernel: its CTAs may be set up while that ends
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)kvs::ceil_div(g.rows, kJoinRows));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_join_kernel<T, NV>, a, p, g);
 }
 
-int simt_grid(const kv_attention_args &a) {
-    return kvs::grid_of(a, kRowTile, kKeyTile, kMinUnits, kCtasPerSm * device_sms());
+kvs::Tiling simt_tiling(const kv_attention_args &a) { return kvs::tiling(a, kRowTile, kKeyShift, kOverhead); }
+
+int simt_grid(const kv_attention_args &a, const kvs::Tiling &g) {
+    return kvs::grid_of(a, g, kMinUnits, kCtasPerSm * device_sms());
 }
 
 template <typename T, int NV>
 cudaError_t launch(const kv_attention_args &a, void *ws, cudaStream_t s) {
-    const int grid = simt_grid(a);
-    const kvs::Parts parts = kvs::parts_at(ws, grid, kRowTile, a.headdim);
+    const kvs::Tiling g = simt_tiling(a);
+    const int grid = simt_grid(a, g);
+    const kvs::Parts parts = kvs::parts_at(ws, grid, g.rows, a.headdim);
     const int smem = smem_bytes(a.headdim);
     cudaError_t e = cudaFuncSetAttribute(kv_attention_simt_kernel<T, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kv_attention_simt_kernel<T, NV><<<grid, kThreads, smem, s>>>(a, parts);
+    kv_attention_simt_kernel<T, NV><<<grid, kThreads, smem, s>>>(a, parts, g);
     e = cudaGetLastError();
-    return e != cudaSuccess ? e : kvs::join_launch(a, parts, grid, kRowTile, s);
+    return e != cudaSuccess ? e : kvs::join_launch(a, parts, grid, g, s);
 }
 
 template <typename T> cudaError_t launch_dim(const kv_attention_args &a, void *ws, cudaStream_t s) {
@@ -288,18 +316,17 @@ template <typename T> cudaError_t launch_dim(const kv_attention_args &a, void *w
 
 }  // namespace
 
-cudaError_t kvs::join_launch(const kv_attention_args &a, const Parts &p, int grid, int row_tile, cudaStream_t s) {
+cudaError_t kvs::join_launch(const kv_attention_args &a, const Parts &p, int grid, const Tiling &g, cudaStream_t s) {
     if (grid < 2) return cudaSuccess;
-    const dim3 g((unsigned)(grid - 1), (unsigned)((row_tile + kJoinRows - 1) / kJoinRows));
     if (a.dtype == SSD_BF16)
-        kv_join_kernel<__nv_bfloat16><<<g, kJoinThreads, 0, s>>>(a, p, row_tile);
-    else
-        kv_join_kernel<float><<<g, kJoinThreads, 0, s>>>(a, p, row_tile);
-    return cudaGetLastError();
+        return a.headdim <= 128 ? launch_join<__nv_bfloat16, 1>(a, p, grid, g, s)
+                                : launch_join<__nv_bfloat16, 2>(a, p, grid, g, s);
+    return a.headdim <= 128 ? launch_join<float, 1>(a, p, grid, g, s) : launch_join<float, 2>(a, p, grid, g, s);
 }
 
 size_t kv_attention_simt_workspace(const kv_attention_args &a) {
-    return kvs::parts_bytes(simt_grid(a), kRowTile, a.headdim);
+    const kvs::Tiling g = simt_tiling(a);
+    return kvs::parts_bytes(simt_grid(a, g), g.rows, a.headdim);
 }
 
 cudaError_t kv_attention_simt_launch(const kv_attention_args &a, void *ws, cudaStream_t s) {

@@ -33,11 +33,13 @@ namespace {
 using namespace tc;
 
 constexpr int kRows = 128;    // TMEM lanes: query rows of a tile
-constexpr int kKeys = 64;     // keys of a tile
+constexpr int kKeyShift = 6;
+constexpr int kKeys = 1 << kKeyShift;  // keys of a tile
 constexpr int kThreads = 192;
 constexpr int kLoadWarp = 4, kMmaWarp = 5;
 constexpr int kStages = 5;
-constexpr int kMinUnits = 2;
+constexpr int kOverhead = 3;  // of an item, in key tiles
+constexpr int kMinUnits = 6;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;  // growth of a maximum (base 2) that is let stand
@@ -45,7 +47,8 @@ constexpr float kSlack = 8.f;  // growth of a maximum (base 2) that is let stand
 struct TcParams {
     kv_attention_args a;
     kvs::Parts parts;
-    int32_t tile_tokens;  // tokens of a row tile
+    kvs::Tiling g;
+    uint32_t group_inv;   // ceil(2^16 / query heads per key head): row / group = row * group_inv >> 16, row < 128
     int32_t box_rows;     // rows of a page that one copy brings: divides block_size and kKeys
     long long wait_limit;
 };
@@ -58,7 +61,7 @@ template <int D> struct Layout {
     static constexpr int kTile = kKeys * D * 2;
     static constexpr int kRing = kQ;
     static constexpr int kBars = kRing + kStages * kTile;
-    static constexpr int kMisc = kBars + NUM_BARS * 8;  // TMEM base, dead mark, item with non-finite values
+    static constexpr int kMisc = kBars + NUM_BARS * 8;  // TMEM base, dead mark, items with non-finite values
     static constexpr int kFind = (kMisc + 16 + 15) / 16 * 16;
     static constexpr int kBytes = kFind + (int)sizeof(kvs::FindSmem);
 };
@@ -170,37 +173,43 @@ __global__ void __launch_bounds__(kThreads, 2)
     constexpr uint32_t COL_S = 0, COL_O = 128;  // two score tiles of 64 columns, the output
     const kv_attention_args &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int group = a.nheads / a.kv_heads, row_tile = p.tile_tokens * group;
+    const int group = a.nheads / a.kv_heads;
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + L::kBars);
     uint32_t *sTmem = reinterpret_cast<uint32_t *>(smem + L::kMisc);
     volatile int *dead = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
     volatile int *dirty = reinterpret_cast<volatile int *>(smem + L::kMisc + 8);
 
-    kvs::Walk w;
-    if (!kvs::find_run(a, group, row_tile, kKeys, kMinUnits, *reinterpret_cast<kvs::FindSmem *>(smem + L::kFind),
-                       p.parts.borders, w))
-        return;
-    if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled tiles need a 1024-byte aligned base
-        if (tid == 0) report(a.err_word, SSD_DEVERR_INTERNAL);
-        return;
-    }
-    if (tid == 0) {
-        for (int i = 0; i < NUM_BARS; ++i) mbar_init(&bar[i], i == Q_EMPTY || i == P_READY0 || i == P_READY1 ? 4 : 1);
-        fence_mbar_init();
-        *dead = 0;
-        *dirty = 0;
-    }
+    // Tensor memory first: the SM only starts its second CTA once the first has given up its right
+    // to allocate more (measured: 3.6 us later when it was allocated after find_run).
     if (warp == kMmaWarp) {
         tmem_alloc(sTmem, kTmemCols);
         tmem_relinquish();
     }
+    if (tid == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmKc);
+        tma_prefetch_desc(&tmVc);
+        tma_prefetch_desc(&tmKn);
+        tma_prefetch_desc(&tmVn);
+        for (int i = 0; i < NUM_BARS; ++i) mbar_init(&bar[i], i == P_READY0 || i == P_READY1 ? 4 : 1);
+        fence_mbar_init();
+        *dead = 0;
+        dirty[0] = dirty[1] = 0;
+    }
+    kvs::Walk w;
+    const bool work =
+        kvs::find_run(a, p.g, kMinUnits, *reinterpret_cast<kvs::FindSmem *>(smem + L::kFind), p.parts.borders, w);
+    const bool aligned = (smem_u32(smem) & 1023u) == 0;  // the swizzled tiles need a 1024-byte aligned base
+    if (!aligned && tid == 0) report(a.err_word, SSD_DEVERR_INTERNAL);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = *sTmem;
     const Waiter wait{dead, a.err_word, p.wait_limit};
 
-    if (warp == kLoadWarp) {
+    if (!work || !aligned) {
+        // nothing to do
+    } else if (warp == kLoadWarp) {
         // ---- loads -----------------------------------------------------------------
         uint32_t slot = 0;  // ring position
         uint32_t items = 0;
@@ -248,10 +257,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             wait(&bar[Q_EMPTY], (items & 1) ^ 1);
             ++items;
             if (!__any_sync(~0u, *dead)) {
-                if (lane == 0) mbar_arrive_expect_tx(&bar[Q_FULL], kHalves * row_tile * 128);
+                if (lane == 0) mbar_arrive_expect_tx(&bar[Q_FULL], kHalves * p.g.rows * 128);
                 __syncwarp();
                 if (lane < kHalves)
-                    tma_load_3d(smem + lane * (kRows * 128), &tmQ, lane * 64, w.h * group, w.q.q0 + w.m * p.tile_tokens,
+                    tma_load_3d(smem + lane * (kRows * 128), &tmQ, lane * 64, w.h * group, w.q.q0 + w.first_token(p.g),
                                 &bar[Q_FULL]);
             }
             for (int t = w.t0; t < w.t1; ++t) {
@@ -262,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 id = id_next;
             }
             load(true, w.t1 - 1, id_before);
-            more = w.next(a, group, row_tile, kKeys);
+            more = w.next(a, p.g);
         }
         if (__any_sync(~0u, *dead)) {  // copies in flight land before the CTA may go
             for (int st = 0; st < kStages; ++st)
@@ -315,11 +324,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                 ++items;
                 for (int t = w.t0; t < w.t1; ++t) {
                     scores();
+                    if (t == w.t1 - 1 && !*dead) mma_commit(&bar[Q_EMPTY]);
                     if (t > w.t0) output(tile - 1, t - 1 == w.t0);
                     ++tile;
                 }
                 output(tile - 1, w.t1 - 1 == w.t0);
-                more = w.next(a, group, row_tile, kKeys);
+                more = w.next(a, p.g);
             }
             mma_commit(&bar[FIN]);  // everything issued is done before the CTA goes
             mbar_wait(&bar[FIN], 0, 20000000ll);
@@ -334,9 +344,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         bool more = true;
         while (more) {
             ++item;
-            const int rows = (int)min((int64_t)row_tile, (int64_t)w.q.n * group - (int64_t)w.m * row_tile);
+            const int rows = w.tokens(p.g) * group, token0 = w.first_token(p.g);
             const bool warp_live = warp * 32 < rows;
-            const int tok = tid < rows ? w.m * p.tile_tokens + tid / group : -1;
+            const int tok = tid < rows ? token0 + (int)(tid * p.group_inv >> 16) : -1;
             const int n_tiles = w.t1 - w.t0;
             float top = -INFINITY, sum = 0.f;
             for (int t = w.t0; t < w.t1; ++t, ++tile) {
@@ -344,7 +354,21 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const bool cached = t < w.cached_tiles;
                 const int limit = cached ? min(kKeys, w.q.c - t * kKeys)
                                          : min(kKeys, w.q.n - (t - w.cached_tiles) * kKeys);
-                const bool partial = !cached || limit < kKeys;
+                // every row sees every key of the tile: cached ones, or for a chain those before the
+                // tile's first token
+                const bool partial = limit < kKeys || (!cached && (a.tree_mask || (t - w.cached_tiles + 1) * kKeys >
+                                                                                      token0 + 1));
+                // The product of the tile before.  Every warp waits for every product once, and before it
+                // lets the next one go: a parity only tells one phase from the next.
+                bool waited = t == w.t0;
+                auto before_done = [&]() {
+                    if (!waited) {
+                        wait(&bar[O_DONE], (tile - 1) & 1);
+                        __syncwarp();
+                        tc_fence_after();
+                        waited = true;
+                    }
+                };
                 wait(&bar[S_FULL0 + (tile & 1)], (tile >> 1) & 1);
                 __syncwarp();
                 tc_fence_after();
@@ -358,9 +382,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                         for (int j = 0; j < 64; ++j)
                             if (!(seen >> j & 1)) s[j] = 0xFF800000u;  // -inf
                     }
-                    float best = __uint_as_float(s[0]);
+                    float b4[4];  // four chains: a single one of 64 would be bound by its latency
 #pragma unroll
-                    for (int j = 1; j < 64; ++j) best = fmaxf(best, __uint_as_float(s[j]));
+                    for (int j = 0; j < 4; ++j) b4[j] = __uint_as_float(s[j]);
+#pragma unroll
+                    for (int j = 4; j < 64; ++j) b4[j & 3] = fmaxf(b4[j & 3], __uint_as_float(s[j]));
+                    const float best = fmaxf(fmaxf(b4[0], b4[1]), fmaxf(b4[2], b4[3]));
                     const float now = best == -INFINITY ? top : fmaxf(top, best * c);
                     const bool grows = now > top + kSlack;  // the first seen key too: top is -inf then
                     if (t == w.t0) {
@@ -369,9 +396,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         const float f = grows ? ex2(top - now) : 1.f;
                         if (grows) top = now;
                         sum *= f;
-                        wait(&bar[O_DONE], (tile - 1) & 1);  // the product of the tile before
-                        __syncwarp();
-                        tc_fence_after();
+                        before_done();
 #pragma unroll 1
                         for (int d = 0; d < D; d += 32) {
                             uint32_t o[32];
@@ -385,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     const float from = top == -INFINITY ? 0.f : top;
                     const float2 c2 = make_float2(c, c), m2 = make_float2(-from, -from);
-                    float2 add = make_float2(0.f, 0.f);
+                    float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     uint32_t pk[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
@@ -393,11 +418,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                         v = fma_f2(v, c2, m2);
                         v.x = ex2(v.x);
                         v.y = ex2(v.y);
-                        add.x += v.x;
-                        add.y += v.y;
+                        add[j & 1] = add_f2(add[j & 1], v);
                         pk[j] = pack_bf16(v.x, v.y);
                     }
-                    sum += add.x + add.y;
+                    sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
                     tmem_st32(s_col, pk);
                     tmem_st_wait();
                 }
@@ -406,77 +430,73 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const int i = t - w.t0;
                     const uint32_t pos = ring + (i == n_tiles - 1 ? 2 * n_tiles - 1 : 2 * i + 2);
                     wait(&bar[KV_FULL0 + pos % kStages], (pos / kStages) & 1);
-                    if (clean_values<D>(smem + L::kRing + (pos % kStages) * L::kTile, limit, !cached, tid)) *dirty = item;
+                    if (clean_values<D>(smem + L::kRing + (pos % kStages) * L::kTile, limit, !cached, tid))
+                        dirty[item & 1] = item;  // a warp is at most one item ahead of another
                     fence_proxy_async_smem();
                 }
+                before_done();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[P_READY0 + (tile & 1)]);
             }
             ring += 2 * n_tiles;
-            // the last two products (a parity tells two phases apart, so one after the other; those
-            // before them were done when the last scores were)
-            if (n_tiles > 1) wait(&bar[O_DONE], tile & 1);
             wait(&bar[O_DONE], (tile - 1) & 1);
             __syncwarp();
             tc_fence_after();
             if (warp_live) {
-                // rows leave through shared memory (the query tile, done with), 32 columns
-                // at a time, so that a warp writes whole runs of each row
+                // A row's thread writes its 64-byte pieces itself: a query tile is free for the next
+                // item's queries as soon as its last scores are done, not after this.
                 const bool whole = w.whole();
-                const bool fix = *dirty == item;
+                const bool fix = dirty[item & 1] == item;
                 const float mul = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;  // a row that saw nothing: zeros
-                const int64_t first_row = (int64_t)w.m * row_tile + warp * 32;
-                const int64_t part = ((int64_t)blockIdx.x * 2 + (w.t0 > 0 ? 0 : 1)) * row_tile + warp * 32;
-                const int live = min(32, rows - warp * 32);
-                float *stage = reinterpret_cast<float *>(smem + warp * (32 * 32 * 4));
+                const int64_t part = ((int64_t)blockIdx.x * 2 + (w.t0 > 0 ? 0 : 1)) * p.g.rows + warp * 32;
+                // output row of the item's row i: (token0 + i / group, head0 + i mod group)
+                const int64_t row0 = (int64_t)(w.q.q0 + token0) * a.nheads + w.h * group;
+                auto out_row = [&](int i) {
+                    const int k = (int)((uint32_t)i * p.group_inv >> 16);
+                    return row0 + (int64_t)k * (a.nheads - group) + i;
+                };
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + out_row(tid) * D;
+                float *sums = p.parts.sums + (part + lane) * D;
 #pragma unroll 1
                 for (int d = 0; d < D; d += 32) {
                     uint32_t o[32];
                     tmem_ld32(lane_base + COL_O + d, o);
                     tmem_ld_wait();
-                    if (fix && tok >= 0) add_nonfinite(a, w, tok, d, o);
-                    __syncwarp();
+                    if (fix && tok >= 0) {  // on copies: what the call takes by address stays in registers otherwise
+                        const kvs::Walk at = w;
+                        uint32_t fixed[32];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float4 v;
-                        v.x = __uint_as_float(o[4 * j]) * mul;
-                        v.y = __uint_as_float(o[4 * j + 1]) * mul;
-                        v.z = __uint_as_float(o[4 * j + 2]) * mul;
-                        v.w = __uint_as_float(o[4 * j + 3]) * mul;
-                        *reinterpret_cast<float4 *>(stage + lane * 32 + ((j ^ (lane & 7)) << 2)) = v;
+                        for (int j = 0; j < 32; ++j) fixed[j] = o[j];
+                        add_nonfinite(a, at, tok, d, fixed);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = fixed[j];
                     }
-                    __syncwarp();
-                    for (int r = lane >> 3; r < live; r += 4) {  // 8 lanes a row
-                        const int j = lane & 7;
-                        const float4 v = *reinterpret_cast<const float4 *>(stage + r * 32 + ((j ^ (r & 7)) << 2));
-                        if (whole) {
-                            const int64_t flat = first_row + r;
-                            const int64_t out_row = (w.q.q0 + flat / group) * a.nheads + w.h * group + flat % group;
-                            uint2 b;
-                            b.x = pack_bf16(v.x, v.y);
-                            b.y = pack_bf16(v.z, v.w);
-                            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + out_row * D + d + 4 * j) = b;
-                        } else {
-                            *reinterpret_cast<float4 *>(p.parts.sums + (part + r) * D + d + 4 * j) = v;
+                    if (tok >= 0 && whole) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            float f[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[j + e]) * mul;
+                            *reinterpret_cast<uint4 *>(out + d + j) =
+                                make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                                           pack_bf16(f[6], f[7]));
                         }
+                    } else if (tok >= 0) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<uint4 *>(sums + d + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                     }
                 }
                 if (tok >= 0) {
                     if (!whole) {
                         p.parts.stats[part + lane] = make_float2(top, sum);
                     } else if (a.lse) {
-                        const int64_t flat = first_row + lane;
-                        a.lse[(w.q.q0 + flat / group) * a.nheads + w.h * group + flat % group] =
-                            sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+                        a.lse[out_row(tid)] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
                     }
                 }
             }
-            fence_proxy_async_smem();  // the query tile's next contents come by TMA
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[Q_EMPTY]);
-            more = w.next(a, group, row_tile, kKeys);
+            more = w.next(a, p.g);
         }
     }
     tc_fence_before();
@@ -487,43 +507,24 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 }
 
-int device_sms() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 152;
-    return sms;
-}
+kvs::Tiling tc_tiling(const kv_attention_args &a) { return kvs::tiling(a, kRows, kKeyShift, kOverhead); }
 
-struct Shape {
-    int group, tile_tokens, row_tile, grid;
-};
-
-Shape shape_of(const kv_attention_args &a) {
-    Shape s;
-    s.group = a.nheads / a.kv_heads;
-    // tokens of a row tile: as many as fit, but no more than a request is said to have, so that
-    // decode steps load and join few rows
-    s.tile_tokens = kRows / s.group;
-    const int hint = a.max_new_tokens > 0 ? a.max_new_tokens : 1;
-    if (hint < s.tile_tokens) s.tile_tokens = hint;
-    s.row_tile = s.tile_tokens * s.group;
-    s.grid = kvs::grid_of(a, s.row_tile, kKeys, kMinUnits, 2 * device_sms());
-    return s;
-}
+int tc_grid(const kv_attention_args &a, const kvs::Tiling &g) { return kvs::grid_of(a, g, kMinUnits, 2 * device_sms()); }
 
 template <int D> cudaError_t launch(const kv_attention_args &a, void *ws, cudaStream_t s) {
-    const Shape sh = shape_of(a);
     TcParams p;
     p.a = a;
-    p.parts = kvs::parts_at(ws, sh.grid, sh.row_tile, D);
-    p.tile_tokens = sh.tile_tokens;
+    p.g = tc_tiling(a);
+    const int grid = tc_grid(a, p.g);
+    p.parts = kvs::parts_at(ws, grid, p.g.rows, D);
+    p.group_inv = (65536u + p.g.heads - 1) / p.g.heads;
     p.box_rows = kKeys;
     while (a.block_size % p.box_rows) p.box_rows /= 2;
     p.wait_limit = a.wait_limit_cycles > 0 ? a.wait_limit_cycles : 2000000000ll;
     const uint64_t H = a.nheads, G = a.kv_heads, T = a.total_tokens;
     CUtensorMap q, kc, vc, kn, vn;
     const bool ok =
-        make_tmap_bf16_3d(&q, a.q, D, H, T, D * 2, (uint64_t)a.q_stride * 2, 64, sh.group, sh.tile_tokens) &&
+        make_tmap_bf16_3d(&q, a.q, D, H, T, D * 2, (uint64_t)a.q_stride * 2, 64, p.g.heads, p.g.tokens) &&
         make_tmap_bf16_3d(&kn, a.k_new, D, G, T, D * 2, (uint64_t)a.k_stride * 2, 64, 1, kKeys) &&
         make_tmap_bf16_3d(&vn, a.v_new, D, G, T, D * 2, (uint64_t)a.v_stride * 2, 64, 1, kKeys) &&
         make_tmap_16bit_4d(&kc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.k_cache, D, G, a.block_size, a.num_blocks, D * 2,
@@ -534,9 +535,9 @@ template <int D> cudaError_t launch(const kv_attention_args &a, void *ws, cudaSt
     constexpr int smem = Layout<D>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(kv_attention_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kv_attention_tc_kernel<D><<<sh.grid, kThreads, smem, s>>>(q, kc, vc, kn, vn, p);
+    kv_attention_tc_kernel<D><<<grid, kThreads, smem, s>>>(q, kc, vc, kn, vn, p);
     e = cudaGetLastError();
-    return e != cudaSuccess ? e : kvs::join_launch(a, p.parts, sh.grid, sh.row_tile, s);
+    return e != cudaSuccess ? e : kvs::join_launch(a, p.parts, grid, p.g, s);
 }
 
 }  // namespace
@@ -550,8 +551,8 @@ bool kv_attention_tc_supported(const kv_attention_args &a) {
 }
 
 size_t kv_attention_tc_workspace(const kv_attention_args &a) {
-    const Shape sh = shape_of(a);
-    return kvs::parts_bytes(sh.grid, sh.row_tile, a.headdim);
+    const kvs::Tiling g = tc_tiling(a);
+    return kvs::parts_bytes(tc_grid(a, g), g.rows, a.headdim);
 }
 
 cudaError_t kv_attention_tc_launch(const kv_attention_args &a, void *ws, cudaStream_t s) {

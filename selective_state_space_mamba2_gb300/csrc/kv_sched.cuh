@@ -1,8 +1,8 @@
 // How kv_tree_attention's work is cut over the GPU (device code shared by its kernels).
 //
-// An item is one tile of query rows of one request and key head: the request's (token, query
-// head) rows are numbered token-major, and tile m holds rows [m * row_tile, (m + 1) * row_tile).
-// An item's keys come in tiles of key_tile: first its cached positions, then the request's new
+// An item is one tile of query rows of one request and key head: `tokens` tokens by the key head's
+// query heads, or, where those are more than a tile's rows, one token by `heads` of them (`parts`
+// tiles per token).  An item's keys come in tiles of 2^key_shift: first its cached positions, then the request's new
 // tokens up to the last one a row of the tile can see.  One (item, key tile) is a unit.  All
 // units in order (request, head, row tile, key tile) are cut into as many equal runs as there
 // are CTAs, so ragged batches fill the GPU and a long cache is split without the host knowing
@@ -16,10 +16,17 @@ namespace kvs {
 
 // Written by a CTA about the item at the start of its run (for the join kernel).
 struct Border {
-    long long lo;          // first unit of the CTA
-    long long item0, item1;  // units of the item that lo falls into
-    int32_t r, h, m, ctas; // the item; number of CTAs that have units
+    long long item0, item1;  // units of the item that the first unit of the run falls into
+    long long total;         // units in all
+    int32_t ctas;            // CTAs they are cut over
+    int32_t token0, tokens;  // rows of the item: first packed token, tokens,
+    int32_t head0, heads;    // first query head, query heads
 };
+
+// First unit of CTA i's run.
+__device__ __forceinline__ long long run_start(long long total, int32_t i, int32_t ctas) {
+    return (long long)((unsigned long long)total * (unsigned long long)i / (unsigned long long)ctas);
+}
 
 struct Request {
     int32_t q0, n, c;  // first packed row, new tokens, cached tokens
@@ -41,108 +48,118 @@ __device__ __forceinline__ Request request(const kv_attention_args &a, int32_t r
     return q;
 }
 
-__device__ __forceinline__ int32_t tiles_of(int32_t n, int32_t tile) { return (n + tile - 1) / tile; }
+struct Tiling {
+    int32_t tokens;     // tokens of a row tile
+    int32_t heads;      // query heads of a row tile (the last part of a token may have fewer)
+    int32_t parts;      // row tiles side by side over a key head's query heads
+    int32_t key_shift;  // key tiles of 2^key_shift
+    int32_t overhead;   // units an item counts besides its key tiles
+    int32_t rows;       // rows a tile is given in the workspace: tokens * heads
+};
 
-// New tokens that row tile m can see: those up to its last row's token, or all with a mask.
-__device__ __forceinline__ int32_t visible_new(const kv_attention_args &a, const Request &q, int32_t group,
-                                               int32_t row_tile, int32_t m) {
-    if (a.tree_mask) return q.n;
-    const int64_t last = min((int64_t)(m + 1) * row_tile, (int64_t)q.n * group) - 1;
-    return (int32_t)(last / group) + 1;
+__host__ __device__ __forceinline__ int32_t ceil_div(int32_t n, int32_t d) { return n / d + (n % d != 0); }
+
+// key tiles of n keys
+__device__ __forceinline__ int32_t tiles_of(const Tiling &g, int32_t n) {
+    return (int32_t)(((uint32_t)n + (1u << g.key_shift) - 1) >> g.key_shift);
 }
 
-__device__ __forceinline__ int32_t row_tiles(const Request &q, int32_t group, int32_t row_tile) {
-    return (int32_t)(((int64_t)q.n * group + row_tile - 1) / row_tile);
+// New tokens that the row tiles of token block b can see: those up to its last token, or all with
+// a mask.
+__device__ __forceinline__ int32_t visible_new(const kv_attention_args &a, const Request &q, const Tiling &g, int32_t b) {
+    return a.tree_mask || q.n - b * g.tokens <= g.tokens ? q.n : (b + 1) * g.tokens;
 }
 
 // Units of one head of a request.
-__device__ __forceinline__ long long units_of(const kv_attention_args &a, const Request &q, int32_t group,
-                                              int32_t row_tile, int32_t key_tile) {
+__device__ __forceinline__ long long units_of(const kv_attention_args &a, const Request &q, const Tiling &g) {
     if (q.n <= 0) return 0;
-    const int32_t tiles = row_tiles(q, group, row_tile);
-    const long long cached = (long long)tiles * tiles_of(q.c, key_tile);
-    if (a.tree_mask) return cached + (long long)tiles * tiles_of(q.n, key_tile);
-    long long sum = cached;
-    for (int32_t m = 0; m < tiles; ++m) sum += tiles_of(visible_new(a, q, group, row_tile, m), key_tile);
-    return sum;
+    const int32_t blocks = ceil_div(q.n, g.tokens);
+    long long sum = (long long)blocks * (g.overhead + tiles_of(g, q.c));
+    if (a.tree_mask) {
+        sum += (long long)blocks * tiles_of(g, q.n);
+    } else {
+        for (int32_t b = 0; b < blocks; ++b) sum += tiles_of(g, visible_new(a, q, g, b));
+    }
+    return sum * g.parts;
 }
 
 // The items of a CTA's run, one after the other.  Every thread that walks them gets the same
 // sequence.
 struct Walk {
     Request q;
-    int32_t r, h, m;        // current item
-    int32_t tiles_m;        // row tiles of the request
+    int32_t r, h, b, part;  // current item: request, key head, token block, part of its heads
+    int32_t blocks;         // token blocks of the request
     int32_t cached_tiles, tiles;  // key tiles: cached ones, and all
     int32_t t0, t1;         // key tiles of the item that fall to this CTA
     int32_t new_seen;       // new tokens the item's keys include
-    long long left;         // units of the run from t0 on
+    int32_t used;           // units of the item in the run
+    long long left;         // units of the run from the item on
 
-    __device__ __forceinline__ void set_item(const kv_attention_args &a, int32_t group, int32_t row_tile,
-                                             int32_t key_tile, int32_t first) {
-        new_seen = visible_new(a, q, group, row_tile, m);
-        cached_tiles = tiles_of(q.c, key_tile);
-        tiles = cached_tiles + tiles_of(new_seen, key_tile);
-        t0 = first;
-        t1 = (int32_t)min((long long)tiles, first + left);
+    // The item's part that starts `first` of its units in.
+    __device__ __forceinline__ void set_item(const kv_attention_args &a, const Tiling &g, int32_t first) {
+        new_seen = visible_new(a, q, g, b);
+        cached_tiles = tiles_of(g, q.c);
+        tiles = cached_tiles + tiles_of(g, new_seen);
+        used = (int32_t)min((long long)(g.overhead + tiles - first), left);
+        t0 = max(0, first - g.overhead);
+        t1 = first + used - g.overhead;
     }
+    __device__ __forceinline__ bool any() const { return t1 > t0; }  // false: the run ends in an item's overhead
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+    // tokens and query heads of the item
+    __device__ __forceinline__ int32_t first_token(const Tiling &g) const { return b * g.tokens; }
+    __device__ __forceinline__ int32_t tokens(const Tiling &g) const { return min(g.tokens, q.n - b * g.tokens); }
+    __device__ __forceinline__ int32_t heads(const Tiling &g, int32_t group) const {
+        return min(g.heads, group - part * g.heads);
+    }
     // To the next item; false at the end of the run.
-    __device__ __forceinline__ bool next(const kv_attention_args &a, int32_t group, int32_t row_tile,
-                                         int32_t key_tile) {
-        left -= t1 - t0;
+    __device__ __forceinline__ bool next(const kv_attention_args &a, const Tiling &g) {
+        left -= used;
         if (left <= 0) return false;
-        if (++m == tiles_m) {
-            m = 0;
-            if (++h == a.kv_heads) {
-                h = 0;
-                do {
-                    if (++r >= a.num_seqs) return false;
-                    q = request(a, r, false);
-                } while (q.n <= 0);
-                tiles_m = row_tiles(q, group, row_tile);
+        if (++part == g.parts) {
+            part = 0;
+            if (++b == blocks) {
+                b = 0;
+                if (++h == a.kv_heads) {
+                    h = 0;
+                    do {
+                        if (++r >= a.num_seqs) return false;
+                        q = request(a, r, false);
+                    } while (q.n <= 0);
+                    blocks = ceil_div(q.n, g.tokens);
+                }
             }
         }
-        set_item(a, group, row_tile, key_tile, 0);
-        return true;
+        set_item(a, g, 0);
+        return any();
     }
 };
 
 struct FindSmem {
     unsigned long long sum[32];
-    long long base;
+    long long base, per_head;
+    Request q;
     int32_t r;
 };
 
 // Called by all threads of the CTA (blockDim.x a multiple of 32): its run, or false when it has
-// none.  min_units: a run is at least that long while there are fewer CTAs' worth of units.
-__device__ __forceinline__ bool find_run(const kv_attention_args &a, int32_t group, int32_t row_tile,
-                                         int32_t key_tile, int32_t min_units, FindSmem &sm, Border *borders,
-                                         Walk &w) {
+// none.  min_units: a run is at least about that long.
+__device__ __forceinline__ bool find_run(const kv_attention_args &a, const Tiling &g, int32_t min_units,
+                                         FindSmem &sm, Border *borders, Walk &w) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nwarp = nthr >> 5;
     const int S = a.num_seqs;
-    unsigned long long total = 0;
-    for (int r = tid; r < S; r += nthr)
-        total += (unsigned long long)units_of(a, request(a, r, blockIdx.x == 0), group, row_tile, key_tile);
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
-    if (lane == 0) sm.sum[warp] = total;
-    __syncthreads();
-    total = 0;
-    for (int i = 0; i < nwarp; ++i) total += sm.sum[i];
-    total *= (unsigned long long)a.kv_heads;
-    const unsigned long long most = (total + min_units - 1) / min_units;
-    const int ctas = (int)(most < gridDim.x ? most : gridDim.x);
-    if ((int)blockIdx.x >= ctas) {
-        if (blockIdx.x == 0 && tid == 0) borders[0].ctas = 0;
-        return false;
-    }
-    const long long lo = (long long)(total * blockIdx.x / ctas), hi = (long long)(total * (blockIdx.x + 1) / ctas);
-
-    unsigned long long carry = 0;
-    for (int base = 0; base < S; base += nthr) {
+    const unsigned long long heads = (unsigned long long)a.kv_heads;
+    // units of the requests, a CTA's worth of them at a time, summed over all
+    auto scan = [&](int base, bool tell, Request &q, unsigned long long &per_head, unsigned long long &before,
+                    unsigned long long &all) {
         const int r = base + tid;
-        unsigned long long own = 0;
-        if (r < S) own = (unsigned long long)(units_of(a, request(a, r, false), group, row_tile, key_tile) * a.kv_heads);
+        q.n = 0;
+        per_head = 0;
+        if (r < S) {
+            q = request(a, r, tell);
+            per_head = (unsigned long long)units_of(a, q, g);
+        }
+        const unsigned long long own = per_head * heads;
         unsigned long long sum = own;
         for (int o = 1; o < 32; o <<= 1) {
             const unsigned long long v = __shfl_up_sync(~0u, sum, o);
@@ -151,88 +168,137 @@ __device__ __forceinline__ bool find_run(const kv_attention_args &a, int32_t gro
         __syncthreads();
         if (lane == 31) sm.sum[warp] = sum;
         __syncthreads();
-        unsigned long long before = carry + sum - own;
+        before = sum - own;
+        all = 0;
         for (int i = 0; i < nwarp; ++i) {
             if (i < warp) before += sm.sum[i];
-            carry += sm.sum[i];
+            all += sm.sum[i];
         }
-        if (own && before <= (unsigned long long)lo && (unsigned long long)lo < before + own) {
-            sm.r = r;
-            sm.base = (long long)before;
+    };
+    Request q;
+    unsigned long long per_head, before, all, total = 0;
+    for (int base = 0; base < S; base += nthr) {
+        scan(base, blockIdx.x == 0, q, per_head, before, all);
+        total += all;
+    }
+    const unsigned long long most = (total + min_units - 1) / min_units;
+    const int ctas = (int)(most < gridDim.x ? most : gridDim.x);
+    if ((int)blockIdx.x >= ctas) {
+        if (blockIdx.x == 0 && tid == 0) borders[0].ctas = 0;
+        return false;
+    }
+    const unsigned long long lo = run_start(total, blockIdx.x, ctas), hi = run_start(total, blockIdx.x + 1, ctas);
+    unsigned long long carry = 0;
+    for (int base = 0; base < S; base += nthr) {
+        if (S > nthr) scan(base, false, q, per_head, before, all);  // else the scan above still holds
+        if (q.n > 0 && carry + before <= lo && lo - (carry + before) < per_head * heads) {
+            sm.r = base + tid;
+            sm.q = q;
+            sm.base = (long long)(carry + before);
+            sm.per_head = (long long)per_head;
         }
-        if (carry > (unsigned long long)lo) break;
+        carry += all;
+        if (carry > lo) break;
     }
     __syncthreads();
 
     w.r = sm.r;
-    w.q = request(a, w.r, false);
-    w.tiles_m = row_tiles(w.q, group, row_tile);
-    w.left = hi - lo;
-    const long long per_head = units_of(a, w.q, group, row_tile, key_tile);
-    long long off = lo - sm.base;
-    w.h = (int32_t)(off / per_head);
-    off -= w.h * per_head;
-    w.m = 0;
-    const int32_t cached = tiles_of(w.q.c, key_tile);
-    while (true) {
-        const long long here = cached + tiles_of(visible_new(a, w.q, group, row_tile, w.m), key_tile);
-        if (off < here) break;
-        off -= here;
-        ++w.m;
+    w.q = sm.q;
+    w.blocks = ceil_div(w.q.n, g.tokens);
+    w.left = (long long)(hi - lo);
+    long long off = (long long)lo - sm.base;
+    w.h = (int32_t)(off / sm.per_head);
+    off -= w.h * sm.per_head;
+    w.b = 0;
+    const int32_t fixed = g.overhead + tiles_of(g, w.q.c);
+    int32_t here;  // units of a token block's part
+    if (a.tree_mask) {
+        here = fixed + tiles_of(g, w.q.n);
+        w.b = (int32_t)(off / ((long long)here * g.parts));
+        off -= (long long)w.b * here * g.parts;
+    } else {
+        while (true) {
+            here = fixed + tiles_of(g, visible_new(a, w.q, g, w.b));
+            if (off < (long long)here * g.parts) break;
+            off -= (long long)here * g.parts;
+            ++w.b;
+        }
     }
-    w.set_item(a, group, row_tile, key_tile, (int32_t)off);
+    w.part = g.parts == 1 ? 0 : (int32_t)off / here;
+    const int32_t first = (int32_t)off - w.part * here;
+    w.set_item(a, g, first);
     if (tid == 0) {
         Border b;
-        b.lo = lo;
-        b.item0 = lo - off;
-        b.item1 = b.item0 + w.tiles;
-        b.r = w.r, b.h = w.h, b.m = w.m, b.ctas = ctas;
+        b.item0 = (long long)lo - first;
+        b.item1 = b.item0 + g.overhead + w.tiles;
+        b.total = (long long)total;
+        b.ctas = ctas;
+        b.token0 = w.q.q0 + w.first_token(g);
+        b.tokens = w.tokens(g);
+        const int32_t group = a.nheads / a.kv_heads;
+        b.heads = w.heads(g, group);
+        b.head0 = w.h * group + w.part * g.heads;
         borders[blockIdx.x] = b;
     }
-    return true;
+    return w.any();
 }
 
 // ---- workspace: Border [grid], then per CTA two parts (0: the item at the start of the run was
-// begun by another CTA; 1: an item begun here and not finished), each sums [row_tile, D] and
-// (maximum, sum) pairs [row_tile] ----
+// begun by another CTA; 1: an item begun here and not finished), each sums [rows, D] and
+// (maximum, sum) pairs [rows] ----
 struct Parts {
     Border *borders;
-    float *sums;   // [grid][2][row_tile][D]
-    float2 *stats; // [grid][2][row_tile]: maximum in the base-2 domain, sum of weights
+    float *sums;   // [grid][2][rows][D]
+    float2 *stats; // [grid][2][rows]: maximum in the base-2 domain, sum of weights
 };
 
 __host__ __device__ inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-inline size_t parts_bytes(int grid, int row_tile, int D) {
-    return up256(sizeof(Border) * (size_t)grid) + up256((size_t)grid * 2 * row_tile * D * 4) +
-           up256((size_t)grid * 2 * row_tile * 8);
+inline size_t parts_bytes(int grid, int rows, int D) {
+    return up256(sizeof(Border) * (size_t)grid) + up256((size_t)grid * 2 * rows * D * 4) + up256((size_t)grid * 2 * rows * 8);
 }
 
-inline Parts parts_at(void *ws, int grid, int row_tile, int D) {
+inline Parts parts_at(void *ws, int grid, int rows, int D) {
     char *p = static_cast<char *>(ws);
     Parts o;
     o.borders = reinterpret_cast<Border *>(p);
     p += up256(sizeof(Border) * (size_t)grid);
     o.sums = reinterpret_cast<float *>(p);
-    p += up256((size_t)grid * 2 * row_tile * D * 4);
+    p += up256((size_t)grid * 2 * rows * D * 4);
     o.stats = reinterpret_cast<float2 *>(p);
     return o;
 }
 
-// Joins the parts of the items that borders cut (one kernel, defined in kv_attention_simt.cu).
-cudaError_t join_launch(const kv_attention_args &a, const Parts &p, int grid, int row_tile, cudaStream_t s);
+// How a kernel with `rows` rows and 2^key_shift keys to a tile cuts these heads.
+inline Tiling tiling(const kv_attention_args &a, int rows, int key_shift, int overhead) {
+    const int group = a.nheads / a.kv_heads;
+    Tiling g;
+    g.key_shift = key_shift;
+    g.overhead = overhead;
+    if (group > rows) {
+        g.tokens = 1, g.heads = rows, g.parts = ceil_div(group, rows);
+    } else {
+        // as many tokens as fit, but no more than a request is said to have, so that decode steps
+        // load and join few rows
+        g.tokens = rows / group, g.heads = group, g.parts = 1;
+        const int hint = a.max_new_tokens > 0 ? a.max_new_tokens : 1;
+        if (hint < g.tokens) g.tokens = hint;
+    }
+    g.rows = g.tokens * g.heads;
+    return g;
+}
 
 // CTAs to launch: `most` at most, fewer where the host's bounds say that there cannot be as many
 // units.
-inline int grid_of(const kv_attention_args &a, int row_tile, int key_tile, int min_units, int most) {
-    const int64_t group = a.nheads / a.kv_heads;
-    const int64_t rows = (int64_t)a.total_tokens * group;
-    const int64_t tiles_m = rows / row_tile + (a.num_seqs < a.total_tokens ? a.num_seqs : a.total_tokens);
-    const int64_t keys = ((int64_t)a.table_cols * a.block_size + key_tile - 1) / key_tile +
-                         ((int64_t)a.total_tokens + key_tile - 1) / key_tile;
-    const double units = (double)tiles_m * (double)keys * a.kv_heads / min_units;
+inline int grid_of(const kv_attention_args &a, const Tiling &g, int min_units, int most) {
+    const double blocks = (double)a.total_tokens / g.tokens + (a.num_seqs < a.total_tokens ? a.num_seqs : a.total_tokens);
+    const double keys = ((double)a.table_cols * a.block_size + a.total_tokens) / (1 << g.key_shift) + 2;
+    const double units = blocks * g.parts * (g.overhead + keys) * a.kv_heads / min_units;
     return units < (double)most ? (int)(units < 1 ? 1 : units + 1) : most;
 }
+
+// Joins the parts of the items that borders cut (one kernel, defined in kv_attention_simt.cu).
+cudaError_t join_launch(const kv_attention_args &a, const Parts &p, int grid, const Tiling &g, cudaStream_t s);
 
 }  // namespace kvs
 }  // namespace ssd

@@ -12,12 +12,16 @@ namespace {
 // n = x w / sqrt(mean(x^2) + eps) and the rotation of n are one linear map of x once the mean is
 // known: y_e = r (a_e x_e + b_e x_p), with p the other entry of e's pair, a_e = w_e cos and
 // b_e = -+ w_p sin (a_e = w_e, b_e = 0 beyond the rotated part).  a and b depend on the token and
-// the weights alone, so a lane computes them once for its 8 entries and reuses them for every
-// head; a row costs 8 squares, a shuffle reduction and 16 multiply-adds per lane.
+// the weights alone, so a lane computes them once per token for its 8 entries and reuses them for
+// every head; a row costs 8 squares, a shuffle reduction and 16 multiply-adds per lane.  CTAs walk
+// over tokens, with the weights in shared memory and the next token's position fetched ahead.
 
-enum { kPairInside = 0, kPairLane = 1, kPairLoad = 2 };  // where a pair's other entry is
+// Where a pair's other entry is: among the lane's own 8 (interleaved), in another lane (pairs half a
+// rotation apart, whole lanes of entries), or anywhere (read again from memory).
+enum { kPairInside = 0, kPairLane = 1, kPairLoad = 2 };
 
 constexpr int kQkThreads = 128;
+constexpr int kQkCtasPerSm = 5;
 
 template <typename T> struct Row8;
 template <> struct Row8<__nv_bfloat16> {
@@ -78,152 +82,238 @@ template <> struct Row8<float> {
     }
 };
 
-// One CTA per token; a row (head) is `width` lanes, 8 entries each (width: headdim / 8 rounded up
-// to a power of two).  W heads of a lane group are loaded before the first is computed.
+// A lane's 8 cosines and sines (the sine with its sign in y_e); 1 and 0 beyond the rotated part.
+template <int PAIR>
+__device__ __forceinline__ void angles(const kv_qk_args &a, int32_t pos, int e0, float (&cs)[8], float (&sn)[8]) {
+    const int R = a.rotary_dim, half = R / 2;
+    const float *row = a.cos_sin + (int64_t)pos * R;
+    if (PAIR == kPairLoad) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = e0 + i;
+            cs[i] = 1.f, sn[i] = 0.f;
+            if (e < R) {
+                const bool low = a.interleaved ? (e & 1) == 0 : e < half;
+                const int idx = a.interleaved ? e >> 1 : (low ? e : e - half);
+                cs[i] = row[idx];
+                sn[i] = low ? -row[half + idx] : row[half + idx];
+            }
+        }
+    } else if (e0 < R) {  // 16-byte pieces; R is a multiple of 8 (inside) or 16 (lane)
+        if (PAIR == kPairInside) {
+            const float4 c = *reinterpret_cast<const float4 *>(row + e0 / 2);
+            const float4 s = *reinterpret_cast<const float4 *>(row + half + e0 / 2);
+            const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                cs[2 * i] = cs[2 * i + 1] = cc[i];
+                sn[2 * i] = -ss[i], sn[2 * i + 1] = ss[i];
+            }
+        } else {
+            const bool low = e0 < half;
+            const float4 *c = reinterpret_cast<const float4 *>(row + (low ? e0 : e0 - half));
+            const float4 *s = reinterpret_cast<const float4 *>(row + half + (low ? e0 : e0 - half));
+            const float4 c0 = c[0], c1 = c[1], s0 = s[0], s1 = s[1];
+            const float f = low ? -1.f : 1.f;
+            cs[0] = c0.x, cs[1] = c0.y, cs[2] = c0.z, cs[3] = c0.w, cs[4] = c1.x, cs[5] = c1.y, cs[6] = c1.z, cs[7] = c1.w;
+            sn[0] = f * s0.x, sn[1] = f * s0.y, sn[2] = f * s0.z, sn[3] = f * s0.w;
+            sn[4] = f * s1.x, sn[5] = f * s1.y, sn[6] = f * s1.z, sn[7] = f * s1.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
+    }
+}
+
+// A row (head) is `width` lanes, 8 entries each (width: headdim / 8 rounded up to a power of two).  A
+// lane group loads its first key and value row and W query rows before it computes the first.
 template <typename T, int PAIR>
-__global__ void __launch_bounds__(kQkThreads) kv_qk_kernel(const kv_qk_args a, const int width) {
-    constexpr int W = 4;
-    const int t = blockIdx.x;
+__global__ void __launch_bounds__(kQkThreads, kQkCtasPerSm) kv_qk_kernel(const kv_qk_args a, const int width) {
+    constexpr int W = (PAIR == kPairLoad ? 2 : 4) / (sizeof(T) == 4 ? 2 : 1);  // query rows in flight
+    __shared__ __align__(16) float weights[4][256];  // of q's entries and their partners, of k's
     const int D = a.headdim, R = a.rotary_dim, half = R / 2;
     const int sub = threadIdx.x & (width - 1), group = threadIdx.x / width, groups = kQkThreads / width;
     const int e0 = sub * 8;
     const bool live = e0 < D;
+    const bool want_k = a.k_out || a.k_cache;
 
-    int32_t pos = 0;
-    if (R > 0) {
-        pos = a.positions[t];
-        if (pos < 0 || pos >= a.max_position) {  // the same for the whole CTA
-            if (threadIdx.x == 0) report(a.err_word, SSD_DEVERR_METADATA);
-            return;
-        }
-    }
-    T *kc = nullptr, *vc = nullptr;
-    if (a.k_cache) {
-        const int32_t slot = a.slots[t];
-        if (slot >= 0) {
-            const int32_t blk = slot / a.block_size;
-            if (blk >= a.num_blocks) {
-                if (threadIdx.x == 0) report(a.err_word, SSD_DEVERR_SLOT);
-            } else {
-                const int64_t at = (int64_t)blk * a.cache_block_stride +
-                                   (int64_t)(slot - blk * a.block_size) * a.kv_heads * D;
-                kc = static_cast<T *>(a.k_cache) + at;
-                vc = static_cast<T *>(a.v_cache) + at;
-            }
-        }
-    }
-
-    // this lane's cosines and sines, and which entry is each one's partner
-    float cs[8], sn[8];
-    int partner[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    int src_lane = 0;  // kPairLane: whose entries are the partners of this lane's
+    if (PAIR == kPairLane && e0 < R) src_lane = (e0 < half ? e0 + half : e0 - half) / 8;
+    auto partner = [&](int i) -> int {
         const int e = e0 + i;
-        cs[i] = 1.f, sn[i] = 0.f, partner[i] = e;
-        if (e < R) {
-            const bool low = PAIR == kPairInside ? (e & 1) == 0 : e < half;
-            const int idx = PAIR == kPairInside ? e >> 1 : (low ? e : e - half);
-            const float *row = a.cos_sin + (int64_t)pos * R;
-            cs[i] = row[idx];
-            sn[i] = low ? -row[half + idx] : row[half + idx];
-            partner[i] = PAIR == kPairInside ? e ^ 1 : (low ? e + half : e - half);
-        }
-    }
-    const int src_lane = PAIR == kPairLane ? min(partner[0] / 8, width - 1) : 0;
-
-    for (int part = 0; part < 2; ++part) {
-        const bool is_q = part == 0;
-        const int heads = is_q ? a.nheads : a.kv_heads;
-        T *out = static_cast<T *>(is_q ? a.q_out : a.k_out);
-        if (!is_q && !out && !kc) break;
-        const float *w = is_q ? a.q_weight : a.k_weight;
-        float fa[8], fb[8];
+        if (e >= R) return e;
+        if (PAIR == kPairInside || (PAIR == kPairLoad && a.interleaved)) return e ^ 1;
+        return e < half ? e + half : e - half;
+    };
+    if (threadIdx.x < width && live) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            fa[i] = cs[i], fb[i] = sn[i];
-            if (w && live) {
-                fa[i] *= w[e0 + i];
-                fb[i] *= w[partner[i]];
-            }
-        }
-        const T *in = static_cast<const T *>(is_q ? a.q : a.k) + (int64_t)t * (is_q ? a.q_stride : a.k_stride);
-        for (int h0 = 0; h0 < heads; h0 += groups * W) {
-            Row8<T> x[W];
-            float other[PAIR == kPairLoad ? W : 1][8];
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                const int h = h0 + j * groups + group;
-                if (h < heads && live) {
-                    x[j].load(in + h * D + e0);
-                    if (PAIR == kPairLoad) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) other[j][i] = to_f32(in[h * D + partner[i]]);
-                    }
-                } else {
-                    float z[8] = {};
-                    x[j].set(z);
-                    if (PAIR == kPairLoad) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) other[j][i] = 0.f;
-                    }
-                }
-            }
-            if (PAIR == kPairLoad) __syncwarp();  // in place: partners are read before a row is overwritten
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                const int h = h0 + j * groups + group;
-                float v[8], y[8];
-                x[j].get(v);
-                float r = 1.f;
-                if (w) {
-                    float ss = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-                    for (int o = width / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-                    r = rsqrtf(ss / (float)D + a.eps);
-                }
-                float p[8];
-                if (PAIR == kPairInside) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) p[i] = v[i ^ 1];
-                } else if (PAIR == kPairLane) {
-                    x[j].from_lane(src_lane, width).get(p);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) p[i] = other[j][i];
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    // beyond the rotated part the partner is the entry itself, and is left out
-                    const float turned = e0 + i < R ? fb[i] * p[i] : 0.f;
-                    y[i] = r * fmaf(fa[i], v[i], turned);
-                }
-                if (h < heads && live) {
-                    Row8<T> o;
-                    o.set(y);
-                    if (out) o.store(out + ((int64_t)t * heads + h) * D + e0);
-                    if (!is_q && kc) o.store(kc + h * D + e0);
-                }
-            }
+            weights[0][e0 + i] = a.q_weight ? a.q_weight[e0 + i] : 1.f;
+            weights[1][e0 + i] = a.q_weight ? a.q_weight[partner(i)] : 1.f;
+            weights[2][e0 + i] = a.k_weight ? a.k_weight[e0 + i] : 1.f;
+            weights[3][e0 + i] = a.k_weight ? a.k_weight[partner(i)] : 1.f;
         }
     }
-    if (vc && live) {
-        const T *in = static_cast<const T *>(a.v) + (int64_t)t * a.v_stride;
-        for (int h = group; h < a.kv_heads; h += groups) {
-            Row8<T> x;
-            x.load(in + h * D + e0);
-            x.store(vc + h * D + e0);
+    __syncthreads();
+    // a and b of this lane's entries for q (which = 0) or k (2)
+    auto factors = [&](int which, const float (&cs)[8], const float (&sn)[8], float (&fa)[8], float (&fb)[8]) {
+        if (!live) return;
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+            const float4 w = *reinterpret_cast<const float4 *>(&weights[which][e0 + i]);
+            const float4 o = *reinterpret_cast<const float4 *>(&weights[which + 1][e0 + i]);
+            fa[i] = cs[i] * w.x, fa[i + 1] = cs[i + 1] * w.y, fa[i + 2] = cs[i + 2] * w.z, fa[i + 3] = cs[i + 3] * w.w;
+            fb[i] = sn[i] * o.x, fb[i + 1] = sn[i + 1] * o.y, fb[i + 2] = sn[i + 2] * o.z, fb[i + 3] = sn[i + 3] * o.w;
         }
+    };
+    const float inv_d = 1.f / (float)D;
+
+    auto fetch = [&](Row8<T> &x, float (&other)[8], const T *in, bool on) {
+        if (on && live) {
+            x.load(in + e0);
+            if (PAIR == kPairLoad) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) other[i] = to_f32(in[partner(i)]);
+            }
+        } else {
+            const float z[8] = {};
+            x.set(z);
+            if (PAIR == kPairLoad) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) other[i] = 0.f;
+            }
+        }
+    };
+    // one row: norm and rotation
+    auto turn = [&](const Row8<T> &x, const float (&other)[8], const float (&fa)[8], const float (&fb)[8], bool norm) {
+        float v[8], p[8], y[8];
+        x.get(v);
+        float r = 1.f;
+        if (norm) {
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+            for (int o = width / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+            r = rsqrtf(fmaf(ss, inv_d, a.eps));
+        }
+        if (PAIR == kPairInside) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = v[i ^ 1];
+        } else if (PAIR == kPairLane) {
+            x.from_lane(src_lane, width).get(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = other[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // beyond the rotated part there is no partner: left out, whatever it holds
+            const float turned = e0 + i < R ? fb[i] * p[i] : 0.f;
+            y[i] = r * fmaf(fa[i], v[i], turned);
+        }
+        Row8<T> o;
+        o.set(y);
+        return o;
+    };
+
+    int t = blockIdx.x;
+    int32_t pos = R > 0 ? a.positions[t] : 0;
+    int32_t slot = a.k_cache ? a.slots[t] : -1;
+    while (true) {
+        const int t_next = t + gridDim.x;
+        const bool more = t_next < a.total_tokens;
+        int32_t pos_next = 0, slot_next = -1;
+        if (more) {
+            if (R > 0) pos_next = a.positions[t_next];
+            if (a.k_cache) slot_next = a.slots[t_next];
+        }
+        if (R > 0 && (pos < 0 || pos >= a.max_position)) {  // the same for the whole CTA
+            if (threadIdx.x == 0) report(a.err_word, SSD_DEVERR_METADATA);
+        } else {
+            T *kc = nullptr, *vc = nullptr;
+            if (slot >= 0) {
+                const int32_t blk = slot / a.block_size;
+                if (blk >= a.num_blocks) {
+                    if (threadIdx.x == 0) report(a.err_word, SSD_DEVERR_SLOT);
+                } else {
+                    const int64_t at = (int64_t)blk * a.cache_block_stride +
+                                       (int64_t)(slot - blk * a.block_size) * a.kv_heads * D;
+                    kc = static_cast<T *>(a.k_cache) + at;
+                    vc = static_cast<T *>(a.v_cache) + at;
+                }
+            }
+            const T *qin = static_cast<const T *>(a.q) + (int64_t)t * a.q_stride;
+            const T *kin = static_cast<const T *>(a.k) + (int64_t)t * a.k_stride;
+            const T *vin = static_cast<const T *>(a.v) + (int64_t)t * a.v_stride;
+            constexpr int kOther = PAIR == kPairLoad ? W : 1;
+            Row8<T> xq[W], xk, xv;
+            float oq[kOther][8], ok[8];
+            fetch(xk, ok, kin + group * D, want_k && group < a.kv_heads);
+            if (vc && live && group < a.kv_heads) xv.load(vin + group * D + e0);
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                const int h = group + j * groups;
+                fetch(xq[j], oq[PAIR == kPairLoad ? j : 0], qin + h * D, h < a.nheads);
+            }
+            float cs[8], sn[8], fa[8] = {}, fb[8] = {};
+            angles<PAIR>(a, pos, e0, cs, sn);
+            if (PAIR == kPairLoad) __syncwarp();  // in place: partners are read before a row is overwritten
+
+            if (want_k) {
+                factors(2, cs, sn, fa, fb);
+                T *out = static_cast<T *>(a.k_out) + (int64_t)t * a.kv_heads * D;
+                for (int h0 = 0; h0 < a.kv_heads; h0 += groups) {
+                    const int h = h0 + group;
+                    const bool on = h < a.kv_heads;
+                    if (h0 > 0) {
+                        fetch(xk, ok, kin + h * D, on);
+                        if (PAIR == kPairLoad) __syncwarp();
+                    }
+                    const Row8<T> o = turn(xk, ok, fa, fb, a.k_weight != nullptr);
+                    if (on && live) {
+                        if (a.k_out) o.store(out + h * D + e0);
+                        if (kc) o.store(kc + h * D + e0);
+                    }
+                }
+            }
+            if (vc && live)
+                for (int h = group; h < a.kv_heads; h += groups) {
+                    if (h != group) xv.load(vin + h * D + e0);
+                    xv.store(vc + h * D + e0);
+                }
+            factors(0, cs, sn, fa, fb);
+            T *out = static_cast<T *>(a.q_out) + (int64_t)t * a.nheads * D;
+            for (int h0 = 0; h0 < a.nheads; h0 += groups * W) {
+                if (h0 > 0) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) {
+                        const int h = h0 + group + j * groups;
+                        fetch(xq[j], oq[PAIR == kPairLoad ? j : 0], qin + h * D, h < a.nheads);
+                    }
+                    if (PAIR == kPairLoad) __syncwarp();
+                }
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    const int h = h0 + group + j * groups;
+                    const Row8<T> o = turn(xq[j], oq[PAIR == kPairLoad ? j : 0], fa, fb, a.q_weight != nullptr);
+                    if (h < a.nheads && live) o.store(out + h * D + e0);
+                }
+            }
+        }
+        if (!more) break;
+        t = t_next, pos = pos_next, slot = slot_next;
     }
 }
 
 template <typename T> cudaError_t launch_qk(const kv_qk_args &a, cudaStream_t s) {
     int width = 1;
     while (width * 8 < a.headdim) width *= 2;
-    const dim3 grid((unsigned)a.total_tokens);
-    if (a.interleaved)
+    const int most = kQkCtasPerSm * device_sms();
+    const dim3 grid((unsigned)(a.total_tokens < most ? a.total_tokens : most));
+    const bool pieces = (reinterpret_cast<uintptr_t>(a.cos_sin) & 15u) == 0;  // 16-byte loads of the angles
+    if (a.interleaved && a.rotary_dim % 8 == 0 && pieces)
         kv_qk_kernel<T, kPairInside><<<grid, kQkThreads, 0, s>>>(a, width);
-    else if (a.rotary_dim % 16 == 0)
+    else if (!a.interleaved && a.rotary_dim % 16 == 0 && pieces)
         kv_qk_kernel<T, kPairLane><<<grid, kQkThreads, 0, s>>>(a, width);
     else
         kv_qk_kernel<T, kPairLoad><<<grid, kQkThreads, 0, s>>>(a, width);
