@@ -47,6 +47,7 @@ __global__ void __launch_bounds__(kThreads) kv_attention_simt_kernel(const kv_at
     float *sq = smem, *sk = sq + kRowTile * pitch, *sv = sk + kKeyTile * pitch, *sp = sv + kKeyTile * pitch;
     const int tid = threadIdx.x, row = tid >> 3, sub = tid & 7;
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join kernel may be set up
     kvs::Walk w;
     if (!kvs::find_run(a, g, kMinUnits, find, parts.borders, w)) return;
     const float c = a.scale * kLog2e;
@@ -195,31 +196,26 @@ __global__ void __launch_bounds__(kThreads) kv_attention_simt_kernel(const kv_at
 
 // ---- joining the parts of a cut item -----------------------------------------------
 //
-// CTA b looks at the border before CTA b's run.  If it cuts an item's key tiles and is the first
-// border to do so, this CTA adds up the item's parts: the one of CTA b - 1 (begun there) and those
-// of b and the CTAs after it while their runs start inside the item:
+// One row of CTAs per border: where the border before CTA b's run is the first to cut an item, its
+// parts are added up, that of CTA b - 1 (which began the item) and those of the CTAs from b on:
 //   out = sum_i 2^(m_i - m) O_i / L,  L = sum_i 2^(m_i - m) l_i,  m = max_i m_i.
-// A warp per row; the parts' factors are worked out a lane each, so that the loads of the sums
-// depend on nothing but one another's order in the sum.
+// Bound by the latency of three dependent reads (border, statistics, sums).  kSplit warps share a
+// row's parts: 4 for decode's few rows, whose items may have dozens of parts (65536 keys of one
+// request: 38), 1 for prompts' many rows of two or three parts.
 constexpr int kJoinThreads = 128;
-constexpr int kJoinRows = 4;  // rows of an item joined by one CTA, a warp each
+constexpr int kSplitRows = 16;  // tiles of at most so many rows are joined by 4 warps a row
 
-template <typename T, int NV>  // NV: 128-float pieces of a row
+template <typename T, int NV, int kSplit>  // NV: 128-float pieces of a row
 __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const kv_attention_args a, const kvs::Parts parts,
                                                                const kvs::Tiling g) {
+    __shared__ float part_acc[kSplit][NV * 128];
+    __shared__ float part_sum[kSplit];
+    const int D = a.headdim, b = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = kSplit > 1 ? blockIdx.y : blockIdx.y * 4 + warp, share = kSplit > 1 ? warp : 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are complete
-    const int b = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int ctas = parts.borders[0].ctas;
-    if (b >= ctas) return;
     const kvs::Border me = parts.borders[b];
-    const long long tile0 = me.item0 + g.overhead;  // unit of the item's first key tile
-    if (kvs::run_start(me.total, b, ctas) <= tile0 || kvs::run_start(me.total, b - 1, ctas) > tile0) return;
-    const int row = blockIdx.y * kJoinRows + warp;
-    if (row >= me.tokens * me.heads) return;
-    // the last CTA with a part: the last one whose run starts before the item's end
-    int last = (int)min((long long)ctas - 1, me.item1 * ctas / me.total + 1);
-    while (kvs::run_start(me.total, last, ctas) >= me.item1) --last;
-    const int D = a.headdim, n = last - b + 2;
+    const int n = me.parts;
+    if (n == 0 || row >= me.tokens * me.heads) return;
     // part k: of CTA b - 1 + k
     auto part_row = [&](int k) { return ((int64_t)(b - 1 + k) * 2 + (k == 0 ? 1 : 0)) * g.rows + row; };
     float top = -INFINITY;
@@ -234,42 +230,80 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const kv_attentio
     }
     const float from = top == -INFINITY ? 0.f : top;
     float sum = 0.f, acc[NV][4] = {};
-    for (int k0 = 0; k0 < n; k0 += 32) {
+    // parts share, share + kSplit, ...: 32 a round, a lane each for the factors
+    for (int k0 = share; k0 < n; k0 += 32 * kSplit) {
+        const int mine = k0 + lane * kSplit;
         float f = 0.f;
-        if (k0 + lane < n) {
-            const float2 st = parts.stats[part_row(k0 + lane)];
+        if (mine < n) {
+            const float2 st = parts.stats[part_row(mine)];
             f = exp2f(st.x - from);
             sum = fmaf(f, st.y, sum);
         }
-        const int here = min(32, n - k0);
-#pragma unroll 8
-        for (int k = 0; k < here; ++k) {
-            const float fk = __shfl_sync(~0u, f, k);
-            const float *src = parts.sums + part_row(k0 + k) * D;
+        const int here = min(32, (n - k0 + kSplit - 1) / kSplit);
+        for (int i0 = 0; i0 < here; i0 += 4) {  // four loads in flight, the last ones repeated with factor 0
+            float4 v[4][NV];
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int e = 128 * j + 4 * lane;
-                if (e < D) {
-                    const float4 v = *reinterpret_cast<const float4 *>(src + e);
-                    acc[j][0] = fmaf(fk, v.x, acc[j][0]);
-                    acc[j][1] = fmaf(fk, v.y, acc[j][1]);
-                    acc[j][2] = fmaf(fk, v.z, acc[j][2]);
-                    acc[j][3] = fmaf(fk, v.w, acc[j][3]);
+            for (int i = 0; i < 4; ++i) {
+                const float *src = parts.sums + part_row(k0 + min(i0 + i, here - 1) * kSplit) * D;
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    v[i][j] = 128 * j + 4 * lane < D ? *reinterpret_cast<const float4 *>(src + 128 * j + 4 * lane)
+                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float fk = __shfl_sync(~0u, f, i0 + i < here ? i0 + i : 0);
+                if (i0 + i < here) {
+#pragma unroll
+                    for (int j = 0; j < NV; ++j) {
+                        acc[j][0] = fmaf(fk, v[i][j].x, acc[j][0]);
+                        acc[j][1] = fmaf(fk, v[i][j].y, acc[j][1]);
+                        acc[j][2] = fmaf(fk, v[i][j].z, acc[j][2]);
+                        acc[j][3] = fmaf(fk, v[i][j].w, acc[j][3]);
+                    }
                 }
             }
         }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    if (kSplit > 1) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            *reinterpret_cast<float4 *>(&part_acc[share][128 * j + 4 * lane]) =
+                make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+        if (lane == 0) part_sum[share] = sum;
+        __syncthreads();
+        if (warp > 0) return;
+        sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSplit; ++w) sum += part_sum[w];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kSplit; ++w) {
+                const float4 v = *reinterpret_cast<const float4 *>(&part_acc[w][128 * j + 4 * lane]);
+                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+            }
+            acc[j][0] = s.x, acc[j][1] = s.y, acc[j][2] = s.z, acc[j][3] = s.w;
+        }
+    }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int64_t out_row = (int64_t)(me.token0 + row / me.heads) * a.nheads + me.head0 + row % me.heads;
     T *out = static_cast<T *>(a.out) + out_row * D;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int e = 128 * j + 4 * lane;
-        if (e < D)
+        if (e < D) {
+            if (sizeof(T) == 4) {
+                *reinterpret_cast<float4 *>(out + e) =
+                    make_float4(acc[j][0] * inv, acc[j][1] * inv, acc[j][2] * inv, acc[j][3] * inv);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) out[e + i] = from_f32<T>(acc[j][i] * inv);
+                for (int i = 0; i < 4; ++i) out[e + i] = from_f32<T>(acc[j][i] * inv);
+            }
+        }
     }
     if (a.lse && lane == 0) a.lse[out_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
@@ -277,8 +311,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const kv_attentio
 template <typename T, int NV>
 cudaError_t launch_join(const kv_attention_args &a, const kvs::Parts &p, int grid, const kvs::Tiling &g, cudaStream_t s) {
     // a programmatic dependent of the attention kernel: its CTAs may be set up while that ends
+    const bool split = g.rows <= kSplitRows;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)kvs::ceil_div(g.rows, kJoinRows));
+    cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)(split ? g.rows : kvs::ceil_div(g.rows, 4)));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -286,7 +321,8 @@ cudaError_t launch_join(const kv_attention_args &a, const kvs::Parts &p, int gri
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_join_kernel<T, NV>, a, p, g);
+    return split ? cudaLaunchKernelEx(&cfg, kv_join_kernel<T, NV, 4>, a, p, g)
+                 : cudaLaunchKernelEx(&cfg, kv_join_kernel<T, NV, 1>, a, p, g);
 }
 
 kvs::Tiling simt_tiling(const kv_attention_args &a) { return kvs::tiling(a, kRowTile, kKeyShift, kOverhead); }

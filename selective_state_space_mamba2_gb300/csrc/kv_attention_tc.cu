@@ -39,7 +39,7 @@ constexpr int kThreads = 192;
 constexpr int kLoadWarp = 4, kMmaWarp = 5;
 constexpr int kStages = 5;
 constexpr int kOverhead = 3;  // of an item, in key tiles
-constexpr int kMinUnits = 6;
+constexpr int kMinUnits = 1;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;  // growth of a maximum (base 2) that is let stand
@@ -50,10 +50,11 @@ struct TcParams {
     kvs::Tiling g;
     uint32_t group_inv;   // ceil(2^16 / query heads per key head): row / group = row * group_inv >> 16, row < 128
     int32_t box_rows;     // rows of a page that one copy brings: divides block_size and kKeys
+    int32_t new_rows;     // rows of new tokens that one copy brings
     long long wait_limit;
 };
 
-enum { Q_FULL, Q_EMPTY, S_FULL0, S_FULL1, P_READY0, P_READY1, O_DONE, FIN, KV_FULL0, KV_EMPTY0 = KV_FULL0 + kStages,
+enum { Q_FULL, Q_EMPTY, S_FULL0, S_FULL1, P_READY0, P_READY1, O_DONE0, O_DONE1, FIN, KV_FULL0, KV_EMPTY0 = KV_FULL0 + kStages,
        NUM_BARS = KV_EMPTY0 + kStages };
 
 template <int D> struct Layout {
@@ -66,21 +67,26 @@ template <int D> struct Layout {
     static constexpr int kBytes = kFind + (int)sizeof(kvs::FindSmem);
 };
 
+// A wait that has to wait, or to look at a limit that may be short.
+__device__ __noinline__ void wait_long(uint64_t *bar, uint32_t parity, volatile int *dead, uint32_t *err, long long limit) {
+    const bool spin = limit < 100000;  // a short limit is not slept through
+    const long long t0 = clock64();
+    while (!(spin ? mbar_test(bar, parity) : mbar_try_wait_sleep(bar, parity, 20000u))) {
+        if (*dead) return;
+        if (clock64() - t0 > limit) {
+            *dead = 1;
+            report(err, SSD_DEVERR_TIMEOUT);
+            return;
+        }
+    }
+}
+
 struct Waiter {
     volatile int *dead;
     uint32_t *err;
     long long limit;
     __device__ __forceinline__ void operator()(uint64_t *bar, uint32_t parity) const {
-        if (mbar_try_wait(bar, parity)) return;
-        const long long t0 = clock64();
-        while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
-            if (*dead) return;
-            if (clock64() - t0 > limit) {
-                *dead = 1;
-                report(err, SSD_DEVERR_TIMEOUT);
-                return;
-            }
-        }
+        if (!mbar_test(bar, parity)) wait_long(bar, parity, dead, err, limit);
     }
 };
 
@@ -179,6 +185,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     volatile int *dead = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
     volatile int *dirty = reinterpret_cast<volatile int *>(smem + L::kMisc + 8);
 
+    launch_dependents();  // the join kernel may be set up as CTAs of this one end
     // Tensor memory first: the SM only starts its second CTA once the first has given up its right
     // to allocate more (measured: 3.6 us later when it was allocated after find_run).
     if (warp == kMmaWarp) {
@@ -244,11 +251,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                                 my_half * 64, w.h, pos % a.block_size, id, full);
                 }
             } else {
-                if (lane == 0) mbar_arrive_expect_tx(full, L::kTile);
+                const int base = (t - w.cached_tiles) * kKeys;
+                const int n = (min(kKeys, w.new_seen - base) + p.new_rows - 1) / p.new_rows;
+                if (lane == 0) mbar_arrive_expect_tx(full, n * kHalves * p.new_rows * 128);
                 __syncwarp();
-                if (lane < kHalves)
-                    tma_load_3d(dst + lane * (kKeys * 128), value ? &tmVn : &tmKn, lane * 64, w.h,
-                                w.q.q0 + (t - w.cached_tiles) * kKeys, full);
+                if (my_box < n)
+                    tma_load_3d(dst + my_half * (kKeys * 128) + my_box * p.new_rows * 128, value ? &tmVn : &tmKn,
+                                my_half * 64, w.h, w.q.q0 + base + my_box * p.new_rows, full);
             }
         };
         bool more = true;
@@ -283,57 +292,65 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     } else if (warp == kMmaWarp) {
         // ---- products --------------------------------------------------------------
-        if (lane == 0) {
-            constexpr uint32_t kIdS = idesc_bf16(kRows, kKeys, 0, 0);
-            constexpr uint32_t kIdO = idesc_bf16(kRows, D, 0, 1);
-            const uint64_t dQ = sw128_desc(smem_u32(smem), 16, 1024);
-            const uint64_t dK = sw128_desc(smem_u32(smem + L::kRing), 16, 1024);
-            const uint64_t dV = sw128_desc(smem_u32(smem + L::kRing), kKeys * 128, 1024);
-            uint32_t slot = 0, tile = 0, items = 0;
-            auto scores = [&]() {  // of tile number `tile`
-                const uint32_t st = slot % kStages;
-                wait(&bar[KV_FULL0 + st], (slot / kStages) & 1);
-                ++slot;
-                if (*dead) return;
-                tc_fence_after();
-                const uint64_t k0 = desc_at(dK, st * L::kTile);
+        // The whole warp walks along, one lane issues.  Order: S of tile 0, then for every tile t
+        // S of t + 1 and O of t; so the scores of a tile are there when the softmax of the one before
+        // is done.  A wait that gave up does not stop this warp: what it then multiplies has no
+        // meaning, but is in bounds, and the loops end.
+        const uint32_t on = lane == 0;
+        constexpr uint32_t kIdS = idesc_bf16(kRows, kKeys, 0, 0);
+        constexpr uint32_t kIdO = idesc_bf16(kRows, D, 0, 1);
+        const uint64_t dQ = sw128_desc(smem_u32(smem), 16, 1024);
+        const uint64_t dK = sw128_desc(smem_u32(smem + L::kRing), 16, 1024);
+        const uint64_t dV = sw128_desc(smem_u32(smem + L::kRing), kKeys * 128, 1024);
+        uint32_t st = 0, phase = 0;  // ring stage and its phase
+        uint32_t tile = 0, items = 0;
+        auto advance = [&]() {
+            if (++st == kStages) st = 0, phase ^= 1;
+        };
+        auto scores = [&](uint32_t g) {  // of tile number g
+            wait(&bar[KV_FULL0 + st], phase);
+            tc_fence_after();
+            const uint64_t k0 = desc_at(dK, st * L::kTile);
+            const uint32_t d = tm + COL_S + 64 * (g & 1);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_ss(tm + COL_S + 64 * (tile & 1), desc_at(dQ, (k >> 2) * (kRows * 128) + (k & 3) * 32),
-                           desc_at(k0, (k >> 2) * (kKeys * 128) + (k & 3) * 32), kIdS, k > 0);
-                mma_commit(&bar[KV_EMPTY0 + st]);
-                mma_commit(&bar[S_FULL0 + (tile & 1)]);
-            };
-            auto output = [&](uint32_t g, bool first) {  // of tile number g
-                wait(&bar[P_READY0 + (g & 1)], (g >> 1) & 1);
-                const uint32_t st = slot % kStages;
-                wait(&bar[KV_FULL0 + st], (slot / kStages) & 1);
-                ++slot;
-                if (*dead) return;
-                tc_fence_after();
-                const uint64_t v0 = desc_at(dV, st * L::kTile);
+            for (int k = 0; k < D / 16; ++k)
+                mma_ss_if(on, d, desc_at(dQ, (k >> 2) * (kRows * 128) + (k & 3) * 32),
+                          desc_at(k0, (k >> 2) * (kKeys * 128) + (k & 3) * 32), kIdS, k > 0);
+            mma_commit_if(on, &bar[S_FULL0 + (g & 1)]);
+            mma_commit_if(on, &bar[KV_EMPTY0 + st]);
+            advance();
+        };
+        auto output = [&](uint32_t g, uint32_t add) {  // of tile number g
+            wait(&bar[KV_FULL0 + st], phase);  // before the weights: most of the time long there
+            const uint64_t v0 = desc_at(dV, st * L::kTile);
+            const uint32_t p0 = tm + COL_S + 64 * (g & 1);
+            wait(&bar[P_READY0 + (g & 1)], (g >> 1) & 1);
+            tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                    mma_ts(tm + COL_O, tm + COL_S + 64 * (g & 1) + 8 * k, desc_at(v0, 2048 * k), kIdO, !first || k > 0);
-                mma_commit(&bar[KV_EMPTY0 + st]);
-                mma_commit(&bar[O_DONE]);
-            };
-            bool more = true;
-            while (more) {
-                wait(&bar[Q_FULL], items & 1);
-                ++items;
-                for (int t = w.t0; t < w.t1; ++t) {
-                    scores();
-                    if (t == w.t1 - 1 && !*dead) mma_commit(&bar[Q_EMPTY]);
-                    if (t > w.t0) output(tile - 1, t - 1 == w.t0);
-                    ++tile;
-                }
-                output(tile - 1, w.t1 - 1 == w.t0);
-                more = w.next(a, p.g);
+            for (int k = 0; k < kKeys / 16; ++k)
+                mma_ts_if(on, tm + COL_O, p0 + 8 * k, desc_at(v0, 2048 * k), kIdO, k > 0 ? 1u : add);
+            mma_commit_if(on, &bar[O_DONE0 + (g & 1)]);
+            mma_commit_if(on, &bar[KV_EMPTY0 + st]);
+            advance();
+        };
+        bool more = true;
+        while (more) {
+            const int n = __shfl_sync(~0u, w.t1 - w.t0, 0);
+            wait(&bar[Q_FULL], items & 1);
+            ++items;
+            scores(tile);
+            if (n == 1) mma_commit_if(on, &bar[Q_EMPTY]);
+            for (int i = 1; i < n; ++i) {
+                scores(tile + i);
+                if (i == n - 1) mma_commit_if(on, &bar[Q_EMPTY]);
+                output(tile + i - 1, i > 1);
             }
-            mma_commit(&bar[FIN]);  // everything issued is done before the CTA goes
-            mbar_wait(&bar[FIN], 0, 20000000ll);
+            output(tile + n - 1, n > 1);
+            tile += n;
+            more = w.next(a, p.g);
         }
+        mma_commit_if(on, &bar[FIN]);  // everything issued is done before the CTA goes
+        mbar_wait(&bar[FIN], 0, 20000000ll);
         __syncwarp();
     } else {
         // ---- softmax and output ------------------------------------------------------
@@ -353,22 +370,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const uint32_t s_col = lane_base + COL_S + 64 * (tile & 1);
                 const bool cached = t < w.cached_tiles;
                 const int limit = cached ? min(kKeys, w.q.c - t * kKeys)
-                                         : min(kKeys, w.q.n - (t - w.cached_tiles) * kKeys);
+                                         : min(kKeys, w.new_seen - (t - w.cached_tiles) * kKeys);
                 // every row sees every key of the tile: cached ones, or for a chain those before the
                 // tile's first token
                 const bool partial = limit < kKeys || (!cached && (a.tree_mask || (t - w.cached_tiles + 1) * kKeys >
                                                                                       token0 + 1));
-                // The product of the tile before.  Every warp waits for every product once, and before it
-                // lets the next one go: a parity only tells one phase from the next.
-                bool waited = t == w.t0;
-                auto before_done = [&]() {
-                    if (!waited) {
-                        wait(&bar[O_DONE], (tile - 1) & 1);
-                        __syncwarp();
-                        tc_fence_after();
-                        waited = true;
-                    }
-                };
                 wait(&bar[S_FULL0 + (tile & 1)], (tile >> 1) & 1);
                 __syncwarp();
                 tc_fence_after();
@@ -396,7 +402,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                         const float f = grows ? ex2(top - now) : 1.f;
                         if (grows) top = now;
                         sum *= f;
-                        before_done();
+                        // the product of the tile before (the one before that was done with these scores)
+                        wait(&bar[O_DONE0 + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1);
+                        __syncwarp();
+                        tc_fence_after();
 #pragma unroll 1
                         for (int d = 0; d < D; d += 32) {
                             uint32_t o[32];
@@ -434,13 +443,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                         dirty[item & 1] = item;  // a warp is at most one item ahead of another
                     fence_proxy_async_smem();
                 }
-                before_done();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[P_READY0 + (tile & 1)]);
             }
             ring += 2 * n_tiles;
-            wait(&bar[O_DONE], (tile - 1) & 1);
+            wait(&bar[O_DONE0 + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1);
             __syncwarp();
             tc_fence_after();
             if (warp_live) {
@@ -520,13 +528,15 @@ template <int D> cudaError_t launch(const kv_attention_args &a, void *ws, cudaSt
     p.group_inv = (65536u + p.g.heads - 1) / p.g.heads;
     p.box_rows = kKeys;
     while (a.block_size % p.box_rows) p.box_rows /= 2;
+    p.new_rows = 8;  // no more than a request is said to have: decode steps bring few rows
+    while (p.new_rows < kKeys && p.new_rows < a.max_new_tokens) p.new_rows *= 2;
     p.wait_limit = a.wait_limit_cycles > 0 ? a.wait_limit_cycles : 2000000000ll;
     const uint64_t H = a.nheads, G = a.kv_heads, T = a.total_tokens;
     CUtensorMap q, kc, vc, kn, vn;
     const bool ok =
         make_tmap_bf16_3d(&q, a.q, D, H, T, D * 2, (uint64_t)a.q_stride * 2, 64, p.g.heads, p.g.tokens) &&
-        make_tmap_bf16_3d(&kn, a.k_new, D, G, T, D * 2, (uint64_t)a.k_stride * 2, 64, 1, kKeys) &&
-        make_tmap_bf16_3d(&vn, a.v_new, D, G, T, D * 2, (uint64_t)a.v_stride * 2, 64, 1, kKeys) &&
+        make_tmap_bf16_3d(&kn, a.k_new, D, G, T, D * 2, (uint64_t)a.k_stride * 2, 64, 1, p.new_rows) &&
+        make_tmap_bf16_3d(&vn, a.v_new, D, G, T, D * 2, (uint64_t)a.v_stride * 2, 64, 1, p.new_rows) &&
         make_tmap_16bit_4d(&kc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.k_cache, D, G, a.block_size, a.num_blocks, D * 2,
                            G * D * 2, (uint64_t)a.cache_block_stride * 2, 64, 1, p.box_rows) &&
         make_tmap_16bit_4d(&vc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.v_cache, D, G, a.block_size, a.num_blocks, D * 2,

@@ -14,11 +14,10 @@
 namespace ssd {
 namespace kvs {
 
-// Written by a CTA about the item at the start of its run (for the join kernel).
+// Written by every CTA, for the join kernel: the item that the border before its run cuts.
 struct Border {
-    long long item0, item1;  // units of the item that the first unit of the run falls into
-    long long total;         // units in all
-    int32_t ctas;            // CTAs they are cut over
+    int32_t parts;           // 0: the border cuts no item, or is not the first to cut this one; else the
+                             // CTAs with a part of it, from the one before the border on
     int32_t token0, tokens;  // rows of the item: first packed token, tokens,
     int32_t head0, heads;    // first query head, query heads
 };
@@ -184,7 +183,7 @@ __device__ __forceinline__ bool find_run(const kv_attention_args &a, const Tilin
     const unsigned long long most = (total + min_units - 1) / min_units;
     const int ctas = (int)(most < gridDim.x ? most : gridDim.x);
     if ((int)blockIdx.x >= ctas) {
-        if (blockIdx.x == 0 && tid == 0) borders[0].ctas = 0;
+        if (tid == 0) borders[blockIdx.x].parts = 0;
         return false;
     }
     const unsigned long long lo = run_start(total, blockIdx.x, ctas), hi = run_start(total, blockIdx.x + 1, ctas);
@@ -227,17 +226,22 @@ __device__ __forceinline__ bool find_run(const kv_attention_args &a, const Tilin
     w.part = g.parts == 1 ? 0 : (int32_t)off / here;
     const int32_t first = (int32_t)off - w.part * here;
     w.set_item(a, g, first);
-    if (tid == 0) {
+    if (tid == nthr - 1) {  // not one of the threads that the run starts with
         Border b;
-        b.item0 = (long long)lo - first;
-        b.item1 = b.item0 + g.overhead + w.tiles;
-        b.total = (long long)total;
-        b.ctas = ctas;
+        const int32_t group = a.nheads / a.kv_heads;
         b.token0 = w.q.q0 + w.first_token(g);
         b.tokens = w.tokens(g);
-        const int32_t group = a.nheads / a.kv_heads;
         b.heads = w.heads(g, group);
         b.head0 = w.h * group + w.part * g.heads;
+        const long long tile0 = (long long)lo - first + g.overhead;  // unit of the item's first key tile
+        b.parts = 0;
+        if ((long long)lo > tile0 && run_start((long long)total, blockIdx.x - 1, ctas) <= tile0) {
+            // runs differ by one unit at most: the last CTA whose run starts before the item's end
+            const long long end = tile0 + w.tiles;
+            int last = (int)min((long long)ctas - 1, (long long)((unsigned long long)end * ctas / total) + 1);
+            while (run_start((long long)total, last, ctas) >= end) --last;
+            b.parts = last - (int)blockIdx.x + 2;
+        }
         borders[blockIdx.x] = b;
     }
     return w.any();
