@@ -1,4 +1,5 @@
-"""ctypes binding of ``include/ssd.h``: argument marshalling only.
+"""Binding of ``include/ssd.h``: argument marshalling only (ctypes, and a compiled module for the
+attention-side calls).
 
 Every numeric step runs in ``libssd_gb300.so``; torch supplies device memory
 and the current stream.  The library is loaded on first use and a missing
@@ -575,77 +576,32 @@ def mamba1_state_update(x, dt, A, B, C, state_cache, state_indices, num_accepted
 
 # ------------------------------------------- attention layers of a hybrid model --
 #
-# Decode steps make these calls every few microseconds of GPU time, so the checks below are one
-# expression per tensor on the way through; only a failed one looks for what to say.
+# These calls are made between kernels of a few microseconds, so their arguments are checked and
+# marshalled by a compiled module (csrc/kv_calls.cpp) instead of ctypes; the structures above are the
+# same ABI for callers that fill them themselves.
 
-_INT32, _FLOAT32, _BF16 = torch.int32, torch.float32, torch.bfloat16
-_TYPE_CODES = {torch.bfloat16: SSD_BF16, torch.float32: SSD_F32}
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _kv_stream(stream, like):
-    """The caller's stream, or the current one of the tensors' device, as a pointer."""
-    if stream is not None:
-        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if _raw_stream is not None:
-        return _raw_stream(like.get_device())
-    return torch.cuda.current_stream(like.device).cuda_stream
+_calls = None
 
 
-def _dense(t, name, shape, dtype):
-    """Pointer of a dense device tensor of that shape and type."""
-    try:
-        if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _dev(t, name, dtype)
-    raise ValueError("%s must be %s of shape %s" % (name, dtype, list(shape)))
+def _kv():
+    """The marshalling module of the kv_ calls (raises if it has not been built)."""
+    global _calls
+    if _calls is None:
+        lib()
+        try:
+            from . import _kv_calls
+        except ImportError as e:
+            raise RuntimeError("%s is missing or does not load: build it with __graft_entry__.build() (%s)"
+                               % (os.path.join(_PKG, "_kv_calls.so"), e)) from e
+        _calls = _kv_calls
+    return _calls
 
 
-def _rows(t, name, shape, dtype):
-    """Pointer and token stride (elements) of a device tensor [T, heads, D] whose tokens are dense rows."""
-    try:
-        if t.shape == shape and t.dtype is dtype and t.is_cuda:
-            T, H, D = shape
-            s = t.stride()
-            if T == 0:
-                return t.data_ptr(), H * D
-            if (s[2] == 1 or D == 1) and (s[1] == D or H == 1):
-                return t.data_ptr(), (s[0] if T > 1 else H * D)
-            raise ValueError("the rows of %s must be dense" % name)
-    except AttributeError:
-        pass
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    raise ValueError("%s must be %s of shape %s" % (name, dtype, list(shape)))
-
-
-def _pages(k_cache, v_cache, H, D, dtype):
-    """Pointers, sizes and block stride of k_cache and v_cache ([num_blocks, block_size, H, D])."""
-    try:
-        shape = k_cache.shape
-        if (k_cache.dtype is dtype and v_cache.dtype is dtype and k_cache.is_cuda and v_cache.is_cuda and
-                len(shape) == 4 and shape == v_cache.shape and shape[2] == H and shape[3] == D):
-            nb, bs = shape[0], shape[1]
-            sk, sv = k_cache.stride(), v_cache.stride()
-            for s in (sk, sv) if sk != sv else (sk,):
-                if (s[3] != 1 and D > 1) or (s[2] != D and H > 1) or (s[1] != H * D and bs > 1):
-                    raise ValueError("the blocks of k_cache and v_cache must be dense")
-            if nb > 1 and sk[0] != sv[0]:
-                raise ValueError("k_cache and v_cache must have the same block stride")
-            return k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, (sk[0] if nb > 1 else bs * H * D)
-    except AttributeError:
-        pass
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError("%s must be a CUDA tensor" % name)
-    raise ValueError("k_cache and v_cache must be %s [num_blocks, block_size, %d, %d]" % (dtype, H, D))
-
-
-def _code(t):
-    code = _TYPE_CODES.get(t.dtype)
-    return _dtype_code(t) if code is None else code
+def _done(fn, result):
+    """A call's result; a status instead of one is an error."""
+    if result.__class__ is int:
+        raise SSDError(fn, result)
+    return result
 
 
 def kv_block_tables(context_lens, new_lens, reserved_lens, block_table, free_ring, ring_state, block_size, num_blocks,
@@ -656,40 +612,9 @@ def kv_block_tables(context_lens, new_lens, reserved_lens, block_table, free_rin
     seq_lens [S], reserved_lens [S] and ring_state [2] (for the next call), slots, positions and token_req
     [max_tokens].  ``out``: such a dict from an earlier call to write to instead (not the one whose
     reserved_lens or ring_state this call reads)."""
-    S = context_lens.numel()
-    one, tokens = (S,), (max_tokens,)
-    p_ctx = _dense(context_lens, "context_lens", one, _INT32)
-    if block_table.dim() != 2 or block_table.shape[0] != S:
-        raise ValueError("block_table must be int32 [%d, cols]" % S)
-    cols = block_table.shape[1]
-    if out is None:
-        empty, dev = torch.empty, context_lens.device
-        cu, seq, res = (empty(S + 1, dtype=_INT32, device=dev), empty(S, dtype=_INT32, device=dev),
-                        empty(S, dtype=_INT32, device=dev))
-        ring, slots = empty(2, dtype=_INT32, device=dev), empty(max_tokens, dtype=_INT32, device=dev)
-        pos, req = empty(max_tokens, dtype=_INT32, device=dev), empty(max_tokens, dtype=_INT32, device=dev)
-        out = {"cu_seqlens": cu, "seq_lens": seq, "reserved_lens": res, "ring_state": ring, "slots": slots,
-               "positions": pos, "token_req": req}
-        outs = (ring.data_ptr(), cu.data_ptr(), seq.data_ptr(), res.data_ptr(), slots.data_ptr(), pos.data_ptr(),
-                req.data_ptr())
-    else:
-        outs = (_dense(out["ring_state"], "out ring_state", (2,), _INT32),
-                _dense(out["cu_seqlens"], "out cu_seqlens", (S + 1,), _INT32),
-                _dense(out["seq_lens"], "out seq_lens", one, _INT32),
-                _dense(out["reserved_lens"], "out reserved_lens", one, _INT32),
-                _dense(out["slots"], "out slots", tokens, _INT32),
-                _dense(out["positions"], "out positions", tokens, _INT32),
-                None if out.get("token_req") is None else _dense(out["token_req"], "out token_req", tokens, _INT32))
-    a = TablesArgs(S, block_size, cols, free_ring.numel(), max_tokens, num_blocks, null_block_id, p_ctx,
-                   _dense(new_lens, "new_lens", one, _INT32), _dense(reserved_lens, "reserved_lens", one, _INT32),
-                   _dense(block_table, "block_table", (S, cols), _INT32),
-                   _dense(free_ring, "free_ring", (free_ring.numel(),), _INT32),
-                   _dense(ring_state, "ring_state", (2,), _INT32), *outs,
-                   None if err_word is None else _dev(err_word, "err_word"))
-    rc = lib().kv_block_tables(ctypes.byref(a), _kv_stream(stream, context_lens))
-    if rc != SSD_OK:
-        raise SSDError("kv_block_tables", rc)
-    return out
+    return _done("kv_block_tables", (_calls or _kv()).block_tables(
+        context_lens, new_lens, reserved_lens, block_table, free_ring, ring_state, block_size, num_blocks, max_tokens,
+        null_block_id, out, err_word, stream))
 
 
 def kv_qk_norm_rope(q, k, positions=None, cos_sin=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
@@ -699,83 +624,33 @@ def kv_qk_norm_rope(q, k, positions=None, cos_sin=None, q_weight=None, k_weight=
     and their rotation by the rows ``positions`` of ``cos_sin`` (float32 [max_position, rotary_dim], cosines then
     sines; None for none), in one pass; with ``k_cache``, ``v_cache`` and ``slots`` the keys and ``v`` go to the
     cache too.  q, k and v may be views of one packed projection.  Returns (q_out, k_out)."""
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q and k must be [T, heads, D]")
-    qs = q.shape
-    T, H, D = qs
-    Hkv = k.shape[1]
-    ks = (T, Hkv, D)
-    dtype = q.dtype
-    code = _code(q)
-    p_q, s_q = _rows(q, "q", qs, dtype)
-    p_k, s_k = _rows(k, "k", ks, dtype)
-    if q_out is None:
-        q_out = torch.empty(qs, dtype=dtype, device=q.device)
-        p_qo = q_out.data_ptr()
-    else:
-        p_qo = _dense(q_out, "q_out", qs, dtype)
-    if k_out is None:
-        k_out = torch.empty(ks, dtype=dtype, device=q.device)
-        p_ko = k_out.data_ptr()
-    else:
-        p_ko = _dense(k_out, "k_out", ks, dtype)
-    p_cs = p_pos = p_v = p_slots = p_kc = p_vc = None
-    top = rot = nb = bs = s_v = block = 0
-    if cos_sin is not None:
-        if cos_sin.dim() != 2:
-            raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
-        top, rot = cos_sin.shape
-        p_cs = _dense(cos_sin, "cos_sin", cos_sin.shape, _FLOAT32)
-        p_pos = _dense(positions, "positions", (T,), _INT32)
-    if k_cache is not None or v_cache is not None or slots is not None:
-        p_kc, p_vc, nb, bs, block = _pages(k_cache, v_cache, Hkv, D, dtype)
-        p_v, s_v = _rows(v, "v", ks, dtype)
-        p_slots = _dense(slots, "slots", (T,), _INT32)
-    a = QkArgs(T, H, Hkv, D, rot, 1 if interleaved else 0, top, code, bs, nb, eps, s_q, s_k, s_v, block, p_q, p_k, p_v,
-               None if q_weight is None else _dense(q_weight, "q_weight", (D,), _FLOAT32),
-               None if k_weight is None else _dense(k_weight, "k_weight", (D,), _FLOAT32), p_cs, p_pos, p_slots, p_qo,
-               p_ko, p_kc, p_vc, None if err_word is None else _dev(err_word, "err_word"))
-    rc = lib().kv_qk_norm_rope(ctypes.byref(a), _kv_stream(stream, q))
-    if rc != SSD_OK:
-        raise SSDError("kv_qk_norm_rope", rc)
-    return q_out, k_out
+    return _done("kv_qk_norm_rope", (_calls or _kv()).norm_rope(
+        q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved, v, k_cache, v_cache, slots, q_out, k_out,
+        err_word, stream))
 
 
 def attention_args(q, k_new, v_new, k_cache, v_cache, cu_seqlens, context_lens, block_table, out, max_new_tokens,
                    tree_mask=None, scale=None, lse=None, err_word=None, wait_limit_cycles=0):
-    """Fills an ``AttentionArgs`` from device tensors (validating shapes and dtypes)."""
-    if q.dim() != 3 or k_new.dim() != 3:
-        raise ValueError("q and k_new must be [T, heads, D]")
-    qs = q.shape
-    T, H, D = qs
-    Hkv = k_new.shape[1]
-    ks = (T, Hkv, D)
-    dtype = q.dtype
-    code = _code(q)
-    S = cu_seqlens.numel() - 1
-    if block_table.dim() != 2 or block_table.shape[0] != S:
-        raise ValueError("block_table must be int32 [%d, cols]" % S)
-    table = block_table.shape
-    p_q, s_q = _rows(q, "q", qs, dtype)
-    p_k, s_k = _rows(k_new, "k_new", ks, dtype)
-    p_v, s_v = _rows(v_new, "v_new", ks, dtype)
-    p_kc, p_vc, nb, bs, block = _pages(k_cache, v_cache, Hkv, D, dtype)
-    p_mask, words = None, 0
-    if tree_mask is not None:
-        if tree_mask.dim() != 2 or tree_mask.shape[0] != T:
-            raise ValueError("tree_mask must be int32 [%d, words]" % T)
-        words = tree_mask.shape[1]
-        p_mask = _dense(tree_mask, "tree_mask", tree_mask.shape, _INT32)
-    return AttentionArgs(T, S, H, Hkv, D, code, bs, nb, table[1], max_new_tokens, words,
-                         D ** -0.5 if scale is None else scale, s_q, s_k, s_v, block, wait_limit_cycles, p_q, p_k, p_v,
-                         p_kc, p_vc, _dense(cu_seqlens, "cu_seqlens", (S + 1,), _INT32),
-                         _dense(context_lens, "context_lens", (S,), _INT32),
-                         _dense(block_table, "block_table", table, _INT32), p_mask, _dense(out, "out", qs, dtype),
-                         None if lse is None else _dense(lse, "lse", (T, H), _FLOAT32),
-                         None if err_word is None else _dev(err_word, "err_word"))
+    """Fills an ``AttentionArgs`` from the tensors' sizes and pointers (for
+    :func:`kv_tree_attention_workspace_size` and direct use of the C ABI); the call itself checks them."""
+    T, H, D = q.shape
+    a = AttentionArgs()
+    a.total_tokens, a.num_seqs, a.nheads, a.kv_heads, a.headdim = T, cu_seqlens.numel() - 1, H, k_new.shape[1], D
+    a.dtype, a.num_blocks, a.block_size = _dtype_code(q), k_cache.shape[0], k_cache.shape[1]
+    a.table_cols, a.max_new_tokens = block_table.shape[1], int(max_new_tokens)
+    a.mask_words = 0 if tree_mask is None else tree_mask.shape[1]
+    a.scale = float(D ** -0.5 if scale is None else scale)
+    a.q_stride, a.k_stride, a.v_stride = q.stride(0), k_new.stride(0), v_new.stride(0)
+    a.cache_block_stride, a.wait_limit_cycles = k_cache.stride(0), int(wait_limit_cycles)
+    for f, t in (("q", q), ("k_new", k_new), ("v_new", v_new), ("k_cache", k_cache), ("v_cache", v_cache),
+                 ("cu_seqlens", cu_seqlens), ("context_lens", context_lens), ("block_table", block_table),
+                 ("tree_mask", tree_mask), ("out", out), ("lse", lse), ("err_word", err_word)):
+        setattr(a, f, None if t is None else t.data_ptr())
+    return a
 
 
 def kv_tree_attention_workspace_size(args):
+    """Bytes of workspace the call with these arguments (:func:`attention_args`) needs."""
     return int(lib().kv_tree_attention_workspace_size(ctypes.byref(args)))
 
 
@@ -785,22 +660,11 @@ def kv_tree_attention(q, k_new, v_new, k_cache, v_cache, cu_seqlens, context_len
     """Attention of every request's new tokens (packed, ``cu_seqlens``) over its ``context_lens`` cached ones and
     one another: bit j of a row of ``tree_mask`` (int32 [T, words]) lets the token see its request's new token j;
     without a mask the new tokens are a chain.  ``scale`` defaults to D ** -0.5.  Returns ``out`` [T, H, D], or
-    (out, lse [T, H] float32) with ``return_lse`` or ``lse``."""
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if lse is None and return_lse:
-        lse = torch.empty(q.shape[:2], dtype=_FLOAT32, device=q.device)
-    a = attention_args(q, k_new, v_new, k_cache, v_cache, cu_seqlens, context_lens, block_table, out, max_new_tokens,
-                       tree_mask, scale, lse, err_word, wait_limit_cycles)
-    L = lib()
-    ref = ctypes.byref(a)
-    if workspace is None:
-        need = L.kv_tree_attention_workspace_size(ref)
-        workspace = torch.empty(need or 1, dtype=torch.uint8, device=q.device)
-    rc = L.kv_tree_attention(ref, workspace.data_ptr(), workspace.numel(), _kv_stream(stream, q))
-    if rc != SSD_OK:
-        raise SSDError("kv_tree_attention", rc)
-    return out if lse is None else (out, lse)
+    (out, lse [T, H] float32) with ``return_lse`` or ``lse``.  ``workspace`` (uint8, allocated with torch when
+    omitted) as :func:`kv_tree_attention_workspace_size` says."""
+    return _done("kv_tree_attention", (_calls or _kv()).tree_attention(
+        q, k_new, v_new, k_cache, v_cache, cu_seqlens, context_lens, block_table, max_new_tokens, tree_mask, scale,
+        out, lse, return_lse, workspace, err_word, stream, wait_limit_cycles))
 
 
 def kv_commit_tokens(k_new, v_new, k_cache, v_cache, slots, cu_seqlens=None, context_lens=None, path=None,
@@ -808,41 +672,5 @@ def kv_commit_tokens(k_new, v_new, k_cache, v_cache, slots, cu_seqlens=None, con
     """Keys and values of accepted tokens to the cache: step i of request r's ``path`` ([S, max_path], the index of
     a new token; None: all of them in order) goes to the slot of its new token i.  ``slots`` may be padded beyond
     the tokens.  Returns the new context lengths, or None without ``context_lens``."""
-    if k_new.dim() != 3:
-        raise ValueError("k_new must be [T, heads, D]")
-    shape = k_new.shape
-    T, H, D = shape
-    dtype = k_new.dtype
-    code = _code(k_new)
-    p_k, s_k = _rows(k_new, "k_new", shape, dtype)
-    p_v, s_v = _rows(v_new, "v_new", shape, dtype)
-    p_kc, p_vc, nb, bs, block = _pages(k_cache, v_cache, H, D, dtype)
-    p_slots = _dense(slots, "slots", (slots.numel(),), _INT32)
-    if slots.numel() < T:
-        raise ValueError("slots must have an entry for each of the %d tokens" % T)
-    S, width = 0, 0
-    p_cu = p_path = p_lens = p_ctx = p_out = None
-    if cu_seqlens is not None:
-        S = cu_seqlens.numel() - 1
-        p_cu = _dense(cu_seqlens, "cu_seqlens", (S + 1,), _INT32)
-    elif path is not None or context_lens is not None:
-        raise ValueError("cu_seqlens is required")
-    if path is not None:
-        if path.dim() != 2 or path.shape[0] != S or path.shape[1] == 0:
-            raise ValueError("path must be int32 [%d, max_path]" % S)
-        width = path.shape[1]
-        p_path = _dense(path, "path", path.shape, _INT32)
-        p_lens = _dense(path_lens, "path_lens", (S,), _INT32)
-    if context_lens is not None:
-        p_ctx = _dense(context_lens, "context_lens", (S,), _INT32)
-        if context_out is None:
-            context_out = torch.empty(S, dtype=_INT32, device=k_new.device)
-            p_out = context_out.data_ptr()
-        else:
-            p_out = _dense(context_out, "context_out", (S,), _INT32)
-    a = CommitArgs(T, S, H, D, code, bs, nb, width, s_k, s_v, block, p_k, p_v, p_slots, p_cu, p_path, p_lens, p_ctx,
-                   p_out, p_kc, p_vc, None if err_word is None else _dev(err_word, "err_word"))
-    rc = lib().kv_commit_tokens(ctypes.byref(a), _kv_stream(stream, k_new))
-    if rc != SSD_OK:
-        raise SSDError("kv_commit_tokens", rc)
-    return context_out
+    return _done("kv_commit_tokens", (_calls or _kv()).commit_tokens(
+        k_new, v_new, k_cache, v_cache, slots, cu_seqlens, context_lens, path, path_lens, context_out, err_word, stream))

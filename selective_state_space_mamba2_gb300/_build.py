@@ -1,13 +1,16 @@
 """Builds the CUDA library ``libssd_gb300.so`` in-tree for sm_103a.
 
 Each translation unit is compiled by its own nvcc process (in parallel),
-then linked; nothing is installed outside the package directory.
+then linked; nothing is installed outside the package directory.  Beside it
+the CPython module ``_kv_calls.so`` (host compiler, torch's headers), which
+marshals the arguments of the attention-side calls.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +24,10 @@ SOURCES = ["api.cu", "decode.cu", "prefill_simt.cu", "prefill_tc.cu", "prefill_s
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
+
+
+CALLS = "kv_calls.cpp"
+CALLS_LIB = os.path.join(PKG, "_kv_calls.so")
 
 
 def nvcc() -> str:
@@ -55,18 +62,62 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
-def build(verbose_ptxas: bool = False) -> str:
-    os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), SOURCES))
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
+def _compile_calls() -> str:
+    obj, srcp = os.path.join(BUILD, CALLS + ".o"), os.path.join(CSRC, CALLS)
+    if os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(srcp), _headers_mtime()):
+        return obj
+    import torch
+    inc = os.path.join(_torch_dir(), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    tmp = obj + ".tmp.%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I", INCLUDE, "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-c", srcp, "-o", tmp]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (CALLS, res.stdout, res.stderr))
+    os.replace(tmp, obj)
+    return obj
+
+
+def _link_calls(obj: str) -> None:
+    if os.path.exists(CALLS_LIB) and os.path.getmtime(CALLS_LIB) >= os.path.getmtime(obj):
+        return
+    tmp = CALLS_LIB + ".tmp.%d" % os.getpid()
+    # torch's libraries are loaded already when the module is; ours is found beside it
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(_torch_dir(), "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("link failed:\n%s\n%s" % (res.stdout, res.stderr))
+    os.replace(tmp, CALLS_LIB)
+
+
+def _link(objs) -> None:
     if os.path.exists(LIB) and all(os.path.getmtime(LIB) >= os.path.getmtime(o) for o in objs):
-        return LIB
+        return
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart", "-lcuda"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (res.stdout, res.stderr))
     os.replace(tmp, LIB)
+
+
+def build(verbose_ptxas: bool = False) -> str:
+    os.makedirs(BUILD, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(_compile_calls)
+        objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), SOURCES))
+        calls = calls.result()
+    _link(objs)
+    _link_calls(calls)
     return LIB
 
 
