@@ -1,13 +1,21 @@
 // Internal declarations of the attention-side calls (kv_*).
 #pragma once
+#include <atomic>
+
 #include "common.cuh"
 
 namespace ssd {
-// SMs of the current device (152 on GB300, also where the attribute cannot be read).
+// SMs of the current device (152 on GB300, also where the attribute cannot be read).  Asked once per
+// device: a decode step's call takes a few microseconds in all.
 inline int device_sms() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 152;
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+    int sms = known[dev].load(std::memory_order_relaxed);
+    if (sms == 0) {
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 152;
+        known[dev].store(sms, std::memory_order_relaxed);
+    }
     return sms;
 }
 

@@ -181,11 +181,19 @@ PyObject *block_tables(PyObject *const *a, PyObject *) {
     int32_t *ptr[7] = {};
     PyObject *out = a[10];
     if (out == Py_None) {
+        // one allocation, each output at a 64-byte boundary of it
+        int64_t at[7], all = 0;
+        for (int i = 0; i < 7; ++i) at[i] = all, all += (sizes[i] + 15) / 16 * 16;
+        const at::Tensor room = empty(all, at::kInt, ctx);
         out = PyDict_New();
         if (!out) throw PythonError{};
         for (int i = 0; i < 7; ++i) {
-            at::Tensor t = empty(sizes[i], at::kInt, ctx);
-            ptr[i] = static_cast<int32_t *>(t.data_ptr());
+            at::Tensor t;
+            {
+                at::AutoDispatchBelowADInplaceOrView no_grad;  // plain views: nothing here has gradients
+                t = room.as_strided(sizes[i], 1, at[i]);
+            }
+            ptr[i] = static_cast<int32_t *>(room.data_ptr()) + at[i];
             PyObject *w = THPVariable_Wrap(std::move(t));
             const int bad = w ? PyDict_SetItemString(out, names[i], w) : -1;
             Py_XDECREF(w);

@@ -13,18 +13,14 @@
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTile = 1024;   // tokens of a CTA
+constexpr int kThreads = 512;
+constexpr int kTile = 2048;   // tokens of a CTA
 constexpr int kInline = 8;    // tokens of a request in a tile that its scanning thread writes itself
 constexpr int kQueue = kTile / (kInline + 1) + 2;
 
 struct Span {  // tokens [t0, t1) of request r
     int32_t t0, t1, r, pos0, held, taken;
-};
-
-struct Totals {
-    unsigned long long tokens, pops;
-    uint32_t bad;
+    bool begins;  // t0 is the request's first new token
 };
 
 __device__ __forceinline__ int32_t blocks_of(int32_t tokens, int32_t b) { return tokens / b + (tokens % b != 0); }
@@ -52,49 +48,75 @@ __device__ __forceinline__ Lens lens_of(const kv_tables_args &a, int32_t r) {
 }
 
 __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const kv_tables_args a) {
-    __shared__ Totals warp_tot[kThreads / 32];
-    __shared__ unsigned long long warp_sum[kThreads / 32];
+    constexpr int kWarps = kThreads / 32;
+    __shared__ unsigned long long warp_tokens[kWarps], warp_pops[kWarps];
+    __shared__ uint32_t warp_bad[kWarps];
     __shared__ Span queue[kQueue];
     __shared__ int queued;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = a.num_reqs, b = a.block_size;
-    if (tid == 0) queued = 0;
+    const int32_t head = a.ring_in[0], count = a.ring_in[1];
+
+    // One chunk of requests, a thread each: its lengths, the tokens and blocks before it in the chunk
+    // and those of the whole chunk.  The sums are 64 bits wide: nothing has been checked yet.
+    Lens l;
+    unsigned long long tokens_before, pops_before, tokens_all, pops_all;
+    uint32_t bad_all;
+    auto scan = [&](int base) {
+        const int r = base + tid;
+        l = Lens{0, 0, 0, 0, 0};
+        if (r < S) l = lens_of(a, r);
+        const unsigned long long n = l.n > 0 ? l.n : 0, p = l.need - l.held;
+        unsigned long long ns = n, ps = p;
+        uint32_t bad = l.bad;
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long nv = __shfl_up_sync(~0u, ns, o), pv = __shfl_up_sync(~0u, ps, o);
+            if (lane >= o) ns += nv, ps += pv;
+        }
+        bad = __reduce_or_sync(~0u, bad);
+        __syncthreads();  // the last chunk's readers are done
+        if (lane == 31) warp_tokens[warp] = ns, warp_pops[warp] = ps, warp_bad[warp] = bad;
+        if (tid == 0) queued = 0;
+        __syncthreads();
+        tokens_before = ns - n, pops_before = ps - p;
+        tokens_all = pops_all = 0;
+        bad_all = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) tokens_before += warp_tokens[w], pops_before += warp_pops[w];
+            tokens_all += warp_tokens[w], pops_all += warp_pops[w];
+            bad_all |= warp_bad[w];
+        }
+    };
 
     // totals and checks over all requests
-    Totals t{0, 0, 0};
-    for (int r = tid; r < S; r += kThreads) {
-        const Lens l = lens_of(a, r);
-        t.bad |= l.bad;
-        t.tokens += l.n > 0 ? l.n : 0;
-        t.pops += l.need - l.held;
+    unsigned long long tokens = 0, pops = 0;
+    uint32_t bad = 0;
+    for (int base = 0; base < S; base += kThreads) {
+        scan(base);
+        tokens += tokens_all, pops += pops_all, bad |= bad_all;
     }
-    for (int o = 16; o > 0; o >>= 1) {
-        t.tokens += __shfl_xor_sync(~0u, t.tokens, o);
-        t.pops += __shfl_xor_sync(~0u, t.pops, o);
-        t.bad |= __shfl_xor_sync(~0u, t.bad, o);
-    }
-    if (lane == 0) warp_tot[warp] = t;
-    const int32_t head = a.ring_in[0], count = a.ring_in[1];
-    __syncthreads();
-    t = Totals{0, 0, 0};
-    for (int w = 0; w < kThreads / 32; ++w) {
-        t.tokens += warp_tot[w].tokens;
-        t.pops += warp_tot[w].pops;
-        t.bad |= warp_tot[w].bad;
-    }
-    if (t.tokens > (unsigned long long)a.max_tokens) t.bad |= SSD_DEVERR_METADATA;
+    if (tokens > (unsigned long long)a.max_tokens) bad |= SSD_DEVERR_METADATA;
     if (head < 0 || count < 0 || count > a.free_capacity || (head >= a.free_capacity && head > 0))
-        t.bad |= SSD_DEVERR_METADATA;
-    else if (t.pops > (unsigned long long)count)
-        t.bad |= SSD_DEVERR_BLOCKS;
-    const bool ok = t.bad == 0;
+        bad |= SSD_DEVERR_METADATA;
+    else if (pops > (unsigned long long)count)
+        bad |= SSD_DEVERR_BLOCKS;
+    const bool ok = bad == 0;
+    // entry `off` of the ring from its head on; head and off are below its capacity
+    auto ring_id = [&](int32_t off) {
+        uint32_t i = (uint32_t)head + (uint32_t)off;
+        if (i >= (uint32_t)a.free_capacity) i -= (uint32_t)a.free_capacity;
+        return a.free_ring[i];
+    };
     if (blockIdx.x == 0 && tid == 0) {
-        if (!ok) report(a.err_word, t.bad);
-        a.ring_out[0] = ok && t.pops ? (int32_t)((head + t.pops) % a.free_capacity) : head;
-        a.ring_out[1] = ok ? count - (int32_t)t.pops : count;
-        a.cu_seqlens[S] = ok ? (int32_t)t.tokens : 0;
+        if (!ok) report(a.err_word, bad);
+        uint32_t next = (uint32_t)head + (ok ? (uint32_t)pops : 0u);
+        if (ok && pops && next >= (uint32_t)a.free_capacity) next -= (uint32_t)a.free_capacity;
+        a.ring_out[0] = (int32_t)next;
+        a.ring_out[1] = ok ? count - (int32_t)pops : count;
+        a.cu_seqlens[S] = ok ? (int32_t)tokens : 0;
     }
-    const int32_t total = ok ? (int32_t)t.tokens : 0;
+    const int32_t total = ok ? (int32_t)tokens : 0;
     const int32_t tile0 = (int32_t)min((long long)blockIdx.x * kTile, (long long)a.max_tokens);
     const int32_t tile1 = (int32_t)min((long long)tile0 + kTile, (long long)a.max_tokens);
 
@@ -112,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const kv_tables_arg
         if (col < held) {
             id = row[col];
         } else {
-            id = a.free_ring[((int64_t)head + taken + (col - held)) % a.free_capacity];
+            id = ring_id(taken + (col - held));
             if (off == 0 || first) row[col] = id;
         }
         int32_t slot = -1;
@@ -127,47 +149,32 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const kv_tables_arg
         if (a.token_req) a.token_req[i] = r;
     };
 
-    // prefix sums, 256 requests at a time: tokens in the high half, blocks taken in the low one
-    unsigned long long carry = 0;
+    unsigned long long tokens_carry = 0, pops_carry = 0;
     for (int base = 0, chunk = 0; base < S; base += kThreads, ++chunk) {
+        if (S > kThreads) scan(base);  // else the scan above still holds
         const int r = base + tid;
-        const bool owner = chunk % gridDim.x == blockIdx.x;
-        Lens l{0, 0, 0, 0, 0};
-        if (r < S && ok) l = lens_of(a, r);
-        const unsigned long long own = (unsigned long long)l.n << 32 | (uint32_t)(l.need - l.held);
-        unsigned long long sum = own;
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long v = __shfl_up_sync(~0u, sum, o);
-            if (lane >= o) sum += v;
-        }
-        __syncthreads();  // the last chunk's readers of warp_sum and the queue are done
-        if (lane == 31) warp_sum[warp] = sum;
-        if (tid == 0) queued = 0;
-        __syncthreads();
-        unsigned long long before = carry + sum - own;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += warp_sum[w];
-            carry += warp_sum[w];
-        }
-        const int32_t first = (int32_t)(before >> 32), taken = (int32_t)(uint32_t)before;
+        // with a refused step every request starts at 0 and has no tokens
+        const int32_t n = ok ? l.n : 0;
+        const int32_t first = ok ? (int32_t)(tokens_carry + tokens_before) : 0;
+        const int32_t taken = ok ? (int32_t)(pops_carry + pops_before) : 0;
+        tokens_carry += tokens_all, pops_carry += pops_all;
         if (r < S) {
-            if (owner) {
+            if (chunk % gridDim.x == blockIdx.x) {  // the requests' own outputs are dealt out by chunks
                 a.cu_seqlens[r] = first;
-                const int32_t c = a.context_lens[r], v = a.reserved_lens[r];
-                a.seq_lens[r] = ok ? c + l.n : c;
-                a.reserved_out[r] = ok ? max(v, c + l.n) : v;
+                const int32_t v = a.reserved_lens[r];
+                a.seq_lens[r] = l.c + n;
+                a.reserved_out[r] = ok ? max(v, l.c + n) : v;
                 // new blocks that no new token falls into
-                const int32_t last = l.n > 0 ? min(l.need, l.c / b) : l.need;
+                const int32_t last = !ok ? l.held : n > 0 ? min(l.need, l.c / b) : l.need;
                 for (int col = l.held; col < last; ++col)
-                    a.block_table[(int64_t)r * a.table_cols + col] =
-                        a.free_ring[((int64_t)head + taken + (col - l.held)) % a.free_capacity];
+                    a.block_table[(int64_t)r * a.table_cols + col] = ring_id(taken + (col - l.held));
             }
-            const int32_t t0 = max(first, tile0), t1 = min(first + l.n, tile1);
+            const int32_t t0 = max(first, tile0), t1 = min(first + n, tile1);
             if (t1 > t0) {
                 if (t1 - t0 <= kInline) {
                     for (int i = t0; i < t1; ++i) token(i, r, l.c + (i - first), l.held, taken, i == first);
                 } else {
-                    queue[atomicAdd(&queued, 1)] = Span{t0, t1, r, l.c + (t0 - first), l.held, taken};
+                    queue[atomicAdd(&queued, 1)] = Span{t0, t1, r, l.c + (t0 - first), l.held, taken, t0 == first};
                 }
             }
         }
@@ -175,11 +182,8 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const kv_tables_arg
         const int nq = queued;
         for (int q = 0; q < nq; ++q) {
             const Span s = queue[q];
-            const int32_t c = a.context_lens[s.r];
-            for (int i = s.t0 + tid; i < s.t1; i += kThreads) {
-                const int32_t pos = s.pos0 + (i - s.t0);
-                token(i, s.r, pos, s.held, s.taken, pos == c);
-            }
+            for (int i = s.t0 + tid; i < s.t1; i += kThreads)
+                token(i, s.r, s.pos0 + (i - s.t0), s.held, s.taken, s.begins && i == s.t0);
         }
     }
 }

@@ -3,6 +3,7 @@
 // Both are bound by HBM: every row is read once and written once in 16-byte pieces (two for
 // fp32), 8 elements a lane.
 #include "kv.cuh"
+#include "tc_ptx.cuh"
 
 namespace ssd {
 namespace {
@@ -21,64 +22,49 @@ namespace {
 enum { kPairInside = 0, kPairLane = 1, kPairLoad = 2 };
 
 constexpr int kQkThreads = 128;
-constexpr int kQkCtasPerSm = 5;
+// CTAs of an SM: what hides the loads' latency is warps (65536 tokens of 32 + 8 heads of 128, bf16: 312,
+// 296, 295, 280 and 308 us with 4 to 8); fp32 and partners read again need more registers each.
+constexpr int qk_ctas_per_sm(int pair, int elem) { return pair == kPairLoad || elem == 4 ? 5 : 7; }
 
+// 8 entries of a row as they lie in memory; get and set go by pairs, for packed fp32 arithmetic.
 template <typename T> struct Row8;
 template <> struct Row8<__nv_bfloat16> {
-    uint4 u;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { u = *reinterpret_cast<const uint4 *>(p); }
-    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint4 *>(p) = u; }
-    __device__ __forceinline__ void get(float (&f)[8]) const {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
+    uint32_t w[4];
+    __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0; }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
     }
-    __device__ __forceinline__ void set(const float (&f)[8]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            w[i] = *reinterpret_cast<uint32_t *>(&v);
-        }
-        u = make_uint4(w[0], w[1], w[2], w[3]);
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    __device__ __forceinline__ Row8 from_lane(int src, int width) const {
-        Row8 o;
-        o.u.x = __shfl_sync(~0u, u.x, src, width);
-        o.u.y = __shfl_sync(~0u, u.y, src, width);
-        o.u.z = __shfl_sync(~0u, u.z, src, width);
-        o.u.w = __shfl_sync(~0u, u.w, src, width);
-        return o;
+    __device__ __forceinline__ float2 get(int i) const {
+        return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    }
+    __device__ __forceinline__ void set(int i, float2 v) {
+        __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+        w[i] = *reinterpret_cast<uint32_t *>(&b);
     }
 };
 template <> struct Row8<float> {
-    float4 a, b;
+    uint32_t w[8];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 0;
+    }
     __device__ __forceinline__ void load(const float *p) {
-        a = reinterpret_cast<const float4 *>(p)[0];
-        b = reinterpret_cast<const float4 *>(p)[1];
+        const uint4 a = reinterpret_cast<const uint4 *>(p)[0], b = reinterpret_cast<const uint4 *>(p)[1];
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
     }
     __device__ __forceinline__ void store(float *p) const {
-        reinterpret_cast<float4 *>(p)[0] = a;
-        reinterpret_cast<float4 *>(p)[1] = b;
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
-    __device__ __forceinline__ void get(float (&f)[8]) const {
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    __device__ __forceinline__ float2 get(int i) const {
+        return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     }
-    __device__ __forceinline__ void set(const float (&f)[8]) {
-        a = make_float4(f[0], f[1], f[2], f[3]);
-        b = make_float4(f[4], f[5], f[6], f[7]);
-    }
-    __device__ __forceinline__ Row8 from_lane(int src, int width) const {
-        float f[8];
-        get(f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __shfl_sync(~0u, f[i], src, width);
-        Row8 o;
-        o.set(f);
-        return o;
+    __device__ __forceinline__ void set(int i, float2 v) {
+        w[2 * i] = __float_as_uint(v.x), w[2 * i + 1] = __float_as_uint(v.y);
     }
 };
 
@@ -125,20 +111,24 @@ __device__ __forceinline__ void angles(const kv_qk_args &a, int32_t pos, int e0,
     }
 }
 
-// A row (head) is `width` lanes, 8 entries each (width: headdim / 8 rounded up to a power of two).  A
-// lane group loads its first key and value row and W query rows before it computes the first.
-template <typename T, int PAIR>
-__global__ void __launch_bounds__(kQkThreads, kQkCtasPerSm) kv_qk_kernel(const kv_qk_args a, const int width) {
+// A row (head) is `width` lanes, 8 entries each (width: headdim / 8 rounded up to a power of two;
+// WIDTH where the kernel is made for it, else 0).  A lane group loads its first key and value row and W
+// query rows before it computes the first.
+template <typename T, int PAIR, int WIDTH>
+__global__ void __launch_bounds__(kQkThreads, qk_ctas_per_sm(PAIR, sizeof(T))) kv_qk_kernel(const kv_qk_args a, const int any_width) {
     constexpr int W = (PAIR == kPairLoad ? 2 : 4) / (sizeof(T) == 4 ? 2 : 1);  // query rows in flight
+    constexpr int kWords = 2 * (int)sizeof(T);  // 32-bit words of 8 entries
     __shared__ __align__(16) float weights[4][256];  // of q's entries and their partners, of k's
+    const int width = WIDTH ? WIDTH : any_width;
     const int D = a.headdim, R = a.rotary_dim, half = R / 2;
     const int sub = threadIdx.x & (width - 1), group = threadIdx.x / width, groups = kQkThreads / width;
     const int e0 = sub * 8;
     const bool live = e0 < D;
     const bool want_k = a.k_out || a.k_cache;
+    const bool turns = e0 < R;  // this lane's entries are (with kPairLoad: may be) rotated
 
     int src_lane = 0;  // kPairLane: whose entries are the partners of this lane's
-    if (PAIR == kPairLane && e0 < R) src_lane = (e0 < half ? e0 + half : e0 - half) / 8;
+    if (PAIR == kPairLane && turns) src_lane = (e0 < half ? e0 + half : e0 - half) / 8;
     auto partner = [&](int i) -> int {
         const int e = e0 + i;
         if (e >= R) return e;
@@ -156,77 +146,78 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtasPerSm) kv_qk_kernel(const k
     }
     __syncthreads();
     // a and b of this lane's entries for q (which = 0) or k (2)
-    auto factors = [&](int which, const float (&cs)[8], const float (&sn)[8], float (&fa)[8], float (&fb)[8]) {
+    auto factors = [&](int which, const float (&cs)[8], const float (&sn)[8], float2 (&fa)[4], float2 (&fb)[4]) {
         if (!live) return;
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
             const float4 w = *reinterpret_cast<const float4 *>(&weights[which][e0 + i]);
             const float4 o = *reinterpret_cast<const float4 *>(&weights[which + 1][e0 + i]);
-            fa[i] = cs[i] * w.x, fa[i + 1] = cs[i + 1] * w.y, fa[i + 2] = cs[i + 2] * w.z, fa[i + 3] = cs[i + 3] * w.w;
-            fb[i] = sn[i] * o.x, fb[i + 1] = sn[i + 1] * o.y, fb[i + 2] = sn[i + 2] * o.z, fb[i + 3] = sn[i + 3] * o.w;
+            fa[i / 2] = tc::mul_f2(make_float2(cs[i], cs[i + 1]), make_float2(w.x, w.y));
+            fa[i / 2 + 1] = tc::mul_f2(make_float2(cs[i + 2], cs[i + 3]), make_float2(w.z, w.w));
+            fb[i / 2] = tc::mul_f2(make_float2(sn[i], sn[i + 1]), make_float2(o.x, o.y));
+            fb[i / 2 + 1] = tc::mul_f2(make_float2(sn[i + 2], sn[i + 3]), make_float2(o.z, o.w));
         }
     };
     const float inv_d = 1.f / (float)D;
 
-    auto fetch = [&](Row8<T> &x, float (&other)[8], const T *in, bool on) {
-        if (on && live) {
-            x.load(in + e0);
-            if (PAIR == kPairLoad) {
+    auto fetch = [&](Row8<T> &x, float2 (&other)[4], const T *in, bool on) {
+        x.clear();
+        if (on && live) x.load(in + e0);
+        if (PAIR == kPairLoad) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) other[i] = to_f32(in[partner(i)]);
-            }
-        } else {
-            const float z[8] = {};
-            x.set(z);
-            if (PAIR == kPairLoad) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) other[i] = 0.f;
-            }
+            for (int i = 0; i < 4; ++i)
+                other[i] = on && live ? make_float2(to_f32(in[partner(2 * i)]), to_f32(in[partner(2 * i + 1)]))
+                                      : make_float2(0.f, 0.f);
         }
     };
     // one row: norm and rotation
-    auto turn = [&](const Row8<T> &x, const float (&other)[8], const float (&fa)[8], const float (&fb)[8], bool norm) {
-        float v[8], p[8], y[8];
-        x.get(v);
+    auto turn = [&](const Row8<T> &x, const float2 (&other)[4], const float2 (&fa)[4], const float2 (&fb)[4], bool norm) {
         float r = 1.f;
         if (norm) {
-            float ss = 0.f;
+            float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-            for (int o = width / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+            for (int i = 0; i < 4; ++i) s2 = tc::fma_f2(x.get(i), x.get(i), s2);
+            float ss = s2.x + s2.y;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                if (o < width) ss += __shfl_xor_sync(~0u, ss, o);
             r = rsqrtf(fmaf(ss, inv_d, a.eps));
         }
-        if (PAIR == kPairInside) {
+        Row8<T> p = x, y;
+        if (PAIR == kPairLane) {
+            // beyond the rotated part there is no partner: zero, whatever the other lane holds
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = v[i ^ 1];
-        } else if (PAIR == kPairLane) {
-            x.from_lane(src_lane, width).get(p);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = other[i];
+            for (int i = 0; i < kWords; ++i) {
+                const uint32_t v = __shfl_sync(~0u, x.w[i], src_lane, width);
+                p.w[i] = turns ? v : 0u;
+            }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // beyond the rotated part there is no partner: left out, whatever it holds
-            const float turned = e0 + i < R ? fb[i] * p[i] : 0.f;
-            y[i] = r * fmaf(fa[i], v[i], turned);
+        for (int i = 0; i < 4; ++i) {
+            float2 o;
+            if (PAIR == kPairInside) {
+                o = make_float2(x.get(i).y, x.get(i).x);
+                if (!turns) o = make_float2(0.f, 0.f);
+            } else if (PAIR == kPairLane) {
+                o = p.get(i);
+            } else {
+                o = other[i];
+                if (e0 + 2 * i >= R) o.x = 0.f;
+                if (e0 + 2 * i + 1 >= R) o.y = 0.f;
+            }
+            y.set(i, tc::mul_f2(make_float2(r, r), tc::fma_f2(fa[i], x.get(i), tc::mul_f2(fb[i], o))));
         }
-        Row8<T> o;
-        o.set(y);
-        return o;
+        return y;
     };
 
     int t = blockIdx.x;
     int32_t pos = R > 0 ? a.positions[t] : 0;
     int32_t slot = a.k_cache ? a.slots[t] : -1;
     while (true) {
-        const int t_next = t + gridDim.x;
-        const bool more = t_next < a.total_tokens;
-        int32_t pos_next = 0, slot_next = -1;
-        if (more) {
-            if (R > 0) pos_next = a.positions[t_next];
-            if (a.k_cache) slot_next = a.slots[t_next];
-        }
+        const bool more = t < a.total_tokens - (int)gridDim.x;
+        const int t_next = more ? t + gridDim.x : t;
+        const int32_t pos_next = R > 0 ? a.positions[t_next] : 0;
+        const int32_t slot_next = a.k_cache ? a.slots[t_next] : -1;
         if (R > 0 && (pos < 0 || pos >= a.max_position)) {  // the same for the whole CTA
             if (threadIdx.x == 0) report(a.err_word, SSD_DEVERR_METADATA);
         } else {
@@ -247,7 +238,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtasPerSm) kv_qk_kernel(const k
             const T *vin = static_cast<const T *>(a.v) + (int64_t)t * a.v_stride;
             constexpr int kOther = PAIR == kPairLoad ? W : 1;
             Row8<T> xq[W], xk, xv;
-            float oq[kOther][8], ok[8];
+            float2 oq[kOther][4], ok[4];
             fetch(xk, ok, kin + group * D, want_k && group < a.kv_heads);
             if (vc && live && group < a.kv_heads) xv.load(vin + group * D + e0);
 #pragma unroll
@@ -255,7 +246,8 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtasPerSm) kv_qk_kernel(const k
                 const int h = group + j * groups;
                 fetch(xq[j], oq[PAIR == kPairLoad ? j : 0], qin + h * D, h < a.nheads);
             }
-            float cs[8], sn[8], fa[8] = {}, fb[8] = {};
+            float cs[8], sn[8];
+            float2 fa[4] = {}, fb[4] = {};
             angles<PAIR>(a, pos, e0, cs, sn);
             if (PAIR == kPairLoad) __syncwarp();  // in place: partners are read before a row is overwritten
 
@@ -305,19 +297,23 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtasPerSm) kv_qk_kernel(const k
     }
 }
 
-template <typename T> cudaError_t launch_qk(const kv_qk_args &a, cudaStream_t s) {
+template <typename T, int PAIR> cudaError_t launch_qk(const kv_qk_args &a, cudaStream_t s) {
     int width = 1;
     while (width * 8 < a.headdim) width *= 2;
-    const int most = kQkCtasPerSm * device_sms();
+    const int most = qk_ctas_per_sm(PAIR, sizeof(T)) * device_sms();
     const dim3 grid((unsigned)(a.total_tokens < most ? a.total_tokens : most));
-    const bool pieces = (reinterpret_cast<uintptr_t>(a.cos_sin) & 15u) == 0;  // 16-byte loads of the angles
-    if (a.interleaved && a.rotary_dim % 8 == 0 && pieces)
-        kv_qk_kernel<T, kPairInside><<<grid, kQkThreads, 0, s>>>(a, width);
-    else if (!a.interleaved && a.rotary_dim % 16 == 0 && pieces)
-        kv_qk_kernel<T, kPairLane><<<grid, kQkThreads, 0, s>>>(a, width);
+    if (width == 16)  // headdim 72 to 128, the common ones: the reduction unrolled
+        kv_qk_kernel<T, PAIR, 16><<<grid, kQkThreads, 0, s>>>(a, width);
     else
-        kv_qk_kernel<T, kPairLoad><<<grid, kQkThreads, 0, s>>>(a, width);
+        kv_qk_kernel<T, PAIR, 0><<<grid, kQkThreads, 0, s>>>(a, width);
     return cudaGetLastError();
+}
+
+template <typename T> cudaError_t launch_qk(const kv_qk_args &a, cudaStream_t s) {
+    const bool pieces = (reinterpret_cast<uintptr_t>(a.cos_sin) & 15u) == 0;  // 16-byte loads of the angles
+    if (a.interleaved && a.rotary_dim % 8 == 0 && pieces) return launch_qk<T, kPairInside>(a, s);
+    if (!a.interleaved && a.rotary_dim % 16 == 0 && pieces) return launch_qk<T, kPairLane>(a, s);
+    return launch_qk<T, kPairLoad>(a, s);
 }
 
 // ---- kv_commit_tokens ----------------------------------------------------------
