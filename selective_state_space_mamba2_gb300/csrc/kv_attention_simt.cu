@@ -1,11 +1,16 @@
 // kv_tree_attention on the CUDA cores, in fp32: every type, head size, group and page size the
 // tensor-core kernel does not take, and the kernel that joins the parts of cut items.
 //
-// Online softmax over key tiles of 32 for 16 query rows a CTA: keys and values of a tile are
-// staged in shared memory as fp32, a thread owns one row's 4 scores of a tile and an eighth of
-// its output.  Bound by shared-memory reads (one 16-byte read for 4 multiply-adds); its use is
-// fp32 decode, where few rows meet each key.
+// Online softmax over key tiles of 32 for 16 query rows a CTA.  Keys and values of a tile come into
+// shared memory by 16-byte asynchronous copies, one tile ahead, in their own type.  What bounds such a
+// kernel is the reads of shared memory (a 16-byte read of a warp takes 4 cycles whatever is shared in
+// it), so a thread takes 4 rows by 4 keys of the scores, each warp a quarter of headdim, and 4 rows by
+// 4 columns in 32 of the output, each warp a quarter of the keys: 8 reads for 64 multiply-adds, and 3
+// for 32 (a row's scores by one thread took 5 for 16: 37 us for 16 fp32 requests of up to 7 tokens
+// and 2000 cached ones, against 28 with this).  The warps' quarters are added up in shared
+// memory, the scores' per tile, the output's per item.
 #include "kv_sched.cuh"
+#include "tc_ptx.cuh"
 
 namespace ssd {
 namespace {
@@ -15,111 +20,169 @@ constexpr int kRowTile = 16;
 constexpr int kKeyShift = 5;
 constexpr int kKeyTile = 1 << kKeyShift;
 constexpr int kOverhead = 1;  // of an item, in key tiles
-constexpr int kMinUnits = 4;
-constexpr int kCtasPerSm = 4;
+constexpr int kMinUnits = 2;
+constexpr int ctas_per_sm(int nv) { return nv <= 2 ? 4 : nv <= 4 ? 3 : 2; }  // by registers
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-constexpr int smem_bytes(int D) { return (kRowTile * (D + 4) + 2 * kKeyTile * (D + 4) + kRowTile * (kKeyTile + 1)) * 4; }
+constexpr int kStages = 2;
+constexpr int kKeyPitch = kRowTile + 4;  // floats of a key's 16 scores or weights: 8 keys side by side in different banks
 
-template <typename T> __device__ __forceinline__ void load8(float (&f)[8], const T *p);
-template <> __device__ __forceinline__ void load8<float>(float (&f)[8], const float *p) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+// a row of keys or values in shared memory: 16 bytes more than it holds, so that 8 rows read side by
+// side lie in different banks
+template <typename T> __host__ __device__ constexpr int row_bytes(int D) { return D * (int)sizeof(T) + 16; }
+
+template <typename T> constexpr int smem_bytes(int D) {
+    return kRowTile * (D + 4) * 4 + kStages * 2 * kKeyTile * row_bytes<T>(D) + 5 * kKeyTile * kKeyPitch * 4;
 }
-template <> __device__ __forceinline__ void load8<__nv_bfloat16>(float (&f)[8], const __nv_bfloat16 *p) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+
+__device__ __forceinline__ float4 get4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 get4(const __nv_bfloat16 *p) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xFFFF0000u));
 }
+
+// 16 bytes to shared memory, zeros where `there` is false (src is not read then)
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // NV: 32-float pieces of a row a thread group covers, headdim <= 32 NV
 template <typename T, int NV>
-__global__ void __launch_bounds__(kThreads) kv_attention_simt_kernel(const kv_attention_args a, const kvs::Parts parts,
-                                                                  const kvs::Tiling g) {
-    extern __shared__ __align__(16) float smem[];
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NV))
+    kv_attention_simt_kernel(const kv_attention_args a, const kvs::Parts parts, const kvs::Tiling g) {
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ kvs::FindSmem find;
+    __shared__ int64_t at_rows[2][2][kKeyTile];
     const int D = a.headdim, group = a.nheads / a.kv_heads, pitch = D + 4;
-    float *sq = smem, *sk = sq + kRowTile * pitch, *sv = sk + kKeyTile * pitch, *sp = sv + kKeyTile * pitch;
-    const int tid = threadIdx.x, row = tid >> 3, sub = tid & 7;
+    const int rb = row_bytes<T>(D), tile_bytes = kKeyTile * rb;
+    float *sq = reinterpret_cast<float *>(smem);
+    uint8_t *ring = smem + kRowTile * pitch * 4;  // per stage: keys, then values
+    float *sp = reinterpret_cast<float *>(ring + kStages * 2 * tile_bytes);  // weights [key][row]
+    float *ss = sp + kKeyTile * kKeyPitch;                                    // scores' quarters [warp][key][row]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int row = tid >> 3, sub = tid & 7;           // softmax and output: a row's eighth
+    const int rg = (lane >> 3) * 4, cg = lane & 7;     // products: 4 rows, and keys or columns
+    __shared__ __align__(16) float shrinks[kRowTile];
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join kernel may be set up
     kvs::Walk w;
     if (!kvs::find_run(a, g, kMinUnits, find, parts.borders, w)) return;
     const float c = a.scale * kLog2e;
-    const int pieces = D / 8;
+    constexpr int kPer = 16 / (int)sizeof(T);  // entries of 16 bytes
+    const int pieces = D / kPer;
+    // Where tile t's keys and values are, in elements from their array's start (-1: nowhere, zeros): found
+    // by one warp a tile ahead of the copies, so that these wait for no table entry and divide nothing.
+    auto find_rows = [&](int t) {
+        const bool cached = t < w.cached_tiles;
+        const int32_t pos = (cached ? t : t - w.cached_tiles) * kKeyTile + tid;
+        int64_t k_at = -1, v_at = -1;
+        if (cached && pos < w.q.c) {
+            const int32_t col = pos / a.block_size;
+            const int32_t id = a.block_table[(int64_t)w.r * a.table_cols + col];
+            if (id >= 0 && id < a.num_blocks)
+                k_at = v_at = (int64_t)id * a.cache_block_stride +
+                              ((int64_t)(pos - col * a.block_size) * a.kv_heads + w.h) * D;
+            else
+                report(a.err_word, SSD_DEVERR_SLOT);
+        } else if (!cached && pos < w.new_seen) {
+            k_at = (int64_t)(w.q.q0 + pos) * a.k_stride + w.h * D;
+            v_at = (int64_t)(w.q.q0 + pos) * a.v_stride + w.h * D;
+        }
+        at_rows[t & 1][0][tid] = k_at;
+        at_rows[t & 1][1][tid] = v_at;
+    };
+    const int key0 = tid / pieces, piece0 = tid - key0 * pieces, key_step = kThreads / pieces,
+              piece_step = kThreads - key_step * pieces;
+    // The copies of key tile t of the current item into stage `st`.
+    auto load = [&](int t, int st) {
+        const bool cached = t < w.cached_tiles;
+        const T *kp = static_cast<const T *>(cached ? a.k_cache : a.k_new);
+        const T *vp = static_cast<const T *>(cached ? a.v_cache : a.v_new);
+        uint8_t *k_to = ring + st * 2 * tile_bytes, *v_to = k_to + tile_bytes;
+        int piece = piece0;
+        for (int key = key0; key < kKeyTile; key += key_step) {
+            const int64_t k_at = at_rows[t & 1][0][key], v_at = at_rows[t & 1][1][key];
+            const bool there = k_at >= 0;
+            copy16(k_to + key * rb + piece * 16, kp + (there ? k_at + piece * kPer : 0), there);
+            copy16(v_to + key * rb + piece * 16, vp + (there ? v_at + piece * kPer : 0), there);
+            piece += piece_step;
+            if (piece >= pieces) piece -= pieces, ++key;
+        }
+        copies_commit();
+    };
     bool more = true;
     while (more) {
         const int heads = w.heads(g, group), rows = w.tokens(g) * heads, head0 = w.h * group + w.part * g.heads;
         const int token0 = w.first_token(g);
-        // query rows
+        __syncthreads();  // the last item's readers are done
+        if (tid < kKeyTile) {
+            find_rows(w.t0);
+            if (w.t0 + 1 < w.t1) find_rows(w.t0 + 1);
+        }
         __syncthreads();
-        for (int i = tid; i < kRowTile * pieces; i += kThreads) {
-            const int r = i / pieces, e = (i % pieces) * 8;
-            float f[8] = {};
+        load(w.t0, 0);
+        // query rows
+        for (int i = tid; i < kRowTile * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), e = (i - r * (D / 4)) * 4;
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows) {
                 const int64_t tok = w.q.q0 + token0 + r / heads;
-                load8(f, static_cast<const T *>(a.q) + tok * a.q_stride + (head0 + r % heads) * D + e);
+                f = get4(static_cast<const T *>(a.q) + tok * a.q_stride + (head0 + r % heads) * D + e);
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sq[r * pitch + e + j] = f[j];
+            *reinterpret_cast<float4 *>(sq + r * pitch + e) = f;
         }
         const int32_t my_tok = row < rows ? token0 + row / heads : -1;
         const uint32_t *mask = a.tree_mask && my_tok >= 0 ? a.tree_mask + (int64_t)(w.q.q0 + my_tok) * a.mask_words : nullptr;
 
-        float top = -INFINITY, sum = 0.f, acc[NV][4] = {};
+        float top = -INFINITY, sum = 0.f;
+        float2 acc[4][NV][2] = {};
         for (int t = w.t0; t < w.t1; ++t) {
             const bool cached = t < w.cached_tiles;
             const int32_t base = (cached ? t : t - w.cached_tiles) * kKeyTile;
             const int32_t limit = cached ? w.q.c : w.new_seen;  // keys from here on do not exist
-            __syncthreads();
-            for (int i = tid; i < kKeyTile * pieces; i += kThreads) {
-                const int key = i / pieces, e = (i % pieces) * 8;
-                const int32_t pos = base + key;
-                float fk[8] = {}, fv[8] = {};
-                if (pos < limit) {
-                    if (cached) {
-                        const int32_t col = pos / a.block_size;
-                        const int32_t id = a.block_table[(int64_t)w.r * a.table_cols + col];
-                        if (id >= 0 && id < a.num_blocks) {
-                            const int64_t at = (int64_t)id * a.cache_block_stride +
-                                               ((int64_t)(pos - col * a.block_size) * a.kv_heads + w.h) * D + e;
-                            load8(fk, static_cast<const T *>(a.k_cache) + at);
-                            load8(fv, static_cast<const T *>(a.v_cache) + at);
-                        } else if (e == 0) {
-                            report(a.err_word, SSD_DEVERR_SLOT);
-                        }
-                    } else {
-                        const int64_t tok = w.q.q0 + pos;
-                        load8(fk, static_cast<const T *>(a.k_new) + tok * a.k_stride + w.h * D + e);
-                        load8(fv, static_cast<const T *>(a.v_new) + tok * a.v_stride + w.h * D + e);
-                    }
-                }
+            const int st = (t - w.t0) & 1;
+            copies_wait<0>();
+            __syncthreads();  // tile t is there, and nobody reads the other stage or the last weights any more
+            if (t + 1 < w.t1) load(t + 1, st ^ 1);
+            if (t + 2 < w.t1 && tid < kKeyTile) find_rows(t + 2);
+            const uint8_t *sk = ring + st * 2 * tile_bytes, *sv = sk + tile_bytes;
+            // scores of rows rg .. rg + 3 and keys cg + 8 j over this warp's entries, even and odd ones apart
+            float2 s2[4][4] = {};
+#pragma unroll 2
+            for (int e = 4 * warp; e < D; e += 16) {
+                float4 x[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    sk[key * pitch + e + j] = fk[j];
-                    sv[key * pitch + e + j] = fv[j];
-                }
-            }
-            __syncthreads();
-            // scores of keys sub + 8 j
-            float s[4] = {};
-            for (int e = 0; e < D; e += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(sq + row * pitch + e);
+                for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(sq + (rg + i) * pitch + e);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float4 y = *reinterpret_cast<const float4 *>(sk + (sub + 8 * j) * pitch + e);
-                    s[j] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s[j]))));
+                    const float4 y = get4(reinterpret_cast<const T *>(sk + (cg + 8 * j) * rb) + e);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        s2[i][j] = tc::fma_f2(make_float2(x[i].x, x[i].y), make_float2(y.x, y.y), s2[i][j]);
+                        s2[i][j] = tc::fma_f2(make_float2(x[i].z, x[i].w), make_float2(y.z, y.w), s2[i][j]);
+                    }
                 }
             }
-            float best = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<float4 *>(ss + (warp * kKeyTile + cg + 8 * j) * kKeyPitch + rg) =
+                    make_float4(s2[0][j].x + s2[0][j].y, s2[1][j].x + s2[1][j].y, s2[2][j].x + s2[2][j].y,
+                                s2[3][j].x + s2[3][j].y);
+            __syncthreads();
+            // softmax of row `row`, keys sub + 8 j
+            float s[4], best = -INFINITY;
             bool sees[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+                const float *q4 = ss + (sub + 8 * j) * kKeyPitch + row;
+                constexpr int kQuarter = kKeyTile * kKeyPitch;
+                s[j] = (q4[0] + q4[kQuarter]) + (q4[2 * kQuarter] + q4[3 * kQuarter]);
                 const int32_t pos = base + sub + 8 * j;
                 sees[j] = pos < limit && my_tok >= 0;
                 if (!cached && sees[j])
@@ -137,57 +200,87 @@ __global__ void __launch_bounds__(kThreads) kv_attention_simt_kernel(const kv_at
             const float shrink = exp2f(top - from);
             top = now;
             sum *= shrink;
+            if (sub == 0) shrinks[row] = shrink;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float p = exp2f(s[j] - from);
-                sp[row * (kKeyTile + 1) + sub + 8 * j] = sees[j] ? p : 0.f;
-                sum += sees[j] ? p : 0.f;
+                const float p = sees[j] ? exp2f(s[j] - from) : 0.f;
+                sp[(sub + 8 * j) * kKeyPitch + row] = p;
+                sum += p;
             }
-            __syncwarp();  // a row's weights are written and read by the same warp
+            __syncthreads();
+            // output of rows rg .. rg + 3, columns 32 v + 4 cg, over this warp's keys
+            const float4 f4 = *reinterpret_cast<const float4 *>(shrinks + rg);
+            const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[v][j] *= shrink;
-            for (int key = 0; key < kKeyTile; ++key) {
-                const float p = sp[row * (kKeyTile + 1) + key];
-                if (p == 0.f) continue;  // not seen: its value stays out, whatever it is
+                for (int v = 0; v < NV; ++v)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) acc[i][v][j] = tc::mul_f2(acc[i][v][j], make_float2(f[i], f[i]));
+            const bool all = cached && base + kKeyTile <= limit;  // every row of the item sees every key
+#pragma unroll 2
+            for (int k = 0; k < kKeyTile / 4; ++k) {
+                const int key = warp * (kKeyTile / 4) + k;
+                const float4 p4 = *reinterpret_cast<const float4 *>(sp + key * kKeyPitch + rg);
+                const float pk[4] = {p4.x, p4.y, p4.z, p4.w};
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
-                    const int e = 32 * v + 4 * sub;
-                    if (e < D) {
-                        const float4 y = *reinterpret_cast<const float4 *>(sv + key * pitch + e);
-                        acc[v][0] = fmaf(p, y.x, acc[v][0]);
-                        acc[v][1] = fmaf(p, y.y, acc[v][1]);
-                        acc[v][2] = fmaf(p, y.z, acc[v][2]);
-                        acc[v][3] = fmaf(p, y.w, acc[v][3]);
+                    const int e = 32 * v + 4 * cg;
+                    const float4 y = e < D ? get4(reinterpret_cast<const T *>(sv + key * rb) + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 p2 = make_float2(pk[i], pk[i]);
+                        if (all || pk[i] != 0.f) {  // not seen (weight 0): its value stays out, whatever it is
+                            acc[i][v][0] = tc::fma_f2(p2, make_float2(y.x, y.y), acc[i][v][0]);
+                            acc[i][v][1] = tc::fma_f2(p2, make_float2(y.z, y.w), acc[i][v][1]);
+                        }
                     }
                 }
             }
         }
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        // the warps' quarters of the output, over the ring (no copy is in flight): [warp][row][D]
+        float *quarters = reinterpret_cast<float *>(ring);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int e = 32 * v + 4 * cg;
+                if (e < D)
+                    *reinterpret_cast<float4 *>(quarters + (warp * kRowTile + rg + i) * D + e) =
+                        make_float4(acc[i][v][0].x, acc[i][v][0].y, acc[i][v][1].x, acc[i][v][1].y);
+            }
+        __syncthreads();
         if (my_tok >= 0) {
-            if (w.whole()) {
-                const int64_t out_row = (int64_t)(w.q.q0 + my_tok) * a.nheads + head0 + row % heads;
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that saw nothing: zeros
-                T *out = static_cast<T *>(a.out) + out_row * D;
+            const bool whole = w.whole();
+            const int64_t out_row = (int64_t)(w.q.q0 + my_tok) * a.nheads + head0 + row % heads;
+            const int64_t part = ((int64_t)blockIdx.x * 2 + (w.t0 > 0 ? 0 : 1)) * g.rows + row;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that saw nothing: zeros
+            T *out = static_cast<T *>(a.out) + out_row * D;
 #pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    const int e = 32 * v + 4 * sub;
-                    if (e < D)
+            for (int v = 0; v < NV; ++v) {
+                const int e = 32 * v + 4 * sub;
+                if (e >= D) continue;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) out[e + j] = from_f32<T>(acc[v][j] * inv);
+                for (int k = 0; k < 4; ++k) {
+                    const float4 x = *reinterpret_cast<const float4 *>(quarters + (k * kRowTile + row) * D + e);
+                    o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
                 }
-                if (a.lse && sub == 0) a.lse[out_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-            } else {
-                const int64_t part = ((int64_t)blockIdx.x * 2 + (w.t0 > 0 ? 0 : 1)) * g.rows + row;
-#pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    const int e = 32 * v + 4 * sub;
-                    if (e < D) *reinterpret_cast<float4 *>(parts.sums + part * D + e) =
-                        make_float4(acc[v][0], acc[v][1], acc[v][2], acc[v][3]);
+                if (whole) {
+                    out[e] = from_f32<T>(o.x * inv), out[e + 1] = from_f32<T>(o.y * inv);
+                    out[e + 2] = from_f32<T>(o.z * inv), out[e + 3] = from_f32<T>(o.w * inv);
+                } else {
+                    *reinterpret_cast<float4 *>(parts.sums + part * D + e) = o;
                 }
-                if (sub == 0) parts.stats[part] = make_float2(top, sum);
+            }
+            if (sub == 0) {
+                if (!whole)
+                    parts.stats[part] = make_float2(top, sum);
+                else if (a.lse)
+                    a.lse[out_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
             }
         }
         more = w.next(a, g);
@@ -327,8 +420,11 @@ cudaError_t launch_join(const kv_attention_args &a, const kvs::Parts &p, int gri
 
 kvs::Tiling simt_tiling(const kv_attention_args &a) { return kvs::tiling(a, kRowTile, kKeyShift, kOverhead); }
 
+// 32-float pieces of a row that the kernel for this head size covers
+int pieces_of(int D) { return D <= 64 ? 2 : D <= 128 ? 4 : 8; }
+
 int simt_grid(const kv_attention_args &a, const kvs::Tiling &g) {
-    return kvs::grid_of(a, g, kMinUnits, kCtasPerSm * device_sms());
+    return kvs::grid_of(a, g, kMinUnits, ctas_per_sm(pieces_of(a.headdim)) * device_sms());
 }
 
 template <typename T, int NV>
@@ -336,7 +432,7 @@ cudaError_t launch(const kv_attention_args &a, void *ws, cudaStream_t s) {
     const kvs::Tiling g = simt_tiling(a);
     const int grid = simt_grid(a, g);
     const kvs::Parts parts = kvs::parts_at(ws, grid, g.rows, a.headdim);
-    const int smem = smem_bytes(a.headdim);
+    const int smem = smem_bytes<T>(a.headdim);
     cudaError_t e = cudaFuncSetAttribute(kv_attention_simt_kernel<T, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     kv_attention_simt_kernel<T, NV><<<grid, kThreads, smem, s>>>(a, parts, g);
@@ -345,9 +441,8 @@ cudaError_t launch(const kv_attention_args &a, void *ws, cudaStream_t s) {
 }
 
 template <typename T> cudaError_t launch_dim(const kv_attention_args &a, void *ws, cudaStream_t s) {
-    if (a.headdim <= 64) return launch<T, 2>(a, ws, s);
-    if (a.headdim <= 128) return launch<T, 4>(a, ws, s);
-    return launch<T, 8>(a, ws, s);
+    const int pieces = pieces_of(a.headdim);
+    return pieces == 2 ? launch<T, 2>(a, ws, s) : pieces == 4 ? launch<T, 4>(a, ws, s) : launch<T, 8>(a, ws, s);
 }
 
 }  // namespace
