@@ -534,3 +534,69 @@ def test_commit_all_tokens_and_errors():
     flat = kc.flatten(0, 1)
     assert torch.isnan(flat[:3]).all() and torch.equal(flat[3], k[3]) and torch.isnan(flat[4]).all()
     assert torch.equal(flat[7], k[7]) and torch.equal(flat[9], k[10])
+
+
+# ----------------------------------------------------------------- together --
+
+def test_hybrid_tree_decode_example():
+    """The four calls beside ssm_decode_update on drafted trees give the tokens that single-token steps give, in fewer
+    steps."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "hybrid_tree_decode.py")
+    spec = importlib.util.spec_from_file_location("hybrid_tree_decode", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    same, n, plain_steps, steps = example.main()
+    assert same and n >= 12 and steps < plain_steps
+
+
+def test_calls_replay_as_a_graph():
+    """A decode step's four calls captured once: replays with new lengths, tokens and tables in the same buffers give
+    the bits of eager calls."""
+    b, S, H, G, D, n = 16, 3, 4, 2, 128, 2
+    g = torch.Generator(device=DEV).manual_seed(3)
+    T = S * n
+    ctx, new = _i([37, 0, 90]), _i([n] * S)
+    kc = torch.randn(40, b, G, D, generator=g, device=DEV).to(BF)
+    vc = torch.randn(40, b, G, D, generator=g, device=DEV).to(BF)
+    table = _i(np.zeros((S, 12)))
+    ring, state = _i(np.random.default_rng(0).permutation(np.arange(1, 40))), _i([5, 39])
+    qkv = torch.randn(T, (H + 2 * G) * D, generator=g, device=DEV).to(BF)
+    cs = torch.randn(256, D, generator=g, device=DEV)
+    zero = _i([0] * S)
+    keep = {}
+
+    def step():
+        q, k, v = (t.unflatten(1, (-1, D)) for t in qkv.split([H * D, G * D, G * D], 1))
+        m = ssd.kv_block_tables(ctx, new, zero, table, ring, state, b, 40, T)
+        q, k = ssd.kv_qk_norm_rope(q, k, m["positions"], cs)
+        o, lse = ssd.kv_tree_attention(q, k, v, kc, vc, m["cu_seqlens"], ctx, table, n, return_lse=True)
+        c = ssd.kv_commit_tokens(k, v, kc, vc, m["slots"], m["cu_seqlens"], ctx)
+        keep.update(m=m, o=o, lse=lse, c=c)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    captured = dict(keep)
+    ctx.copy_(_i([80, 3, 17]))
+    qkv.normal_(generator=g)
+    before = kc.clone(), vc.clone(), table.clone()
+    graph.replay()
+    torch.cuda.synchronize()
+    after = kc.clone(), vc.clone(), table.clone()
+    for t, old in zip((kc, vc, table), before):
+        t.copy_(old)
+    step()
+    torch.cuda.synchronize()
+    for key in keep["m"]:
+        assert torch.equal(keep["m"][key], captured["m"][key]), key
+    assert torch.equal(keep["o"], captured["o"]) and torch.equal(keep["lse"], captured["lse"])
+    assert torch.equal(keep["c"], captured["c"])
+    for t, got in zip((kc, vc, table), after):
+        assert torch.equal(t, got)
