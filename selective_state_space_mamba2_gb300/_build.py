@@ -92,7 +92,8 @@ def _link_calls(obj: str) -> None:
     tmp = CALLS_LIB + ".tmp.%d" % os.getpid()
     # torch's libraries are loaded already when the module is; ours is found beside it
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
-           "-L", os.path.join(_torch_dir(), "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_cuda"]
+           "-L", os.path.join(_torch_dir(), "lib"), "-lc10", "-ltorch_cpu", "-ltorch_cuda",
+           "-ltorch_python", "-lc10_cuda"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (res.stdout, res.stderr))

@@ -7,6 +7,7 @@
 // is refused raises ValueError; a status other than SSD_OK comes back as a Python int, which the
 // binding raises as SSDError.
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <Python.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -150,7 +151,15 @@ ssd_stream_t stream_of(PyObject *o, const at::Tensor &like) {
 }
 
 at::Tensor empty(at::IntArrayRef shape, ScalarType type, const at::Tensor &like) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
+    return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
+}
+
+// A dense int32 tensor of n entries in `room`'s memory, from entry `at` on.
+at::Tensor piece_of(const at::Tensor &room, int64_t n, int64_t at) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(room.storage()), room.key_set(), room.dtype());
+    t.unsafeGetTensorImpl()->set_storage_offset(at);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+    return t;
 }
 
 PyObject *status(ssd_status_t s) { return PyLong_FromLong((long)s); }
@@ -175,8 +184,11 @@ PyObject *block_tables(PyObject *const *a, PyObject *) {
     p.max_tokens = int32(a[8], "max_tokens");
     p.null_block_id = int32(a[9], "null_block_id");
     if (p.max_tokens < 0) refuse("max_tokens must not be negative");
-    static const char *const names[7] = {"cu_seqlens", "seq_lens", "reserved_lens", "ring_state", "slots", "positions",
-                                         "token_req"};
+    static const char *const keys[7] = {"cu_seqlens", "seq_lens", "reserved_lens", "ring_state", "slots", "positions",
+                                        "token_req"};
+    static PyObject *names[7] = {};  // made once, as attribute names are (under the interpreter's lock)
+    for (int i = 0; i < 7 && !names[i]; ++i)
+        if (!(names[i] = PyUnicode_InternFromString(keys[i]))) throw PythonError{};
     const int64_t sizes[7] = {S + 1, S, S, 2, p.max_tokens, p.max_tokens, p.max_tokens};
     int32_t *ptr[7] = {};
     PyObject *out = a[10];
@@ -188,14 +200,9 @@ PyObject *block_tables(PyObject *const *a, PyObject *) {
         out = PyDict_New();
         if (!out) throw PythonError{};
         for (int i = 0; i < 7; ++i) {
-            at::Tensor t;
-            {
-                at::AutoDispatchBelowADInplaceOrView no_grad;  // plain views: nothing here has gradients
-                t = room.as_strided(sizes[i], 1, at[i]);
-            }
             ptr[i] = static_cast<int32_t *>(room.data_ptr()) + at[i];
-            PyObject *w = THPVariable_Wrap(std::move(t));
-            const int bad = w ? PyDict_SetItemString(out, names[i], w) : -1;
+            PyObject *w = THPVariable_Wrap(piece_of(room, sizes[i], at[i]));
+            const int bad = w ? PyDict_SetItem(out, names[i], w) : -1;
             Py_XDECREF(w);
             if (bad) {
                 Py_DECREF(out);
@@ -204,14 +211,14 @@ PyObject *block_tables(PyObject *const *a, PyObject *) {
         }
     } else {
         for (int i = 0; i < 7; ++i) {
-            PyObject *t = PyMapping_GetItemString(out, names[i]);
+            PyObject *t = PyObject_GetItem(out, names[i]);
             if (!t) {
                 if (i < 6) throw PythonError{};
                 PyErr_Clear();  // token_req may be left out
                 continue;
             }
             Py_DECREF(t);  // the mapping keeps it
-            if (i < 6 || t != Py_None) ptr[i] = const_cast<int32_t *>(ints(t, names[i], sizes[i]));
+            if (i < 6 || t != Py_None) ptr[i] = const_cast<int32_t *>(ints(t, keys[i], sizes[i]));
         }
         Py_INCREF(out);
     }

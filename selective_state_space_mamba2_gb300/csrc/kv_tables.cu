@@ -1,13 +1,12 @@
 // kv_block_tables: block tables, slot map and positions of one step from the requests' lengths.
 //
-// Everything a token needs follows from three prefix sums over the requests (tokens, blocks
-// taken) and its own request's lengths, so one launch does it all: every CTA scans all S
-// requests (12 bytes each, from L2 after the first CTA) and then writes only its own tile of
-// tokens; no CTA waits for another's result.  A block's table entry is written by the CTA that
-// owns the block's first new token.  Requests with many tokens in a tile are queued and
-// written by the whole CTA, the others by the thread that scanned them.
-// What bounds it: 12 bytes per token at HBM speed in large steps, launch and two dependent
-// rounds of loads in small ones.
+// Everything a token needs follows from two prefix sums over the requests (tokens, blocks taken)
+// and its own request's lengths, so one launch does it all: every CTA scans all S requests (12
+// bytes each, from L2 after the first CTA) and then writes only its own tile of tokens; no CTA
+// waits for another's result.  A token finds its request by bisection among the 512 just scanned,
+// in shared memory.  A block's table entry is written by the thread of the block's first new token.
+// What bounds it: 12 bytes per token in large steps (524672 tokens of 392 requests: MEASURED us, of
+// which 2 are the launch), two dependent rounds of loads in small ones (256 requests of 4: 4.2 us).
 #include "kv.cuh"
 
 namespace ssd {
@@ -15,13 +14,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kTile = 2048;   // tokens of a CTA
-constexpr int kInline = 8;    // tokens of a request in a tile that its scanning thread writes itself
-constexpr int kQueue = kTile / (kInline + 1) + 2;
-
-struct Span {  // tokens [t0, t1) of request r
-    int32_t t0, t1, r, pos0, held, taken;
-    bool begins;  // t0 is the request's first new token
-};
+constexpr int kPer = kTile / kThreads;  // of a thread
 
 __device__ __forceinline__ int32_t blocks_of(int32_t tokens, int32_t b) { return tokens / b + (tokens % b != 0); }
 
@@ -51,8 +44,8 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const kv_tables_arg
     constexpr int kWarps = kThreads / 32;
     __shared__ unsigned long long warp_tokens[kWarps], warp_pops[kWarps];
     __shared__ uint32_t warp_bad[kWarps];
-    __shared__ Span queue[kQueue];
-    __shared__ int queued;
+    // of the chunk's requests: first packed token, context, blocks held, blocks taken before
+    __shared__ int32_t first_of[kThreads], context_of[kThreads], held_of[kThreads], taken_of[kThreads];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = a.num_reqs, b = a.block_size;
     const int32_t head = a.ring_in[0], count = a.ring_in[1];
@@ -76,7 +69,6 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const kv_tables_arg
         bad = __reduce_or_sync(~0u, bad);
         __syncthreads();  // the last chunk's readers are done
         if (lane == 31) warp_tokens[warp] = ns, warp_pops[warp] = ps, warp_bad[warp] = bad;
-        if (tid == 0) queued = 0;
         __syncthreads();
         tokens_before = ns - n, pops_before = ps - p;
         tokens_all = pops_all = 0;
@@ -103,10 +95,18 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const kv_tables_arg
         bad |= SSD_DEVERR_BLOCKS;
     const bool ok = bad == 0;
     // entry `off` of the ring from its head on; head and off are below its capacity
-    auto ring_id = [&](int32_t off) {
+    auto ring_entry = [&](int32_t off) {
         uint32_t i = (uint32_t)head + (uint32_t)off;
         if (i >= (uint32_t)a.free_capacity) i -= (uint32_t)a.free_capacity;
-        return a.free_ring[i];
+        return a.free_ring + i;
+    };
+    // block and offset of a position: the high word of a product with floor((2^32 - 1) / b) is the
+    // quotient or one less, positions being below 2^31
+    const uint32_t inv_b = 0xFFFFFFFFu / (uint32_t)b;
+    auto block_of = [&](int32_t p, int32_t &col, int32_t &off) {
+        uint32_t q = __umulhi((uint32_t)p, inv_b), r = (uint32_t)p - q * (uint32_t)b;
+        if (r >= (uint32_t)b) ++q, r -= (uint32_t)b;
+        col = (int32_t)q, off = (int32_t)r;
     };
     if (blockIdx.x == 0 && tid == 0) {
         if (!ok) report(a.err_word, bad);
@@ -127,28 +127,6 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const kv_tables_arg
         if (a.token_req) a.token_req[i] = -1;
     }
 
-    auto token = [&](int32_t i, int32_t r, int32_t pos, int32_t held, int32_t taken, bool first) {
-        const int32_t col = pos / b, off = pos - col * b;
-        int32_t *row = a.block_table + (int64_t)r * a.table_cols;
-        int32_t id;
-        if (col < held) {
-            id = row[col];
-        } else {
-            id = ring_id(taken + (col - held));
-            if (off == 0 || first) row[col] = id;
-        }
-        int32_t slot = -1;
-        if (id != a.null_block_id) {
-            if (id < 0 || id >= a.num_blocks)
-                report(a.err_word, SSD_DEVERR_SLOT);
-            else
-                slot = id * b + off;
-        }
-        a.slots[i] = slot;
-        a.positions[i] = pos;
-        if (a.token_req) a.token_req[i] = r;
-    };
-
     unsigned long long tokens_carry = 0, pops_carry = 0;
     for (int base = 0, chunk = 0; base < S; base += kThreads, ++chunk) {
         if (S > kThreads) scan(base);  // else the scan above still holds
@@ -167,23 +145,51 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const kv_tables_arg
                 // new blocks that no new token falls into
                 const int32_t last = !ok ? l.held : n > 0 ? min(l.need, l.c / b) : l.need;
                 for (int col = l.held; col < last; ++col)
-                    a.block_table[(int64_t)r * a.table_cols + col] = ring_id(taken + (col - l.held));
-            }
-            const int32_t t0 = max(first, tile0), t1 = min(first + n, tile1);
-            if (t1 > t0) {
-                if (t1 - t0 <= kInline) {
-                    for (int i = t0; i < t1; ++i) token(i, r, l.c + (i - first), l.held, taken, i == first);
-                } else {
-                    queue[atomicAdd(&queued, 1)] = Span{t0, t1, r, l.c + (t0 - first), l.held, taken, t0 == first};
-                }
+                    a.block_table[(int64_t)r * a.table_cols + col] = *ring_entry(taken + (col - l.held));
             }
         }
+        first_of[tid] = first, context_of[tid] = l.c, held_of[tid] = l.held, taken_of[tid] = taken;
         __syncthreads();
-        const int nq = queued;
-        for (int q = 0; q < nq; ++q) {
-            const Span s = queue[q];
-            for (int i = s.t0 + tid; i < s.t1; i += kThreads)
-                token(i, s.r, s.pos0 + (i - s.t0), s.held, s.taken, s.begins && i == s.t0);
+        // the chunk's tokens in this tile
+        const int32_t from = max(first_of[0], tile0), to = min((int32_t)(ok ? tokens_carry : 0), tile1);
+        if (from >= to) continue;
+        // The last request that starts at token i or before it: the ones without tokens start where the
+        // next does.  No branches: the bisections of a thread's tokens run side by side.
+        int at[kPer] = {};
+#pragma unroll
+        for (int step = kThreads / 2; step > 0; step /= 2)
+#pragma unroll
+            for (int k = 0; k < kPer; ++k)
+                if (first_of[at[k] + step] <= min(max(tile0 + tid + k * kThreads, from), to - 1)) at[k] += step;
+        int32_t pos[kPer], col[kPer], off[kPer], id[kPer];
+        bool entry[kPer];  // the first new token of a new block
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int32_t i = min(max(tile0 + tid + k * kThreads, from), to - 1);
+            pos[k] = context_of[at[k]] + (i - first_of[at[k]]);
+            block_of(pos[k], col[k], off[k]);
+            const int32_t fresh = col[k] - held_of[at[k]];
+            const int32_t *src = fresh < 0 ? a.block_table + (int64_t)(base + at[k]) * a.table_cols + col[k]
+                                           : ring_entry(taken_of[at[k]] + fresh);
+            id[k] = *src;
+            entry[k] = fresh >= 0 && (off[k] == 0 || i == first_of[at[k]]);
+        }
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int32_t i = tile0 + tid + k * kThreads;
+            if (i < from || i >= to) continue;
+            const int32_t req = base + at[k];
+            if (entry[k]) a.block_table[(int64_t)req * a.table_cols + col[k]] = id[k];
+            int32_t slot = -1;
+            if (id[k] != a.null_block_id) {
+                if (id[k] < 0 || id[k] >= a.num_blocks)
+                    report(a.err_word, SSD_DEVERR_SLOT);
+                else
+                    slot = id[k] * b + off[k];
+            }
+            a.slots[i] = slot;
+            a.positions[i] = pos[k];
+            if (a.token_req) a.token_req[i] = req;
         }
     }
 }
