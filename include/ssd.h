@@ -567,8 +567,9 @@ SSD_API ssd_status_t mamba1_state_update(const mamba1_args *args, ssd_stream_t s
  * empty step: cu_seqlens all 0, every row padding, seq_lens = context_lens,
  * reserved_out = reserved_lens, ring_out = ring_in.
  * Inputs and outputs must not overlap (ring_out is not ring_in, reserved_out
- * not reserved_lens).  Host checks: sizes, pointers,
- * num_blocks * block_size < 2^31 (slots are 32 bits wide).  One kernel.
+ * not reserved_lens).  Host checks: sizes, pointers, no output that starts
+ * where an input does, num_blocks * block_size < 2^31 (slots are 32 bits
+ * wide).  One kernel.
  */
 typedef struct kv_tables_args {
     int32_t num_reqs;      /* S */
@@ -652,8 +653,8 @@ SSD_API ssd_status_t kv_qk_norm_rope(const kv_qk_args *args, ssd_stream_t stream
  * over what it sees; a token that sees nothing gets out = 0, lse = -inf.  What
  * is not seen does not enter the result whatever it holds (NaN in stale page
  * rows, in rejected drafts).  Softmax statistics and sums are fp32.
- * bf16 with headdim 64 or 128, at most 128 query heads to a key head, block_size a
- * multiple of 8 and 16-byte strides runs on the tensor cores, its probabilities
+ * bf16 with headdim 64 or 128, at most 128 query heads to a key head, block_size
+ * a multiple of 8 and a positive scale runs on the tensor cores, its probabilities
  * rounded to bf16; everything else, fp32 above all, on the CUDA cores in fp32.
  *
  * Work is cut into equal shares over the GPU along requests, heads, query

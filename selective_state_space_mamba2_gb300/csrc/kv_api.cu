@@ -32,10 +32,16 @@ ssd_status_t check_tables(const kv_tables_args *a) {
     if (a->num_reqs < 0 || a->max_tokens < 0 || a->block_size < 1 || a->table_cols < 0 || a->free_capacity < 0 ||
         a->num_blocks < 0 || (int64_t)a->block_size * a->num_blocks >= (int64_t{1} << 31))
         return SSD_ERR_INVALID_ARG;
-    if (!a->ring_in || !a->ring_out || !a->cu_seqlens || a->ring_in == a->ring_out) return SSD_ERR_INVALID_ARG;
-    if (a->num_reqs > 0 && (!a->context_lens || !a->new_lens || !a->reserved_lens || !a->seq_lens ||
-                            !a->reserved_out || a->reserved_lens == a->reserved_out))
+    if (!a->ring_in || !a->ring_out || !a->cu_seqlens) return SSD_ERR_INVALID_ARG;
+    if (a->num_reqs > 0 && (!a->context_lens || !a->new_lens || !a->reserved_lens || !a->seq_lens || !a->reserved_out))
         return SSD_ERR_INVALID_ARG;
+    // every CTA reads the inputs again while others write outputs already
+    const int32_t *const outs[] = {a->ring_out, a->cu_seqlens, a->seq_lens, a->reserved_out, a->slots, a->positions,
+                                   a->token_req};
+    const int32_t *const ins[] = {a->context_lens, a->new_lens, a->reserved_lens, a->ring_in, a->free_ring, a->block_table};
+    for (const int32_t *o : outs)
+        for (const int32_t *i : ins)
+            if (o && o == i) return SSD_ERR_INVALID_ARG;
     if (a->num_reqs > 0 && a->table_cols > 0 && !a->block_table) return SSD_ERR_INVALID_ARG;
     if (a->free_capacity > 0 && !a->free_ring) return SSD_ERR_INVALID_ARG;
     if (a->max_tokens > 0 && (!a->slots || !a->positions)) return SSD_ERR_INVALID_ARG;
@@ -81,7 +87,7 @@ ssd_status_t check_attention(const kv_attention_args *a) {
         return SSD_ERR_INVALID_ARG;
     const int64_t row = (int64_t)a->kv_heads * a->headdim;
     if (!pages_ok(a->block_size, a->num_blocks, a->cache_block_stride, row, a->dtype) ||
-        (int64_t)a->table_cols * a->block_size >= (int64_t{1} << 31))
+        (int64_t)a->table_cols * a->block_size > INT32_MAX - 1024)  // positions up to a key tile's end fit 32 bits
         return SSD_ERR_INVALID_ARG;
     if (!stride_ok(a->q_stride, (int64_t)a->nheads * a->headdim, a->dtype) ||
         !stride_ok(a->k_stride, row, a->dtype) || !stride_ok(a->v_stride, row, a->dtype))

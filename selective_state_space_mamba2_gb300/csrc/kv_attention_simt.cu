@@ -423,8 +423,14 @@ kvs::Tiling simt_tiling(const kv_attention_args &a) { return kvs::tiling(a, kRow
 // 32-float pieces of a row that the kernel for this head size covers
 int pieces_of(int D) { return D <= 64 ? 2 : D <= 128 ? 4 : 8; }
 
+int smem_of(const kv_attention_args &a) {
+    return a.dtype == SSD_BF16 ? smem_bytes<__nv_bfloat16>(a.headdim) : smem_bytes<float>(a.headdim);
+}
+
 int simt_grid(const kv_attention_args &a, const kvs::Tiling &g) {
-    return kvs::grid_of(a, g, kMinUnits, ctas_per_sm(pieces_of(a.headdim)) * device_sms());
+    const int by_smem = (227 * 1024) / (smem_of(a) + 3 * 1024);  // with what a CTA takes besides
+    const int ctas = ctas_per_sm(pieces_of(a.headdim));
+    return kvs::grid_of(a, g, kMinUnits, (by_smem < ctas ? by_smem : ctas) * device_sms());
 }
 
 template <typename T, int NV>
@@ -432,7 +438,7 @@ cudaError_t launch(const kv_attention_args &a, void *ws, cudaStream_t s) {
     const kvs::Tiling g = simt_tiling(a);
     const int grid = simt_grid(a, g);
     const kvs::Parts parts = kvs::parts_at(ws, grid, g.rows, a.headdim);
-    const int smem = smem_bytes<T>(a.headdim);
+    const int smem = smem_of(a);
     cudaError_t e = cudaFuncSetAttribute(kv_attention_simt_kernel<T, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     kv_attention_simt_kernel<T, NV><<<grid, kThreads, smem, s>>>(a, parts, g);

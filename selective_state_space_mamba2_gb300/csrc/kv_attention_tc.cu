@@ -553,10 +553,11 @@ template <int D> cudaError_t launch(const kv_attention_args &a, void *ws, cudaSt
 }  // namespace
 
 // A rule on sizes alone: what the TMA boxes and the two products take.  A negative scale would
-// turn the maximum of the scores into that of their opposites.
+// turn the maximum of the scores into that of their opposites, and zero times the minus infinity
+// that stands for a masked score is NaN.
 bool kv_attention_tc_supported(const kv_attention_args &a) {
     return a.dtype == SSD_BF16 && (a.headdim == 64 || a.headdim == 128) && a.nheads / a.kv_heads <= kRows &&
-           a.block_size % 8 == 0 && a.scale >= 0.f && a.cache_block_stride < (int64_t{1} << 38) &&
+           a.block_size % 8 == 0 && a.scale > 0.f && a.cache_block_stride < (int64_t{1} << 38) &&
            a.q_stride < (int64_t{1} << 38) && a.k_stride < (int64_t{1} << 38) && a.v_stride < (int64_t{1} << 38);
 }
 

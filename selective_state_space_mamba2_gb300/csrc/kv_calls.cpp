@@ -9,6 +9,7 @@
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <Python.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -162,6 +163,15 @@ at::Tensor piece_of(const at::Tensor &room, int64_t n, int64_t at) {
     return t;
 }
 
+// Memory made here on the current stream and used on another: not handed out again before that other
+// stream is done with it.
+void used_on(const at::Tensor &t, ssd_stream_t s) {
+    const auto dev = t.get_device();
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
+    if (cs != c10::cuda::getCurrentCUDAStream(dev).stream())
+        c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), c10::cuda::getStreamFromExternal(cs, dev));
+}
+
 PyObject *status(ssd_status_t s) { return PyLong_FromLong((long)s); }
 
 PyObject *block_tables(PyObject *const *a, PyObject *) {
@@ -192,11 +202,12 @@ PyObject *block_tables(PyObject *const *a, PyObject *) {
     const int64_t sizes[7] = {S + 1, S, S, 2, p.max_tokens, p.max_tokens, p.max_tokens};
     int32_t *ptr[7] = {};
     PyObject *out = a[10];
+    at::Tensor room;
     if (out == Py_None) {
         // one allocation, each output at a 64-byte boundary of it
         int64_t at[7], all = 0;
         for (int i = 0; i < 7; ++i) at[i] = all, all += (sizes[i] + 15) / 16 * 16;
-        const at::Tensor room = empty(all, at::kInt, ctx);
+        room = empty(all, at::kInt, ctx);
         out = PyDict_New();
         if (!out) throw PythonError{};
         for (int i = 0; i < 7; ++i) {
@@ -227,7 +238,9 @@ PyObject *block_tables(PyObject *const *a, PyObject *) {
     ssd_status_t s;
     try {
         p.err_word = error_word(a[11]);
-        s = kv_block_tables(&p, stream_of(a[12], ctx));
+        const ssd_stream_t stream = stream_of(a[12], ctx);
+        s = kv_block_tables(&p, stream);
+        if (room.defined()) used_on(room, stream);
     } catch (...) {
         Py_DECREF(out);
         throw;
@@ -283,7 +296,10 @@ PyObject *norm_rope(PyObject *const *a, PyObject *) {
         p.k_out = dense(a[13], "k_out", ks, type);
     }
     p.err_word = error_word(a[14]);
-    const ssd_status_t s = kv_qk_norm_rope(&p, stream_of(a[15], q));
+    const ssd_stream_t stream = stream_of(a[15], q);
+    const ssd_status_t s = kv_qk_norm_rope(&p, stream);
+    for (const at::Tensor *t : {&q_new, &k_new})
+        if (t->defined()) used_on(*t, stream);
     if (s != SSD_OK) return status(s);
     PyObject *qo = a[12] == Py_None ? THPVariable_Wrap(std::move(q_new)) : Py_NewRef(a[12]);
     PyObject *ko = a[13] == Py_None ? THPVariable_Wrap(std::move(k_new)) : Py_NewRef(a[13]);
@@ -345,7 +361,11 @@ PyObject *tree_attention(PyObject *const *a, PyObject *) {
     } else {
         room = tensor(a[14], "workspace");
     }
-    const ssd_status_t s = kv_tree_attention(&p, room.data_ptr(), (size_t)room.nbytes(), stream_of(a[16], q));
+    const ssd_stream_t stream = stream_of(a[16], q);
+    const ssd_status_t s = kv_tree_attention(&p, room.data_ptr(), (size_t)room.nbytes(), stream);
+    if (a[14] == Py_None) used_on(room, stream);
+    for (const at::Tensor *t : {&out, &lse})
+        if (t->defined()) used_on(*t, stream);
     if (s != SSD_OK) return status(s);
     PyObject *oo = a[11] == Py_None ? THPVariable_Wrap(std::move(out)) : Py_NewRef(a[11]);
     if (!with_lse || !oo) return oo;
@@ -400,7 +420,9 @@ PyObject *commit_tokens(PyObject *const *a, PyObject *) {
         }
     }
     p.err_word = error_word(a[10]);
-    const ssd_status_t s = kv_commit_tokens(&p, stream_of(a[11], k));
+    const ssd_stream_t stream = stream_of(a[11], k);
+    const ssd_status_t s = kv_commit_tokens(&p, stream);
+    if (made.defined()) used_on(made, stream);
     if (s != SSD_OK) return status(s);
     if (made.defined()) return THPVariable_Wrap(std::move(made));
     return Py_NewRef(out);

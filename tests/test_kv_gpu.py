@@ -181,6 +181,31 @@ def test_norm_rope(dtype, D, rot, inter, H, Hkv, T):
     assert torch.isnan(rest).all()
 
 
+@pytest.mark.parametrize("dtype,D,rot,inter", [(BF, 128, 128, False), (F32, 80, 40, False), (BF, 64, 64, True)])
+def test_norm_rope_more_tokens_than_ctas(dtype, D, rot, inter):
+    """Tokens beyond the grid: every CTA walks over several, one of them with a position that is none."""
+    T, H, Hkv = 2500, 3, 1
+    g = torch.Generator(device=DEV).manual_seed(D)
+    q, k = torch.randn(T, H, D, generator=g, device=DEV).to(dtype), torch.randn(T, Hkv, D, generator=g, device=DEV).to(dtype)
+    w = torch.randn(D, generator=g, device=DEV)
+    cs = torch.randn(3000, rot, generator=g, device=DEV)
+    at = np.arange(T)
+    at[7] = 3000
+    kc, vc = F.poison((320, 8, Hkv, D), dtype, DEV), F.poison((320, 8, Hkv, D), dtype, DEV)
+    slots = np.random.default_rng(0).permutation(2560)[:T]
+    qo, ko, err = F.poison(q.shape, dtype, DEV), F.poison(k.shape, dtype, DEV), _err()
+    ssd.kv_qk_norm_rope(q, k, _i(at), cs, w, w, 1e-6, inter, k, kc, vc, _i(slots), q_out=qo, k_out=ko, err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 2 and torch.isnan(qo[7]).all() and torch.isnan(ko[7]).all()
+    keep = torch.arange(T) != 7
+    at[7] = 0
+    for got, x in ((qo, q), (ko, k)):
+        want, mag = F.norm_rope(x, w, cs, _i(at), 1e-6, inter)
+        assert ((got.double().cpu() - want).abs() <= F.rope_bound(want, mag, D, dtype))[keep].all()
+    rows = torch.from_numpy(slots[keep.numpy()]).to(DEV)
+    assert torch.equal(kc.flatten(0, 1)[rows], ko[keep.to(DEV)]) and torch.equal(vc.flatten(0, 1)[rows], k[keep.to(DEV)])
+
+
 @pytest.mark.parametrize("rot", [64, 40])
 def test_norm_rope_in_place_and_without_norm(rot):
     T, H, Hkv, D = 9, 3, 3, 64
@@ -352,6 +377,17 @@ def test_attention_long_caches_are_split(dtype, H, Hkv, D):
     _check(_attn(dtype, H, Hkv, D, 16, [1, 2, 1], [20011, 5, 700], False, seed=9))
 
 
+@pytest.mark.parametrize("dtype,H,Hkv,D", [(BF, 2, 1, 64), (BF, 4, 4, 128), (F32, 2, 1, 64)])
+def test_attention_many_requests(dtype, H, Hkv, D):
+    """More requests than a CTA has threads, most of them without new tokens, so that runs begin and end anywhere."""
+    rng = np.random.default_rng(31)
+    S = 450
+    new = (rng.integers(1, 4, S) * (rng.random(S) < 0.3)).tolist()
+    new[-1] = 2
+    ctx = rng.integers(0, 150, S).tolist()
+    _check(_attn(dtype, H, Hkv, D, 16, new, ctx, False, seed=31))
+
+
 @pytest.mark.parametrize("dtype,D", [(BF, 128), (BF, 64), (F32, 64)])
 def test_attention_nan_drafts_stay_out(dtype, D):
     """A draft whose key and value are NaN touches nobody but itself."""
@@ -383,6 +419,35 @@ def test_attention_infinite_values(dtype):
 def test_attention_score_ranges(dtype, gain):
     """Peaked scores (hundreds apart, so running maxima jump), and equal ones."""
     _check(_attn(dtype, 8, 2, 128, 16, [4, 1, 33], [500, 1000, 77], False, seed=6, qk_gain=gain))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1.7])
+def test_attention_scales(dtype, scale):
+    """Any finite scale, zero (the mean of what is seen) and negative ones among them."""
+    _check(_attn(dtype, 4, 2, 64, 16, [3, 1, 20], [100, 40, 0], True, seed=14, scale=scale))
+
+
+def test_attention_outputs_made_for_another_stream():
+    """Outputs and workspace that a call allocates itself, used on a stream other than the current one, are not handed
+    out again while that stream still works on them."""
+    c = _attn(BF, 8, 2, 128, 16, [2, 1, 30], [3000, 40, 900], False, seed=23)
+    want, lse = _run(c, _err())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    mask = None
+    args = (c["q"], c["k"], c["v"], c["kc"], c["vc"], _i(c["cu"]), _i(c["ctx"]), _i(c["table"]), c["max_new"])
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        out, l2 = ssd.kv_tree_attention(*args, tree_mask=mask, return_lse=True, stream=s)
+        outs.append((out, l2))
+        del out, l2
+        for size in (1 << 12, 1 << 20, 1 << 22):  # would land in the freed workspace
+            torch.full((size,), float("nan"), device=DEV)
+    torch.cuda.synchronize()
+    for out, l2 in outs:
+        assert torch.equal(out, want) and torch.equal(l2, lse)
 
 
 def test_attention_does_not_depend_on_the_hint():

@@ -35,7 +35,8 @@ def _tables(**over):
 
 @pytest.mark.parametrize("over", [dict(num_reqs=-1), dict(block_size=0), dict(max_tokens=-1), dict(table_cols=-1),
                                   dict(block_size=1 << 16, num_blocks=1 << 15), dict(ring_in=None),
-                                  dict(ring_out=0x60000), dict(reserved_out=0x30000), dict(context_lens=None),
+                                  dict(ring_out=0x60000), dict(reserved_out=0x30000), dict(seq_lens=0x10000),
+                                  dict(cu_seqlens=0x20000), dict(slots=0x50000), dict(context_lens=None),
                                   dict(block_table=None), dict(free_ring=None), dict(slots=None)])
 def test_tables_refusals(lib, over):
     assert lib.kv_block_tables(ctypes.byref(_tables(**over)), None) == B.SSD_ERR_INVALID_ARG
