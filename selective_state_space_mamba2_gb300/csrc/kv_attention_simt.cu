@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NV))
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join kernel may be set up
     kvs::Walk w;
-    if (!kvs::find_run(a, g, kMinUnits, find, parts.borders, w)) return;
+    if (!kvs::find_run(a, g, kMinUnits, blockIdx.x, gridDim.x, find, parts.borders, w)) return;
     const float c = a.scale * kLog2e;
     constexpr int kPer = 16 / (int)sizeof(T);  // entries of 16 bytes
     const int pieces = D / kPer;

@@ -15,6 +15,12 @@
 // warps 0-3 softmax and output, warp 4 TMA loads, warp 5 the products.  Keys and values pass
 // through one ring of 64-row tiles in the order they are used: K0 K1 V0 K2 V1 ...
 //
+// Requests of more rows than a tile takes (prompts, larger trees) are worked on by pairs of CTAs, a
+// cluster of two: an item is then two row tiles, one a CTA, and both walk over the same keys.  CTA 0
+// of the pair loads each tile of keys into both CTAs' shared memory (TMA multicast), CTA 1 each
+// tile of values, so a pair reads from L2 what one CTA alone would; a slot of the ring is loaded again
+// when the products of both have read it (tcgen05.commit to both CTAs' barriers).
+//
 // Masked places: a score that must not count is replaced, not added to, so a NaN key is harmless.
 // A value enters the product whatever its weight, so in tiles with rows that are not there or
 // that some query does not see, the rows that are not there are zeroed in shared memory, and
@@ -48,6 +54,7 @@ struct TcParams {
     kv_attention_args a;
     kvs::Parts parts;
     kvs::Tiling g;
+    int32_t tile_tokens;  // tokens of a row tile
     uint32_t group_inv;   // ceil(2^16 / query heads per key head): row / group = row * group_inv >> 16, row < 128
     int32_t box_rows;     // rows of a page that one copy brings: divides block_size and kKeys
     int32_t new_rows;     // rows of new tokens that one copy brings
@@ -167,7 +174,7 @@ __device__ __noinline__ void add_nonfinite(const kv_attention_args &a, const kvs
     }
 }
 
-template <int D>
+template <int D, int kPair>
 __global__ void __launch_bounds__(kThreads, 2)
     kv_attention_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKc,
                            const __grid_constant__ CUtensorMap tmVc, const __grid_constant__ CUtensorMap tmKn,
@@ -180,6 +187,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const kv_attention_args &a = p.a;
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
     const int group = a.nheads / a.kv_heads;
+    const int rank = kPair > 1 ? (int)cluster_rank() : 0, worker = blockIdx.x / kPair;
+    constexpr uint16_t kBoth = 3;
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + L::kBars);
     uint32_t *sTmem = reinterpret_cast<uint32_t *>(smem + L::kMisc);
     volatile int *dead = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
@@ -198,18 +207,23 @@ __global__ void __launch_bounds__(kThreads, 2)
         tma_prefetch_desc(&tmVc);
         tma_prefetch_desc(&tmKn);
         tma_prefetch_desc(&tmVn);
-        for (int i = 0; i < NUM_BARS; ++i) mbar_init(&bar[i], i == P_READY0 || i == P_READY1 ? 4 : 1);
+        for (int i = 0; i < NUM_BARS; ++i)
+            mbar_init(&bar[i], i == P_READY0 || i == P_READY1 ? 4 : i >= KV_EMPTY0 ? kPair : 1);
         fence_mbar_init();
         *dead = 0;
         dirty[0] = dirty[1] = 0;
     }
     kvs::Walk w;
     const bool work =
-        kvs::find_run(a, p.g, kMinUnits, *reinterpret_cast<kvs::FindSmem *>(smem + L::kFind), p.parts.borders, w);
+        kvs::find_run(a, p.g, kMinUnits, worker, gridDim.x / kPair, *reinterpret_cast<kvs::FindSmem *>(smem + L::kFind),
+                      p.parts.borders, w);
     const bool aligned = (smem_u32(smem) & 1023u) == 0;  // the swizzled tiles need a 1024-byte aligned base
     if (!aligned && tid == 0) report(a.err_word, SSD_DEVERR_INTERNAL);
     tc_fence_before();
-    __syncthreads();
+    if (kPair > 1)
+        cluster_sync();  // both CTAs' barriers are set up
+    else
+        __syncthreads();
     tc_fence_after();
     const uint32_t tm = *sTmem;
     const Waiter wait{dead, a.err_word, p.wait_limit};
@@ -245,19 +259,28 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const uint32_t n = __popc(__ballot_sync(~0u, id >= 0));
                 if (lane == 0) mbar_arrive_expect_tx(full, n * p.box_rows * 128);
                 __syncwarp();
-                if (id >= 0) {
+                if (id >= 0 && (kPair == 1 || rank == value)) {
                     const int32_t pos = t * kKeys + my_box * p.box_rows;
-                    tma_load_4d(dst + my_half * (kKeys * 128) + my_box * p.box_rows * 128, value ? &tmVc : &tmKc,
-                                my_half * 64, w.h, pos % a.block_size, id, full);
+                    uint8_t *to = dst + my_half * (kKeys * 128) + my_box * p.box_rows * 128;
+                    const CUtensorMap *map = value ? &tmVc : &tmKc;
+                    if (kPair == 1)
+                        tma_load_4d(to, map, my_half * 64, w.h, pos % a.block_size, id, full);
+                    else
+                        tma_load_4d_multi(to, map, my_half * 64, w.h, pos % a.block_size, id, full, kBoth);
                 }
             } else {
                 const int base = (t - w.cached_tiles) * kKeys;
                 const int n = (min(kKeys, w.new_seen - base) + p.new_rows - 1) / p.new_rows;
                 if (lane == 0) mbar_arrive_expect_tx(full, n * kHalves * p.new_rows * 128);
                 __syncwarp();
-                if (my_box < n)
-                    tma_load_3d(dst + my_half * (kKeys * 128) + my_box * p.new_rows * 128, value ? &tmVn : &tmKn,
-                                my_half * 64, w.h, w.q.q0 + base + my_box * p.new_rows, full);
+                if (my_box < n && (kPair == 1 || rank == value)) {
+                    uint8_t *to = dst + my_half * (kKeys * 128) + my_box * p.new_rows * 128;
+                    const CUtensorMap *map = value ? &tmVn : &tmKn;
+                    if (kPair == 1)
+                        tma_load_3d(to, map, my_half * 64, w.h, w.q.q0 + base + my_box * p.new_rows, full);
+                    else
+                        tma_load_3d_multi(to, map, my_half * 64, w.h, w.q.q0 + base + my_box * p.new_rows, full, kBoth);
+                }
             }
         };
         bool more = true;
@@ -266,11 +289,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             wait(&bar[Q_EMPTY], (items & 1) ^ 1);
             ++items;
             if (!__any_sync(~0u, *dead)) {
-                if (lane == 0) mbar_arrive_expect_tx(&bar[Q_FULL], kHalves * p.g.rows * 128);
+                if (lane == 0) mbar_arrive_expect_tx(&bar[Q_FULL], kHalves * p.tile_tokens * group * 128);
                 __syncwarp();
                 if (lane < kHalves)
-                    tma_load_3d(smem + lane * (kRows * 128), &tmQ, lane * 64, w.h * group, w.q.q0 + w.first_token(p.g),
-                                &bar[Q_FULL]);
+                    tma_load_3d(smem + lane * (kRows * 128), &tmQ, lane * 64, w.h * group,
+                                w.q.q0 + w.first_token(p.g) + rank * p.tile_tokens, &bar[Q_FULL]);
             }
             for (int t = w.t0; t < w.t1; ++t) {
                 const int32_t id_next = page(t + 1);  // looked up a tile ahead
@@ -289,6 +312,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                     mbar_wait(&bar[KV_FULL0 + st], (last / kStages) & 1, 20000000ll);
                 }
             mbar_wait(&bar[Q_FULL], (items - 1) & 1, 20000000ll);
+            if (kPair > 1)  // and so do those that the other CTA has sent here without this one's asking
+                for (const long long t0 = clock64(); clock64() - t0 < 200000;) __nanosleep(1000);
+        } else if (kPair > 1) {  // nor does the other's last commit arrive at a CTA that is gone
+            for (uint32_t k = 0; k < kStages && k < slot; ++k) {
+                const uint32_t last = slot - 1 - k;
+                wait(&bar[KV_EMPTY0 + last % kStages], (last / kStages) & 1);
+            }
         }
     } else if (warp == kMmaWarp) {
         // ---- products --------------------------------------------------------------
@@ -310,9 +340,19 @@ __global__ void __launch_bounds__(kThreads, 2)
         auto advance = [&]() {
             if (++st == kStages) st = 0, phase ^= 1;
         };
+        // A CTA that gave up says nothing more to the other of its pair, which then gives up too, instead of
+        // counting arrivals that stand for nothing.
+        auto alive = [&]() { return kPair == 1 || !__any_sync(~0u, *dead); };
+        auto let_go = [&](uint32_t stage, bool tell) {
+            if (kPair == 1)
+                mma_commit(&bar[KV_EMPTY0 + stage]);
+            else if (tell)
+                mma_commit_multi(&bar[KV_EMPTY0 + stage], kBoth);
+        };
         auto scores = [&](uint32_t g, bool last) {  // of tile number g, the item's last or not
             wait(&bar[KV_FULL0 + st], phase);
             tc_fence_after();
+            const bool tell = alive();
             const uint32_t sg = __shfl_sync(~0u, st, 0), gg = __shfl_sync(~0u, g, 0);
             const uint64_t k0 = desc_at(dK, sg * L::kTile);
             const uint32_t d = tmu + COL_S + 64 * (gg & 1);
@@ -322,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     mma_ss(d, desc_at(dQ, (k >> 2) * (kRows * 128) + (k & 3) * 32),
                            desc_at(k0, (k >> 2) * (kKeys * 128) + (k & 3) * 32), kIdS, k > 0);
                 mma_commit(&bar[S_FULL0 + (gg & 1)]);
-                mma_commit(&bar[KV_EMPTY0 + sg]);
+                let_go(sg, tell);
                 if (last) mma_commit(&bar[Q_EMPTY]);
             }
             __syncwarp();
@@ -335,12 +375,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint32_t p0 = tmu + COL_S + 64 * (gg & 1);
             wait(&bar[P_READY0 + (g & 1)], (g >> 1) & 1);
             tc_fence_after();
+            const bool tell = alive();
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
                     mma_ts(tmu + COL_O, p0 + 8 * k, desc_at(v0, 2048 * k), kIdO, k > 0 ? 1u : add);
                 mma_commit(&bar[O_DONE0 + (gg & 1)]);
-                mma_commit(&bar[KV_EMPTY0 + sg]);
+                let_go(sg, tell);
             }
             __syncwarp();
             advance();
@@ -371,7 +412,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         bool more = true;
         while (more) {
             ++item;
-            const int rows = w.tokens(p.g) * group, token0 = w.first_token(p.g);
+            const int token0 = w.first_token(p.g) + rank * p.tile_tokens;
+            const int rows = min(p.tile_tokens, w.q.n - token0) * group;  // none or less: an odd row tile's other half
             const bool warp_live = warp * 32 < rows;
             const int tok = tid < rows ? token0 + (int)(tid * p.group_inv >> 16) : -1;
             const int n_tiles = w.t1 - w.t0;
@@ -467,7 +509,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const bool whole = w.whole();
                 const bool fix = dirty[item & 1] == item;
                 const float mul = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;  // a row that saw nothing: zeros
-                const int64_t part = ((int64_t)blockIdx.x * 2 + (w.t0 > 0 ? 0 : 1)) * p.g.rows + warp * 32;
+                const int64_t part = ((int64_t)worker * 2 + (w.t0 > 0 ? 0 : 1)) * p.g.rows + rank * p.tile_tokens * group +
+                                     warp * 32;
                 // output row of the item's row i: (token0 + i / group, head0 + i mod group)
                 const int64_t row0 = (int64_t)(w.q.q0 + token0) * a.nheads + w.h * group;
                 auto out_row = [&](int i) {
@@ -518,23 +561,50 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     }
     tc_fence_before();
-    __syncthreads();
+    if (kPair > 1)
+        cluster_sync();  // the other CTA's copies and commits come here, too
+    else
+        __syncthreads();
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tm, kTmemCols);
     }
 }
 
-kvs::Tiling tc_tiling(const kv_attention_args &a) { return kvs::tiling(a, kRows, kKeyShift, kOverhead); }
+// CTAs that share an item, by a rule on sizes: a pair where the requests have more rows than a tile
+// takes on the average, and its two row tiles see the same keys but for one tile of them at most: with a
+// mask, or where they are 64 tokens or fewer.  Measured alone / in pairs: 4 prompts of 512 to 4096 tokens
+// over up to 8192 cached, 4 query heads to a key head, 930 / 820 us (1 query head, nothing cached: 178 /
+// 188); 24 trees of 33 to 64 tokens over up to 16384, 8 query heads, 227 / 204 us, of 33 to 48 with 4
+// heads 310 / 215; but a prompt of 512 tokens beside 64 single tokens 184 / 234, since one CTA of the pair
+// then has no rows most of the time.  Groups of four CTAs (two pairs) on an item: 805 and 200 us for the first
+// two, 364 for the trees of up to 48 tokens; a cluster of four loading for one another: 1320 and 319.
+int pair_for(const kv_attention_args &a) {
+    const int64_t group = a.nheads / a.kv_heads;
+    return (int64_t)a.total_tokens * group > (int64_t)kRows * a.num_seqs && (a.mask_words > 0 || 2 * (kRows / group) <= kKeys)
+               ? 2
+               : 1;
+}
 
-int tc_grid(const kv_attention_args &a, const kvs::Tiling &g) { return kvs::grid_of(a, g, kMinUnits, 2 * device_sms()); }
+kvs::Tiling tc_tiling(const kv_attention_args &a) {
+    kvs::Tiling g = kvs::tiling(a, kRows, kKeyShift, kOverhead);
+    g.tokens *= pair_for(a);
+    g.rows *= pair_for(a);
+    return g;
+}
 
-template <int D> cudaError_t launch(const kv_attention_args &a, void *ws, cudaStream_t s) {
+// workers: CTAs or pairs
+int tc_workers(const kv_attention_args &a, const kvs::Tiling &g) {
+    return kvs::grid_of(a, g, kMinUnits, 2 * device_sms() / pair_for(a));
+}
+
+template <int D, int kPair> cudaError_t launch(const kv_attention_args &a, void *ws, cudaStream_t s) {
     TcParams p;
     p.a = a;
     p.g = tc_tiling(a);
-    const int grid = tc_grid(a, p.g);
-    p.parts = kvs::parts_at(ws, grid, p.g.rows, D);
+    p.tile_tokens = p.g.tokens / kPair;
+    const int workers = tc_workers(a, p.g);
+    p.parts = kvs::parts_at(ws, workers, p.g.rows, D);
     p.group_inv = (65536u + p.g.heads - 1) / p.g.heads;
     p.box_rows = kKeys;
     while (a.block_size % p.box_rows) p.box_rows /= 2;
@@ -544,7 +614,7 @@ template <int D> cudaError_t launch(const kv_attention_args &a, void *ws, cudaSt
     const uint64_t H = a.nheads, G = a.kv_heads, T = a.total_tokens;
     CUtensorMap q, kc, vc, kn, vn;
     const bool ok =
-        make_tmap_bf16_3d(&q, a.q, D, H, T, D * 2, (uint64_t)a.q_stride * 2, 64, p.g.heads, p.g.tokens) &&
+        make_tmap_bf16_3d(&q, a.q, D, H, T, D * 2, (uint64_t)a.q_stride * 2, 64, p.g.heads, p.tile_tokens) &&
         make_tmap_bf16_3d(&kn, a.k_new, D, G, T, D * 2, (uint64_t)a.k_stride * 2, 64, 1, p.new_rows) &&
         make_tmap_bf16_3d(&vn, a.v_new, D, G, T, D * 2, (uint64_t)a.v_stride * 2, 64, 1, p.new_rows) &&
         make_tmap_16bit_4d(&kc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.k_cache, D, G, a.block_size, a.num_blocks, D * 2,
@@ -553,11 +623,22 @@ template <int D> cudaError_t launch(const kv_attention_args &a, void *ws, cudaSt
                            G * D * 2, (uint64_t)a.cache_block_stride * 2, 64, 1, p.box_rows);
     if (!ok) return cudaErrorInvalidValue;
     constexpr int smem = Layout<D>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(kv_attention_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const auto kernel = kv_attention_tc_kernel<D, kPair>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kv_attention_tc_kernel<D><<<grid, kThreads, smem, s>>>(q, kc, vc, kn, vn, p);
-    e = cudaGetLastError();
-    return e != cudaSuccess ? e : kvs::join_launch(a, p.parts, grid, p.g, s);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(workers * kPair));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kPair;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kPair > 1 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, kernel, q, kc, vc, kn, vn, p);
+    return e != cudaSuccess ? e : kvs::join_launch(a, p.parts, workers, p.g, s);
 }
 
 }  // namespace
@@ -573,11 +654,12 @@ bool kv_attention_tc_supported(const kv_attention_args &a) {
 
 size_t kv_attention_tc_workspace(const kv_attention_args &a) {
     const kvs::Tiling g = tc_tiling(a);
-    return kvs::parts_bytes(tc_grid(a, g), g.rows, a.headdim);
+    return kvs::parts_bytes(tc_workers(a, g), g.rows, a.headdim);
 }
 
 cudaError_t kv_attention_tc_launch(const kv_attention_args &a, void *ws, cudaStream_t s) {
-    return a.headdim == 64 ? launch<64>(a, ws, s) : launch<128>(a, ws, s);
+    if (pair_for(a) == 1) return a.headdim == 64 ? launch<64, 1>(a, ws, s) : launch<128, 1>(a, ws, s);
+    return a.headdim == 64 ? launch<64, 2>(a, ws, s) : launch<128, 2>(a, ws, s);
 }
 
 }  // namespace ssd

@@ -141,10 +141,11 @@ struct FindSmem {
     int32_t r;
 };
 
-// Called by all threads of the CTA (blockDim.x a multiple of 32): its run, or false when it has
-// none.  min_units: a run is at least about that long.
-__device__ __forceinline__ bool find_run(const kv_attention_args &a, const Tiling &g, int32_t min_units,
-                                         FindSmem &sm, Border *borders, Walk &w) {
+// Called by all threads of the CTA (blockDim.x a multiple of 32): the run of worker `me` of `of` (a CTA,
+// or a pair of them that share their runs), or false when it has none.  min_units: a run is at least
+// about that long.
+__device__ __forceinline__ bool find_run(const kv_attention_args &a, const Tiling &g, int32_t min_units, int32_t me,
+                                         int32_t of, FindSmem &sm, Border *borders, Walk &w) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nwarp = nthr >> 5;
     const int S = a.num_seqs;
     const unsigned long long heads = (unsigned long long)a.kv_heads;
@@ -181,12 +182,12 @@ __device__ __forceinline__ bool find_run(const kv_attention_args &a, const Tilin
         total += all;
     }
     const unsigned long long most = (total + min_units - 1) / min_units;
-    const int ctas = (int)(most < gridDim.x ? most : gridDim.x);
-    if ((int)blockIdx.x >= ctas) {
-        if (tid == 0) borders[blockIdx.x].parts = 0;
+    const int ctas = (int)(most < (unsigned)of ? most : (unsigned)of);
+    if (me >= ctas) {
+        if (tid == 0) borders[me].parts = 0;
         return false;
     }
-    const unsigned long long lo = run_start(total, blockIdx.x, ctas), hi = run_start(total, blockIdx.x + 1, ctas);
+    const unsigned long long lo = run_start(total, me, ctas), hi = run_start(total, me + 1, ctas);
     unsigned long long carry = 0;
     for (int base = 0; base < S; base += nthr) {
         if (S > nthr) scan(base, false, q, per_head, before, all);  // else the scan above still holds
@@ -235,14 +236,14 @@ __device__ __forceinline__ bool find_run(const kv_attention_args &a, const Tilin
         b.head0 = w.h * group + w.part * g.heads;
         const long long tile0 = (long long)lo - first + g.overhead;  // unit of the item's first key tile
         b.parts = 0;
-        if ((long long)lo > tile0 && run_start((long long)total, blockIdx.x - 1, ctas) <= tile0) {
+        if ((long long)lo > tile0 && run_start((long long)total, me - 1, ctas) <= tile0) {
             // runs differ by one unit at most: the last CTA whose run starts before the item's end
             const long long end = tile0 + w.tiles;
             int last = (int)min((long long)ctas - 1, (long long)((unsigned long long)end * ctas / total) + 1);
             while (run_start((long long)total, last, ctas) >= end) --last;
-            b.parts = last - (int)blockIdx.x + 2;
+            b.parts = last - me + 2;
         }
-        borders[blockIdx.x] = b;
+        borders[me] = b;  // a pair writes the same twice
     }
     return w.any();
 }

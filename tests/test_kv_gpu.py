@@ -537,6 +537,48 @@ def test_attention_waits_are_bounded(D):
     _check(c)
 
 
+PAIRS = [  # query heads, key heads, head size, block size, tree, new tokens, cached
+    (8, 1, 128, 16, True, [17, 33, 0, 100, 48, 16, 64], [0, 5000, 7, 64, 130, 0, 2049]),
+    (16, 2, 64, 32, False, [49, 1, 16, 31, 0, 90], [700, 64, 0, 3000, 100, 1]),
+    (5, 1, 128, 64, False, [26, 51, 400, 2], [65, 1000, 0, 3]),
+    (4, 4, 64, 16, True, [300, 129], [100, 0]),
+    (40, 1, 128, 16, False, [4, 7, 3, 13], [40, 0, 9000, 500]),
+    (128, 1, 64, 8, True, [1, 2, 3, 4], [63, 1, 300, 0]),
+]
+
+
+@pytest.mark.parametrize("H,Hkv,D,b,tree,new,ctx", PAIRS)
+def test_attention_pairs_of_row_tiles(H, Hkv, D, b, tree, new, ctx):
+    """Requests of more rows than a tensor-core tile on the average, which two tiles work on together: requests that end
+    in the first tile or the second, or have one token or none, few rows of a tile in use, and several items a request."""
+    c = _attn(BF, H, Hkv, D, b, new, ctx, tree, seed=len(new) + H, empty_rows=[(0, 0)] if tree else ())
+    _check(c)
+
+
+def test_attention_pairs_keep_bad_values_apart():
+    """NaN drafts and an infinite value in the second tile of a pair, and in keys that only one of the tiles sees."""
+    c = _attn(BF, 8, 1, 128, 16, [40, 30], [33, 200], True, seed=40, poison_new=[(0, 2), (0, 39), (1, 20)])
+    _check(c, nan_rows=[2, 39, 60])
+    c = _attn(BF, 8, 1, 64, 16, [40], [100], False, seed=41)
+    c["v"][20, 0, 7] = float("inf")  # a token of the second tile: the first one's rows stay finite
+    out, _ = _run(c, _err())
+    torch.cuda.synchronize()
+    assert torch.isfinite(out[:20]).all() and (out[20:, :, 7] == float("inf")).all()
+    assert torch.isfinite(out[20:, :, :7]).all() and torch.isfinite(out[20:, :, 8:]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("limit", [20, 20000])
+def test_attention_waits_of_pairs_are_bounded(D, limit):
+    """As above, where two tiles share their loads: one that gives up ends the other's waits, too."""
+    c = _attn(BF, 8, 1, D, 16, [40, 30, 64, 17], [3000, 400, 0, 900], False, seed=42)
+    err = _err()
+    _run(c, err, wait_limit_cycles=limit)
+    torch.cuda.synchronize()
+    assert int(err.item()) == ssd.DEVERR_TIMEOUT or (limit > 20 and int(err.item()) == 0)
+    _check(c)
+
+
 def test_attention_without_tokens():
     c = _attn(BF, 4, 1, 128, 16, [0, 0], [100, 40], False, seed=5)
     out, lse = _run(c, _err())
