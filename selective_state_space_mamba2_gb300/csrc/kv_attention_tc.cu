@@ -236,19 +236,29 @@ __global__ void __launch_bounds__(kThreads, 2)
         uint32_t items = 0;
         const int boxes = kKeys / p.box_rows;
         const int my_box = lane / kHalves, my_half = lane % kHalves;
-        // this lane's page of cached tile t: block id, or -1 where it has none to load
-        auto page = [&](int t) -> int32_t {
-            if (my_box >= boxes) return -1;
-            const int32_t pos = t * kKeys + my_box * p.box_rows;
-            if (t >= w.cached_tiles || pos >= w.q.c) return -1;
-            const int32_t id = a.block_table[(int64_t)w.r * a.table_cols + pos / a.block_size];
-            if (id < 0 || id >= a.num_blocks) {
-                report(a.err_word, SSD_DEVERR_SLOT);
-                return a.num_blocks;  // outside the tensor: reads as zeros
-            }
-            return id;
+        // This lane's page of cached tile t.  Its block id is only looked at when it is used, so that the read is
+        // not waited for before; from tile to tile the page is stepped on (4 prompts of 512 to 4096 tokens 829
+        // to 785 us, trees 203 to 191, against two divisions and a wait for the id in every tile).
+        struct Page {
+            int32_t col, off, id;
+            bool any;
         };
-        auto load = [&](bool value, int t, int32_t id) {
+        const int step = kKeys / a.block_size, step_off = kKeys % a.block_size;
+        auto page = [&](int32_t col, int32_t off, int t) {
+            Page g{col, off, 0, my_box < boxes && t < w.cached_tiles && t * kKeys + my_box * p.box_rows < w.q.c};
+            if (g.any) g.id = a.block_table[(int64_t)w.r * a.table_cols + col];
+            return g;
+        };
+        auto page_of = [&](int t) {
+            const int32_t pos = t * kKeys + my_box * p.box_rows;
+            return page(pos / a.block_size, pos % a.block_size, t);
+        };
+        auto page_after = [&](const Page &g, int t) {
+            const int32_t off = g.off + step_off;
+            const bool over = off >= a.block_size;
+            return page(g.col + step + over, over ? off - a.block_size : off, t);
+        };
+        auto load = [&](bool value, int t, Page g) {
             const uint32_t st = slot % kStages;
             wait(&bar[KV_EMPTY0 + st], ((slot / kStages) & 1) ^ 1);
             ++slot;
@@ -256,17 +266,21 @@ __global__ void __launch_bounds__(kThreads, 2)
             uint8_t *dst = smem + L::kRing + st * L::kTile;
             uint64_t *full = &bar[KV_FULL0 + st];
             if (t < w.cached_tiles) {
-                const uint32_t n = __popc(__ballot_sync(~0u, id >= 0));
+                const uint32_t n = __popc(__ballot_sync(~0u, g.any));
                 if (lane == 0) mbar_arrive_expect_tx(full, n * p.box_rows * 128);
                 __syncwarp();
-                if (id >= 0 && (kPair == 1 || rank == value)) {
-                    const int32_t pos = t * kKeys + my_box * p.box_rows;
+                if (g.any && (kPair == 1 || rank == value)) {
+                    int32_t id = g.id;
+                    if (id < 0 || id >= a.num_blocks) {
+                        report(a.err_word, SSD_DEVERR_SLOT);
+                        id = a.num_blocks;  // outside the tensor: reads as zeros
+                    }
                     uint8_t *to = dst + my_half * (kKeys * 128) + my_box * p.box_rows * 128;
                     const CUtensorMap *map = value ? &tmVc : &tmKc;
                     if (kPair == 1)
-                        tma_load_4d(to, map, my_half * 64, w.h, pos % a.block_size, id, full);
+                        tma_load_4d(to, map, my_half * 64, w.h, g.off, id, full);
                     else
-                        tma_load_4d_multi(to, map, my_half * 64, w.h, pos % a.block_size, id, full, kBoth);
+                        tma_load_4d_multi(to, map, my_half * 64, w.h, g.off, id, full, kBoth);
                 }
             } else {
                 const int base = (t - w.cached_tiles) * kKeys;
@@ -285,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         };
         bool more = true;
         while (more) {
-            int32_t id = page(w.t0), id_before = -1;
+            Page now = page_of(w.t0), before = now;
             wait(&bar[Q_EMPTY], (items & 1) ^ 1);
             ++items;
             if (!__any_sync(~0u, *dead)) {
@@ -296,13 +310,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                                 w.q.q0 + w.first_token(p.g) + rank * p.tile_tokens, &bar[Q_FULL]);
             }
             for (int t = w.t0; t < w.t1; ++t) {
-                const int32_t id_next = page(t + 1);  // looked up a tile ahead
-                load(false, t, id);
-                if (t > w.t0) load(true, t - 1, id_before);
-                id_before = id;
-                id = id_next;
+                const Page next = page_after(now, t + 1);  // a tile ahead
+                load(false, t, now);
+                if (t > w.t0) load(true, t - 1, before);
+                before = now;
+                now = next;
             }
-            load(true, w.t1 - 1, id_before);
+            load(true, w.t1 - 1, before);
             more = w.next(a, p.g);
         }
         if (__any_sync(~0u, *dead)) {  // copies in flight land before the CTA may go
@@ -417,16 +431,14 @@ __global__ void __launch_bounds__(kThreads, 2)
             const bool warp_live = warp * 32 < rows;
             const int tok = tid < rows ? token0 + (int)(tid * p.group_inv >> 16) : -1;
             const int n_tiles = w.t1 - w.t0;
+            // Tiles of which some row does not see every key: the last cached one, and new ones from the one of
+            // the row tile's first token on.
+            const int part_cached = w.q.c % kKeys ? w.cached_tiles - 1 : -1;
+            const int part_new = w.cached_tiles + (a.tree_mask ? 0 : (token0 + 1) / kKeys);
             float top = -INFINITY, sum = 0.f;
             for (int t = w.t0; t < w.t1; ++t, ++tile) {
                 const uint32_t s_col = lane_base + COL_S + 64 * (tile & 1);
-                const bool cached = t < w.cached_tiles;
-                const int limit = cached ? min(kKeys, w.q.c - t * kKeys)
-                                         : min(kKeys, w.new_seen - (t - w.cached_tiles) * kKeys);
-                // every row sees every key of the tile: cached ones, or for a chain those before the
-                // tile's first token
-                const bool partial = limit < kKeys || (!cached && (a.tree_mask || (t - w.cached_tiles + 1) * kKeys >
-                                                                                      token0 + 1));
+                const bool partial = t == part_cached || t >= part_new;
                 wait(&bar[S_FULL0 + (tile & 1)], (tile >> 1) & 1);
                 __syncwarp();
                 tc_fence_after();
@@ -487,6 +499,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     tmem_st_wait();
                 }
                 if (partial) {
+                    const bool cached = t < w.cached_tiles;
+                    const int limit = cached ? w.q.c - t * kKeys : w.new_seen - (t - w.cached_tiles) * kKeys;  // rows there
                     // ring position of this tile's values: K0 K1 V0 K2 V1 ... V(n-1)
                     const int i = t - w.t0;
                     const uint32_t pos = ring + (i == n_tiles - 1 ? 2 * n_tiles - 1 : 2 * i + 2);
@@ -574,11 +588,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 // CTAs that share an item, by a rule on sizes: a pair where the requests have more rows than a tile
 // takes on the average, and its two row tiles see the same keys but for one tile of them at most: with a
 // mask, or where they are 64 tokens or fewer.  Measured alone / in pairs: 4 prompts of 512 to 4096 tokens
-// over up to 8192 cached, 4 query heads to a key head, 930 / 820 us (1 query head, nothing cached: 178 /
-// 188); 24 trees of 33 to 64 tokens over up to 16384, 8 query heads, 227 / 204 us, of 33 to 48 with 4
-// heads 310 / 215; but a prompt of 512 tokens beside 64 single tokens 184 / 234, since one CTA of the pair
-// then has no rows most of the time.  Groups of four CTAs (two pairs) on an item: 805 and 200 us for the first
-// two, 364 for the trees of up to 48 tokens; a cluster of four loading for one another: 1320 and 319.
+// over up to 8192 cached, 4 query heads to a key head, 818 / 765 us (1 query head, nothing cached: 176 /
+// 188); 24 trees of 33 to 64 tokens over up to 16384, 8 query heads, 219 / 189 us, of 33 to 48 with 4
+// heads 302 / 203; 2 times 512 tokens over 65536 557 / 430; but a prompt of 512 tokens beside 64 single
+// tokens 183 / 224, since one CTA of the pair then has no rows most of the time.  Clusters of four that load
+// for one another: 1320 us for the prompts.
 int pair_for(const kv_attention_args &a) {
     const int64_t group = a.nheads / a.kv_heads;
     return (int64_t)a.total_tokens * group > (int64_t)kRows * a.num_seqs && (a.mask_words > 0 || 2 * (kRows / group) <= kKeys)
