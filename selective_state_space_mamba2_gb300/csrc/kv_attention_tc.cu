@@ -21,6 +21,15 @@
 // tile of values, so a pair reads from L2 what one CTA alone would; a slot of the ring is loaded again
 // when the products of both have read it (tcgen05.commit to both CTAs' barriers).
 //
+// What bounds it.  Few rows a request (decode steps, short drafts): the bytes of the cache, 256 requests
+// of 4 tokens over up to 8192 cached 684 us, 6.6 TB/s.  Prompts and large trees: shared memory.  Of a
+// tile's 512 cycles of products S takes 384 instead of 256 (a product 128 x 64 x 16 reads 6 KB), V is
+// read in 128, and the copies write 32 KB in 256: 768, and 720 to 790 measured; 4 prompts of 512 to 4096
+// tokens over up to 8192 774 to 787 us, 1350 TFLOP/s.  Tried against that, and not faster: tiles of 128
+// keys with one buffer of scores (the chain of scores, softmax, output then is the bound), two row tiles
+// in a CTA, and products of a pair's 256 rows (cta_group::2, half the keys and values in each CTA: 830
+// us; the weights of both CTAs have to reach the one that issues, 0.8 us a tile for the chain).
+//
 // Masked places: a score that must not count is replaced, not added to, so a NaN key is harmless.
 // A value enters the product whatever its weight, so in tiles with rows that are not there or
 // that some query does not see, the rows that are not there are zeroed in shared memory, and
@@ -56,8 +65,9 @@ struct TcParams {
     kvs::Tiling g;
     int32_t tile_tokens;  // tokens of a row tile
     uint32_t group_inv;   // ceil(2^16 / query heads per key head): row / group = row * group_inv >> 16, row < 128
-    int32_t box_rows;     // rows of a page that one copy brings: divides block_size and kKeys
-    int32_t new_rows;     // rows of new tokens that one copy brings
+    int32_t box_shift;  // rows of a page that one copy brings: a power of two that divides block_size and kKeys
+    int32_t new_shift;  // rows of new tokens that one copy brings, too
+    int32_t box_halves, new_halves;  // 64-column pieces that it brings of them
     long long wait_limit;
 };
 
@@ -232,25 +242,26 @@ __global__ void __launch_bounds__(kThreads, 2)
         // nothing to do
     } else if (warp == kLoadWarp) {
         // ---- loads -----------------------------------------------------------------
-        uint32_t slot = 0;  // ring position
+        uint32_t st = 0, phase = 0, slots = 0;  // ring stage, its phase, stages used
         uint32_t items = 0;
-        const int boxes = kKeys / p.box_rows;
-        const int my_box = lane / kHalves, my_half = lane % kHalves;
+        // one copy brings both halves of the columns where it brings all rows
+        const int per = kHalves / p.box_halves, my_box = lane / per, my_half = lane % per;
+        const int new_per = kHalves / p.new_halves, new_box = lane / new_per, new_half = lane % new_per;
         // This lane's page of cached tile t.  Its block id is only looked at when it is used, so that the read is
         // not waited for before; from tile to tile the page is stepped on (4 prompts of 512 to 4096 tokens 829
         // to 785 us, trees 203 to 191, against two divisions and a wait for the id in every tile).
         struct Page {
             int32_t col, off, id;
-            bool any;
         };
         const int step = kKeys / a.block_size, step_off = kKeys % a.block_size;
         auto page = [&](int32_t col, int32_t off, int t) {
-            Page g{col, off, 0, my_box < boxes && t < w.cached_tiles && t * kKeys + my_box * p.box_rows < w.q.c};
-            if (g.any) g.id = a.block_table[(int64_t)w.r * a.table_cols + col];
+            Page g{col, off, 0};
+            if (t < w.cached_tiles && my_box < kKeys >> p.box_shift && t * kKeys + (my_box << p.box_shift) < w.q.c)
+                g.id = a.block_table[(int64_t)w.r * a.table_cols + col];
             return g;
         };
         auto page_of = [&](int t) {
-            const int32_t pos = t * kKeys + my_box * p.box_rows;
+            const int32_t pos = t * kKeys + (my_box << p.box_shift);
             return page(pos / a.block_size, pos % a.block_size, t);
         };
         auto page_after = [&](const Page &g, int t) {
@@ -259,43 +270,41 @@ __global__ void __launch_bounds__(kThreads, 2)
             return page(g.col + step + over, over ? off - a.block_size : off, t);
         };
         auto load = [&](bool value, int t, Page g) {
-            const uint32_t st = slot % kStages;
-            wait(&bar[KV_EMPTY0 + st], ((slot / kStages) & 1) ^ 1);
-            ++slot;
-            if (__any_sync(~0u, *dead)) return;
+            wait(&bar[KV_EMPTY0 + st], phase ^ 1);
             uint8_t *dst = smem + L::kRing + st * L::kTile;
             uint64_t *full = &bar[KV_FULL0 + st];
-            if (t < w.cached_tiles) {
-                const uint32_t n = __popc(__ballot_sync(~0u, g.any));
-                if (lane == 0) mbar_arrive_expect_tx(full, n * p.box_rows * 128);
-                __syncwarp();
-                if (g.any && (kPair == 1 || rank == value)) {
-                    int32_t id = g.id;
-                    if (id < 0 || id >= a.num_blocks) {
-                        report(a.err_word, SSD_DEVERR_SLOT);
-                        id = a.num_blocks;  // outside the tensor: reads as zeros
-                    }
-                    uint8_t *to = dst + my_half * (kKeys * 128) + my_box * p.box_rows * 128;
-                    const CUtensorMap *map = value ? &tmVc : &tmKc;
-                    if (kPair == 1)
-                        tma_load_4d(to, map, my_half * 64, w.h, g.off, id, full);
-                    else
-                        tma_load_4d_multi(to, map, my_half * 64, w.h, g.off, id, full, kBoth);
+            ++slots;
+            if (++st == kStages) st = 0, phase ^= 1;
+            if (__any_sync(~0u, *dead)) return;
+            const bool cached = t < w.cached_tiles;
+            const int base = (cached ? t : t - w.cached_tiles) * kKeys;
+            const int shift = cached ? p.box_shift : p.new_shift;
+            const int boxes = (min(kKeys, (cached ? w.q.c : w.new_seen) - base) + (1 << shift) - 1) >> shift;
+            if (lane == 0) mbar_arrive_expect_tx(full, (boxes * kHalves * 128) << shift);
+            __syncwarp();
+            if (kPair > 1 && rank != value) return;
+            if (cached && my_box < boxes) {
+                int32_t id = g.id;
+                if (id < 0 || id >= a.num_blocks) {
+                    report(a.err_word, SSD_DEVERR_SLOT);
+                    id = a.num_blocks;  // outside the tensor: reads as zeros
                 }
-            } else {
-                const int base = (t - w.cached_tiles) * kKeys;
-                const int n = (min(kKeys, w.new_seen - base) + p.new_rows - 1) / p.new_rows;
-                if (lane == 0) mbar_arrive_expect_tx(full, n * kHalves * p.new_rows * 128);
-                __syncwarp();
-                if (my_box < n && (kPair == 1 || rank == value)) {
-                    uint8_t *to = dst + my_half * (kKeys * 128) + my_box * p.new_rows * 128;
-                    const CUtensorMap *map = value ? &tmVn : &tmKn;
-                    if (kPair == 1)
-                        tma_load_3d(to, map, my_half * 64, w.h, w.q.q0 + base + my_box * p.new_rows, full);
-                    else
-                        tma_load_3d_multi(to, map, my_half * 64, w.h, w.q.q0 + base + my_box * p.new_rows, full, kBoth);
-                }
+                uint8_t *to = dst + my_half * (kKeys * 128) + (my_box << shift) * 128;
+                const CUtensorMap *map = value ? &tmVc : &tmKc;
+                if (kPair == 1)
+                    tma_load_5d(to, map, 0, g.off, my_half, w.h, id, full);
+                else
+                    tma_load_5d_multi(to, map, 0, g.off, my_half, w.h, id, full, kBoth);
+            } else if (!cached && new_box < boxes) {
+                uint8_t *to = dst + new_half * (kKeys * 128) + (new_box << shift) * 128;
+                const CUtensorMap *map = value ? &tmVn : &tmKn;
+                const int32_t row = w.q.q0 + base + (new_box << shift);
+                if (kPair == 1)
+                    tma_load_4d(to, map, 0, row, new_half, w.h, full);
+                else
+                    tma_load_4d_multi(to, map, 0, row, new_half, w.h, full, kBoth);
             }
+            __syncwarp();
         };
         bool more = true;
         while (more) {
@@ -319,20 +328,15 @@ __global__ void __launch_bounds__(kThreads, 2)
             load(true, w.t1 - 1, before);
             more = w.next(a, p.g);
         }
+        // stages used, their last phases: st's was one round ago
+        const auto last_phase = [&](uint32_t k) { return phase ^ (k >= st); };
         if (__any_sync(~0u, *dead)) {  // copies in flight land before the CTA may go
-            for (int st = 0; st < kStages; ++st)
-                if (slot > (uint32_t)st) {
-                    const uint32_t last = slot - 1 - (slot - 1 - st) % kStages;
-                    mbar_wait(&bar[KV_FULL0 + st], (last / kStages) & 1, 20000000ll);
-                }
+            for (uint32_t k = 0; k < kStages && k < slots; ++k) mbar_wait(&bar[KV_FULL0 + k], last_phase(k), 20000000ll);
             mbar_wait(&bar[Q_FULL], (items - 1) & 1, 20000000ll);
             if (kPair > 1)  // and so do those that the other CTA has sent here without this one's asking
                 for (const long long t0 = clock64(); clock64() - t0 < 200000;) __nanosleep(1000);
         } else if (kPair > 1) {  // nor does the other's last commit arrive at a CTA that is gone
-            for (uint32_t k = 0; k < kStages && k < slot; ++k) {
-                const uint32_t last = slot - 1 - k;
-                wait(&bar[KV_EMPTY0 + last % kStages], (last / kStages) & 1);
-            }
+            for (uint32_t k = 0; k < kStages && k < slots; ++k) wait(&bar[KV_EMPTY0 + k], last_phase(k));
         }
     } else if (warp == kMmaWarp) {
         // ---- products --------------------------------------------------------------
@@ -595,9 +599,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 // for one another: 1320 us for the prompts.
 int pair_for(const kv_attention_args &a) {
     const int64_t group = a.nheads / a.kv_heads;
-    return (int64_t)a.total_tokens * group > (int64_t)kRows * a.num_seqs && (a.mask_words > 0 || 2 * (kRows / group) <= kKeys)
-               ? 2
-               : 1;
+    const bool many = (int64_t)a.total_tokens * group > (int64_t)kRows * a.num_seqs;
+    return many && (a.mask_words > 0 || 2 * (kRows / group) <= kKeys) ? 2 : 1;
 }
 
 kvs::Tiling tc_tiling(const kv_attention_args &a) {
@@ -620,21 +623,31 @@ template <int D, int kPair> cudaError_t launch(const kv_attention_args &a, void 
     const int workers = tc_workers(a, p.g);
     p.parts = kvs::parts_at(ws, workers, p.g.rows, D);
     p.group_inv = (65536u + p.g.heads - 1) / p.g.heads;
-    p.box_rows = kKeys;
-    while (a.block_size % p.box_rows) p.box_rows /= 2;
-    p.new_rows = 8;  // no more than a request is said to have: decode steps bring few rows
-    while (p.new_rows < kKeys && p.new_rows < a.max_new_tokens) p.new_rows *= 2;
+    p.box_shift = kKeyShift;
+    while (a.block_size % (1 << p.box_shift)) --p.box_shift;
+    p.new_shift = 3;  // no more than a request is said to have: decode steps bring few rows
+    while (p.new_shift < kKeyShift && (1 << p.new_shift) < a.max_new_tokens) ++p.new_shift;
     p.wait_limit = a.wait_limit_cycles > 0 ? a.wait_limit_cycles : 2000000000ll;
-    const uint64_t H = a.nheads, G = a.kv_heads, T = a.total_tokens;
+    constexpr uint32_t halves = D / 64;
+    const uint32_t box = 1u << p.box_shift, fresh = 1u << p.new_shift;
+    p.box_halves = box == kKeys ? halves : 1;
+    p.new_halves = fresh == kKeys ? halves : 1;
+    const uint64_t H = a.nheads, G = a.kv_heads, T = a.total_tokens, rows = a.block_size, blocks = a.num_blocks;
+    const uint64_t head = D * 2, line = G * head, block = (uint64_t)a.cache_block_stride * 2;  // strides in bytes
+    const uint64_t k_stride = (uint64_t)a.k_stride * 2, v_stride = (uint64_t)a.v_stride * 2;
+    constexpr auto kType = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     CUtensorMap q, kc, vc, kn, vn;
-    const bool ok =
-        make_tmap_bf16_3d(&q, a.q, D, H, T, D * 2, (uint64_t)a.q_stride * 2, 64, p.g.heads, p.tile_tokens) &&
-        make_tmap_bf16_3d(&kn, a.k_new, D, G, T, D * 2, (uint64_t)a.k_stride * 2, 64, 1, p.new_rows) &&
-        make_tmap_bf16_3d(&vn, a.v_new, D, G, T, D * 2, (uint64_t)a.v_stride * 2, 64, 1, p.new_rows) &&
-        make_tmap_16bit_4d(&kc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.k_cache, D, G, a.block_size, a.num_blocks, D * 2,
-                           G * D * 2, (uint64_t)a.cache_block_stride * 2, 64, 1, p.box_rows) &&
-        make_tmap_16bit_4d(&vc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.v_cache, D, G, a.block_size, a.num_blocks, D * 2,
-                           G * D * 2, (uint64_t)a.cache_block_stride * 2, 64, 1, p.box_rows);
+    // caches: 64 columns, rows of a block, column halves, heads, blocks; new tokens the same without blocks
+    const cuuint64_t cache_dims[5] = {64, rows, halves, G, blocks}, cache_strides[4] = {line, 128, head, block};
+    const cuuint32_t cache_box[5] = {64, box, (uint32_t)p.box_halves, 1, 1};
+    const cuuint64_t new_dims[4] = {64, T, halves, G}, kn_strides[3] = {k_stride, 128, head};
+    const cuuint64_t vn_strides[3] = {v_stride, 128, head};
+    const cuuint32_t new_box[4] = {64, fresh, (uint32_t)p.new_halves, 1};
+    const bool ok = make_tmap_bf16_3d(&q, a.q, D, H, T, head, (uint64_t)a.q_stride * 2, 64, p.g.heads, p.tile_tokens) &&
+                    make_tmap_16bit<5>(&kc, kType, a.k_cache, cache_dims, cache_strides, cache_box) &&
+                    make_tmap_16bit<5>(&vc, kType, a.v_cache, cache_dims, cache_strides, cache_box) &&
+                    make_tmap_16bit<4>(&kn, kType, a.k_new, new_dims, kn_strides, new_box) &&
+                    make_tmap_16bit<4>(&vn, kType, a.v_new, new_dims, vn_strides, new_box);
     if (!ok) return cudaErrorInvalidValue;
     constexpr int smem = Layout<D>::kBytes;
     const auto kernel = kv_attention_tc_kernel<D, kPair>;

@@ -38,17 +38,16 @@ inline bool make_tmap_16bit_3d(CUtensorMap *m, CUtensorMapDataType type, const v
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The same with a fourth dimension d3 (byte stride s3); its box is one entry deep.
-inline bool make_tmap_16bit_4d(CUtensorMap *m, CUtensorMapDataType type, const void *base, uint64_t d0, uint64_t d1,
-                               uint64_t d2, uint64_t d3, uint64_t s1, uint64_t s2, uint64_t s3, uint32_t b0, uint32_t b1,
-                               uint32_t b2) {
+// Tensor of `rank` dimensions (innermost first) of 16-bit elements, strides[i] bytes between entries of
+// dimension i + 1.
+template <int rank>
+inline bool make_tmap_16bit(CUtensorMap *m, CUtensorMapDataType type, const void *base, const cuuint64_t (&dims)[rank],
+                            const cuuint64_t (&strides)[rank - 1], const cuuint32_t (&box)[rank]) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
-    cuuint64_t dims[4] = {d0, d1, d2, d3};
-    cuuint64_t strides[3] = {s1, s2, s3};
-    cuuint32_t box[4] = {b0, b1, b2, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    return enc(m, type, 4, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    cuuint32_t estr[rank];
+    for (int i = 0; i < rank; ++i) estr[i] = 1;
+    return enc(m, type, rank, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
