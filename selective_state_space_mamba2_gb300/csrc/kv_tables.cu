@@ -5,8 +5,8 @@
 // bytes each, from L2 after the first CTA) and then writes only its own tile of tokens; no CTA
 // waits for another's result.  A token finds its request by bisection among the 512 just scanned,
 // in shared memory.  A block's table entry is written by the thread of the block's first new token.
-// What bounds it: 12 bytes per token in large steps (524672 tokens of 392 requests: MEASURED us, of
-// which 2 are the launch), two dependent rounds of loads in small ones (256 requests of 4: 4.2 us).
+// What bounds it: 12 bytes per token in large steps (524672 tokens of 392 requests: 6.7 us, of
+// which 2 are the launch), two dependent rounds of loads in small ones (256 requests of 4: 4.8 us).
 #include "kv.cuh"
 
 namespace ssd {
