@@ -579,6 +579,19 @@ def test_attention_waits_of_pairs_are_bounded(D, limit):
     _check(c)
 
 
+def test_attention_pairs_do_not_depend_on_the_hint():
+    """Tiles of as many tokens as a request is said to have, two of them side by side; and a batch where two tiles would
+    work together, but no token belongs to a request."""
+    for hint in (0, 1, 7, 1000):
+        _check(_attn(BF, 8, 1, 128, 16, [40, 64, 1], [50, 0, 200], True, seed=43, max_new=hint))
+    c = _attn(BF, 8, 1, 128, 16, [40], [100], False, seed=44)
+    c["cu"] = np.array([0, 0], np.int32)
+    out = F.poison((40, 8, 128), BF, DEV)
+    _run(c, _err(), out=out)
+    torch.cuda.synchronize()
+    assert torch.isnan(out).all()
+
+
 def test_attention_without_tokens():
     c = _attn(BF, 4, 1, 128, 16, [0, 0], [100, 40], False, seed=5)
     out, lse = _run(c, _err())
