@@ -292,27 +292,47 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NV))
 // One row of CTAs per border: where the border before CTA b's run is the first to cut an item, its
 // parts are added up, that of CTA b - 1 (which began the item) and those of the CTAs from b on:
 //   out = sum_i 2^(m_i - m) O_i / L,  L = sum_i 2^(m_i - m) l_i,  m = max_i m_i.
-// Bound by the latency of three dependent reads (border, statistics, sums).  kSplit warps share a
-// row's parts: 4 for decode's few rows, whose items may have dozens of parts (65536 keys of one
-// request: 38), 1 for prompts' many rows of two or three parts.
+// A warp sums a row.  Bound by the latency of dependent reads, border, statistics and sums, so the first sums
+// are read while the statistics are on their way; for prompts by the bytes of the parts in L2 (four rows a
+// warp: the same).  In tiles of few rows (decode) an item may be in dozens of parts (65536 keys of one
+// request: 38): the CTA's four warps then share a row's.
 constexpr int kJoinThreads = 128;
-constexpr int kSplitRows = 16;  // tiles of at most so many rows are joined by 4 warps a row
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kFewRows = 32;     // tiles of at most so many rows
+constexpr int kAloneParts = 4;   // items of at most so many parts have a warp a row there, too (16 fp32 requests of
+                                 // up to 2000 keys 29.2 us, 30.5 with up to 8; one of 777 14.3 us with up to 16)
+constexpr int kFlight = 4;       // parts in flight
 
-template <typename T, int NV, int kSplit>  // NV: 128-float pieces of a row
+template <typename T, int NV, bool kFew>  // NV: 128-float pieces of a row
 __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const kv_attention_args a, const kvs::Parts parts,
                                                                const kvs::Tiling g) {
-    __shared__ float part_acc[kSplit][NV * 128];
-    __shared__ float part_sum[kSplit];
+    __shared__ float4 quarters[kFew ? kJoinWarps : 1][NV * 32];
     const int D = a.headdim, b = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = kSplit > 1 ? blockIdx.y : blockIdx.y * 4 + warp, share = kSplit > 1 ? warp : 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are complete
     const kvs::Border me = parts.borders[b];
-    const int n = me.parts;
-    if (n == 0 || row >= me.tokens * me.heads) return;
+    const int n = me.parts, rows = me.tokens * me.heads;
+    // CTAs of tiles of few rows: every fourth one has four rows, or each has one
+    const bool alone = !kFew || n <= kAloneParts;
+    const int row = kFew ? blockIdx.y + (alone ? warp : 0) : blockIdx.y * kJoinWarps + warp;
+    if (n == 0 || row >= rows || (kFew && alone && blockIdx.y % kJoinWarps != 0)) return;
+    const int share = alone ? 0 : warp, step = alone ? 1 : kJoinWarps;  // parts of this warp
     // part k: of CTA b - 1 + k
     auto part_row = [&](int k) { return ((int64_t)(b - 1 + k) * 2 + (k == 0 ? 1 : 0)) * g.rows + row; };
-    float top = -INFINITY;
-    for (int k = lane; k < n; k += 32) {
+    float4 v[kFlight][NV];
+    auto read = [&](int k) {  // the last ones repeated
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            const float *src = parts.sums + part_row(k + i * step < n ? k + i * step : k) * D;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                v[i][j] = 128 * j + 4 * lane < D ? *reinterpret_cast<const float4 *>(src + 128 * j + 4 * lane)
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    };
+    if (share < n) read(share);
+    float2 st = lane < n ? parts.stats[part_row(lane)] : make_float2(-INFINITY, 0.f);  // a lane a part
+    float top = st.x;
+    for (int k = lane + 32; k < n; k += 32) {
         const float m = parts.stats[part_row(k)].x;
         top = m > top || m != m ? m : top;
     }
@@ -322,37 +342,26 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const kv_attentio
         top = m > top || m != m ? m : top;
     }
     const float from = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, acc[NV][4] = {};
-    // parts share, share + kSplit, ...: 32 a round, a lane each for the factors
-    for (int k0 = share; k0 < n; k0 += 32 * kSplit) {
-        const int mine = k0 + lane * kSplit;
-        float f = 0.f;
-        if (mine < n) {
-            const float2 st = parts.stats[part_row(mine)];
-            f = exp2f(st.x - from);
-            sum = fmaf(f, st.y, sum);
-        }
-        const int here = min(32, (n - k0 + kSplit - 1) / kSplit);
-        for (int i0 = 0; i0 < here; i0 += 4) {  // four loads in flight, the last ones repeated with factor 0
-            float4 v[4][NV];
+    float sum = 0.f;
+    float4 acc[NV];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float *src = parts.sums + part_row(k0 + min(i0 + i, here - 1) * kSplit) * D;
+    for (int j = 0; j < NV; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < n; k0 += 32) {
+        if (k0 > 0) st = k0 + lane < n ? parts.stats[part_row(k0 + lane)] : make_float2(-INFINITY, 0.f);
+        const float f = k0 + lane < n ? exp2f(st.x - from) : 0.f;
+        sum = fmaf(f, st.y, sum);
+        for (int k = k0 + share; k < min(n, k0 + 32); k += kFlight * step) {
+            if (k > share) read(k);
 #pragma unroll
-                for (int j = 0; j < NV; ++j)
-                    v[i][j] = 128 * j + 4 * lane < D ? *reinterpret_cast<const float4 *>(src + 128 * j + 4 * lane)
-                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float fk = __shfl_sync(~0u, f, i0 + i < here ? i0 + i : 0);
-                if (i0 + i < here) {
+            for (int i = 0; i < kFlight; ++i) {
+                const float fk = __shfl_sync(~0u, f, (k + i * step) & 31);
+                if (k + i * step < n) {
 #pragma unroll
                     for (int j = 0; j < NV; ++j) {
-                        acc[j][0] = fmaf(fk, v[i][j].x, acc[j][0]);
-                        acc[j][1] = fmaf(fk, v[i][j].y, acc[j][1]);
-                        acc[j][2] = fmaf(fk, v[i][j].z, acc[j][2]);
-                        acc[j][3] = fmaf(fk, v[i][j].w, acc[j][3]);
+                        acc[j].x = fmaf(fk, v[i][j].x, acc[j].x);
+                        acc[j].y = fmaf(fk, v[i][j].y, acc[j].y);
+                        acc[j].z = fmaf(fk, v[i][j].z, acc[j].z);
+                        acc[j].w = fmaf(fk, v[i][j].w, acc[j].w);
                     }
                 }
             }
@@ -360,43 +369,31 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const kv_attentio
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    if (kSplit > 1) {
+    if (!alone) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            *reinterpret_cast<float4 *>(&part_acc[share][128 * j + 4 * lane]) =
-                make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-        if (lane == 0) part_sum[share] = sum;
+        for (int j = 0; j < NV; ++j) quarters[warp][j * 32 + lane] = acc[j];
         __syncthreads();
         if (warp > 0) return;
-        sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kSplit; ++w) sum += part_sum[w];
+        for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kSplit; ++w) {
-                const float4 v = *reinterpret_cast<const float4 *>(&part_acc[w][128 * j + 4 * lane]);
-                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+            for (int w = 1; w < kJoinWarps; ++w) {
+                const float4 q = quarters[w][j * 32 + lane];
+                acc[j].x += q.x, acc[j].y += q.y, acc[j].z += q.z, acc[j].w += q.w;
             }
-            acc[j][0] = s.x, acc[j][1] = s.y, acc[j][2] = s.z, acc[j][3] = s.w;
-        }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that saw nothing: zeros
     const int64_t out_row = (int64_t)(me.token0 + row / me.heads) * a.nheads + me.head0 + row % me.heads;
     T *out = static_cast<T *>(a.out) + out_row * D;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int e = 128 * j + 4 * lane;
-        if (e < D) {
-            if (sizeof(T) == 4) {
-                *reinterpret_cast<float4 *>(out + e) =
-                    make_float4(acc[j][0] * inv, acc[j][1] * inv, acc[j][2] * inv, acc[j][3] * inv);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) out[e + i] = from_f32<T>(acc[j][i] * inv);
-            }
-        }
+        if (e >= D) continue;
+        const float4 o = make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv);
+        if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<float4 *>(out + e) = o;
+        else
+            *reinterpret_cast<uint2 *>(out + e) = make_uint2(tc::pack_bf16(o.x, o.y), tc::pack_bf16(o.z, o.w));
     }
     if (a.lse && lane == 0) a.lse[out_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
@@ -404,9 +401,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const kv_attentio
 template <typename T, int NV>
 cudaError_t launch_join(const kv_attention_args &a, const kvs::Parts &p, int grid, const kvs::Tiling &g, cudaStream_t s) {
     // a programmatic dependent of the attention kernel: its CTAs may be set up while that ends
-    const bool split = g.rows <= kSplitRows;
+    const bool few = g.rows <= kFewRows;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)(split ? g.rows : kvs::ceil_div(g.rows, 4)));
+    cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)(few ? g.rows : kvs::ceil_div(g.rows, kJoinWarps)));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -414,8 +411,8 @@ cudaError_t launch_join(const kv_attention_args &a, const kvs::Parts &p, int gri
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return split ? cudaLaunchKernelEx(&cfg, kv_join_kernel<T, NV, 4>, a, p, g)
-                 : cudaLaunchKernelEx(&cfg, kv_join_kernel<T, NV, 1>, a, p, g);
+    return few ? cudaLaunchKernelEx(&cfg, kv_join_kernel<T, NV, true>, a, p, g)
+               : cudaLaunchKernelEx(&cfg, kv_join_kernel<T, NV, false>, a, p, g);
 }
 
 kvs::Tiling simt_tiling(const kv_attention_args &a) { return kvs::tiling(a, kRowTile, kKeyShift, kOverhead); }

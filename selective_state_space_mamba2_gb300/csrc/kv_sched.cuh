@@ -22,10 +22,26 @@ struct Border {
     int32_t head0, heads;    // first query head, query heads
 };
 
-// First unit of CTA i's run.
-__device__ __forceinline__ long long run_start(long long total, int32_t i, int32_t ctas) {
-    return (long long)((unsigned long long)total * (unsigned long long)i / (unsigned long long)ctas);
+// n / d; 64-bit division takes several hundred cycles, and few calls need it.
+__device__ __forceinline__ unsigned long long quotient(unsigned long long n, unsigned long long d) {
+    return (n | d) >> 32 ? n / d : (uint32_t)n / (uint32_t)d;
 }
+
+// `total` units cut into `runs` runs: the first `rem` of them have base + 1, the others base.
+struct Cut {
+    unsigned long long base, rem;
+    __device__ __forceinline__ Cut(unsigned long long total, uint32_t runs) {
+        base = quotient(total, runs);
+        rem = total - base * runs;
+    }
+    // first unit of run i
+    __device__ __forceinline__ unsigned long long start(uint32_t i) const { return i * base + (i < rem ? i : rem); }
+    // the run that unit u is in
+    __device__ __forceinline__ uint32_t run_of(unsigned long long u) const {
+        const unsigned long long longer = rem * (base + 1);
+        return (uint32_t)(u < longer ? quotient(u, base + 1) : rem + quotient(u - longer, base));
+    }
+};
 
 struct Request {
     int32_t q0, n, c;  // first packed row, new tokens, cached tokens
@@ -69,17 +85,33 @@ __device__ __forceinline__ int32_t visible_new(const kv_attention_args &a, const
     return a.tree_mask || q.n - b * g.tokens <= g.tokens ? q.n : (b + 1) * g.tokens;
 }
 
-// Units of one head of a request.
+// Key tiles that the first `blocks` token blocks of a chain see of its new tokens, none of them the last
+// block: sum over b of ceil(b t / K), b = 1 .. blocks, t tokens a block, K keys a tile.  K ceil(x / K) is
+// x + (-x mod K), and -b t mod K takes every multiple of K / P below K once in P blocks in a row, P = K / gcd(t, K).
+__device__ __forceinline__ long long tiles_before(const Tiling &g, int32_t blocks) {
+    const uint32_t t = (uint32_t)g.tokens, mask = (1u << g.key_shift) - 1;
+    const int zeros = min(__ffs((int)t) - 1, g.key_shift), p_shift = g.key_shift - zeros;
+    const uint32_t b = (uint32_t)blocks, left = b & ((1u << p_shift) - 1);
+    unsigned long long rest = (unsigned long long)(b >> p_shift) * ((((1ull << p_shift) - 1) << g.key_shift) / 2);
+    uint32_t x = (b - left) * t;  // modulo K is all that counts
+    for (uint32_t i = 0; i < left; ++i) {
+        x += t;
+        rest += (0u - x) & mask;
+    }
+    return (long long)(((unsigned long long)b * (b + 1) / 2 * t + rest) >> g.key_shift);
+}
+
+// Units of one head of a request's first `blocks` token blocks, of all of it with the last.
+__device__ __forceinline__ long long units_before(const kv_attention_args &a, const Request &q, const Tiling &g,
+                                                  int32_t blocks) {
+    const long long fixed = (long long)blocks * (g.overhead + tiles_of(g, q.c));
+    const long long fresh = a.tree_mask ? (long long)blocks * tiles_of(g, q.n) : tiles_before(g, blocks);
+    return (fixed + fresh) * g.parts;
+}
 __device__ __forceinline__ long long units_of(const kv_attention_args &a, const Request &q, const Tiling &g) {
     if (q.n <= 0) return 0;
-    const int32_t blocks = ceil_div(q.n, g.tokens);
-    long long sum = (long long)blocks * (g.overhead + tiles_of(g, q.c));
-    if (a.tree_mask) {
-        sum += (long long)blocks * tiles_of(g, q.n);
-    } else {
-        for (int32_t b = 0; b < blocks; ++b) sum += tiles_of(g, visible_new(a, q, g, b));
-    }
-    return sum * g.parts;
+    const int32_t before = ceil_div(q.n, g.tokens) - 1;
+    return units_before(a, q, g, before) + (long long)(g.overhead + tiles_of(g, q.c) + tiles_of(g, q.n)) * g.parts;
 }
 
 // The items of a CTA's run, one after the other.  Every thread that walks them gets the same
@@ -136,115 +168,97 @@ struct Walk {
 
 struct FindSmem {
     unsigned long long sum[32];
-    long long base, per_head;
-    Request q;
-    int32_t r;
+    Walk w;
 };
 
 // Called by all threads of the CTA (blockDim.x a multiple of 32): the run of worker `me` of `of` (a CTA,
 // or a pair of them that share their runs), or false when it has none.  min_units: a run is at least
-// about that long.
+// about that long.  Latency is all that counts here: lengths are read once, S / blockDim.x requests a thread,
+// sums over a prompt's token blocks are closed forms (prompts of up to 4096 tokens 5.2 to 3.6 us), and where a
+// run starts is worked out by the one thread that has its request.
 __device__ __forceinline__ bool find_run(const kv_attention_args &a, const Tiling &g, int32_t min_units, int32_t me,
                                          int32_t of, FindSmem &sm, Border *borders, Walk &w) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nwarp = nthr >> 5;
     const int S = a.num_seqs;
     const unsigned long long heads = (unsigned long long)a.kv_heads;
-    // units of the requests, a CTA's worth of them at a time, summed over all
-    auto scan = [&](int base, bool tell, Request &q, unsigned long long &per_head, unsigned long long &before,
-                    unsigned long long &all) {
-        const int r = base + tid;
-        q.n = 0;
-        per_head = 0;
-        if (r < S) {
-            q = request(a, r, tell);
-            per_head = (unsigned long long)units_of(a, q, g);
-        }
-        const unsigned long long own = per_head * heads;
-        unsigned long long sum = own;
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long v = __shfl_up_sync(~0u, sum, o);
-            if (lane >= o) sum += v;
-        }
-        __syncthreads();
-        if (lane == 31) sm.sum[warp] = sum;
-        __syncthreads();
-        before = sum - own;
-        all = 0;
-        for (int i = 0; i < nwarp; ++i) {
-            if (i < warp) before += sm.sum[i];
-            all += sm.sum[i];
-        }
-    };
+    const int per = ceil_div(S, nthr), r0 = tid * per, r1 = (int)min((long long)S, (long long)r0 + per);
     Request q;
-    unsigned long long per_head, before, all, total = 0;
-    for (int base = 0; base < S; base += nthr) {
-        scan(base, blockIdx.x == 0, q, per_head, before, all);
-        total += all;
+    unsigned long long per_head = 0, own = 0;
+    q.q0 = q.n = q.c = 0;
+    for (int r = r0; r < r1; ++r) {
+        q = request(a, r, blockIdx.x == 0);
+        per_head = (unsigned long long)units_of(a, q, g);
+        own += per_head * heads;
     }
-    const unsigned long long most = (total + min_units - 1) / min_units;
-    const int ctas = (int)(most < (unsigned)of ? most : (unsigned)of);
-    if (me >= ctas) {
+    unsigned long long sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long v = __shfl_up_sync(~0u, sum, o);
+        if (lane >= o) sum += v;
+    }
+    if (lane == 31) sm.sum[warp] = sum;
+    __syncthreads();
+    unsigned long long before = sum - own, total = 0;
+    for (int i = 0; i < nwarp; ++i) {
+        const unsigned long long v = sm.sum[i];
+        if (i < warp) before += v;
+        total += v;
+    }
+    const unsigned long long most = quotient(total + min_units - 1, min_units);
+    const uint32_t runs = (uint32_t)(most < (unsigned)of ? most : (unsigned)of);
+    if ((uint32_t)me >= runs) {
         if (tid == 0) borders[me].parts = 0;
         return false;
     }
-    const unsigned long long lo = run_start(total, me, ctas), hi = run_start(total, me + 1, ctas);
-    unsigned long long carry = 0;
-    for (int base = 0; base < S; base += nthr) {
-        if (S > nthr) scan(base, false, q, per_head, before, all);  // else the scan above still holds
-        if (q.n > 0 && carry + before <= lo && lo - (carry + before) < per_head * heads) {
-            sm.r = base + tid;
-            sm.q = q;
-            sm.base = (long long)(carry + before);
-            sm.per_head = (long long)per_head;
+    const Cut cut(total, runs);
+    const unsigned long long lo = cut.start(me);
+    if (before <= lo && lo - before < own) {  // one thread's request
+        unsigned long long off = lo - before;
+        w.r = r0;
+        if (per > 1) {
+            for (;; ++w.r) {
+                q = request(a, w.r, false);
+                per_head = (unsigned long long)units_of(a, q, g);
+                if (off < per_head * heads) break;
+                off -= per_head * heads;
+            }
         }
-        carry += all;
-        if (carry > lo) break;
-    }
-    __syncthreads();
-
-    w.r = sm.r;
-    w.q = sm.q;
-    w.blocks = ceil_div(w.q.n, g.tokens);
-    w.left = (long long)(hi - lo);
-    long long off = (long long)lo - sm.base;
-    w.h = (int32_t)(off / sm.per_head);
-    off -= w.h * sm.per_head;
-    w.b = 0;
-    const int32_t fixed = g.overhead + tiles_of(g, w.q.c);
-    int32_t here;  // units of a token block's part
-    if (a.tree_mask) {
-        here = fixed + tiles_of(g, w.q.n);
-        w.b = (int32_t)(off / ((long long)here * g.parts));
-        off -= (long long)w.b * here * g.parts;
-    } else {
-        while (true) {
-            here = fixed + tiles_of(g, visible_new(a, w.q, g, w.b));
-            if (off < (long long)here * g.parts) break;
-            off -= (long long)here * g.parts;
-            ++w.b;
+        w.q = q;
+        w.blocks = ceil_div(q.n, g.tokens);
+        w.left = (long long)(cut.start(me + 1) - lo);
+        w.h = (int32_t)quotient(off, per_head);
+        off -= w.h * per_head;
+        w.b = 0;
+        const int32_t fixed = g.overhead + tiles_of(g, q.c);
+        if (a.tree_mask) {
+            w.b = (int32_t)quotient(off, (unsigned long long)(fixed + tiles_of(g, q.n)) * g.parts);
+        } else if (w.blocks > 1) {
+            // units before block b are about parts (b^2 t / 2K + b (fixed + t / 2K + 1/2)): the root, then the last step
+            const float half = 0.5f * (float)g.tokens / (float)(1 << g.key_shift), c = (float)fixed + half + 0.5f;
+            const float u = (float)off / (float)g.parts;
+            w.b = min((int32_t)(2.f * u / (c + sqrtf(c * c + 4.f * half * u))), w.blocks - 1);
+            while (w.b > 0 && (unsigned long long)units_before(a, q, g, w.b) > off) --w.b;
+            while (w.b + 1 < w.blocks && (unsigned long long)units_before(a, q, g, w.b + 1) <= off) ++w.b;
         }
-    }
-    w.part = g.parts == 1 ? 0 : (int32_t)off / here;
-    const int32_t first = (int32_t)off - w.part * here;
-    w.set_item(a, g, first);
-    if (tid == nthr - 1) {  // not one of the threads that the run starts with
+        off -= (unsigned long long)units_before(a, q, g, w.b);
+        const int32_t here = fixed + tiles_of(g, visible_new(a, q, g, w.b));  // units of a token block's part
+        w.part = g.parts == 1 ? 0 : (int32_t)off / here;
+        const int32_t first = (int32_t)off - w.part * here;
+        w.set_item(a, g, first);
+        sm.w = w;
         Border b;
         const int32_t group = a.nheads / a.kv_heads;
-        b.token0 = w.q.q0 + w.first_token(g);
+        b.token0 = q.q0 + w.first_token(g);
         b.tokens = w.tokens(g);
         b.heads = w.heads(g, group);
         b.head0 = w.h * group + w.part * g.heads;
-        const long long tile0 = (long long)lo - first + g.overhead;  // unit of the item's first key tile
         b.parts = 0;
-        if ((long long)lo > tile0 && run_start((long long)total, me - 1, ctas) <= tile0) {
-            // runs differ by one unit at most: the last CTA whose run starts before the item's end
-            const long long end = tile0 + w.tiles;
-            int last = (int)min((long long)ctas - 1, (long long)((unsigned long long)end * ctas / total) + 1);
-            while (run_start((long long)total, last, ctas) >= end) --last;
-            b.parts = last - me + 2;
-        }
+        const unsigned long long tile0 = lo - first + g.overhead;  // unit of the item's first key tile
+        if (lo > tile0 && cut.start(me - 1) <= tile0) b.parts = (int32_t)cut.run_of(tile0 + w.tiles - 1) - me + 2;
         borders[me] = b;  // a pair writes the same twice
     }
+    __syncthreads();
+    w = sm.w;
     return w.any();
 }
 
