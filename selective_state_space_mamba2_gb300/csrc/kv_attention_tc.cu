@@ -22,10 +22,10 @@
 // when the products of both have read it (tcgen05.commit to both CTAs' barriers).
 //
 // What bounds it.  Few rows a request (decode steps, short drafts): the bytes of the cache, 256 requests
-// of 4 tokens over up to 8192 cached 684 us, 6.6 TB/s.  Prompts and large trees: shared memory.  Of a
+// of 4 tokens over up to 8192 cached 663 to 690 us, 6.6 to 6.8 TB/s.  Prompts and large trees: shared memory.  Of a
 // tile's 512 cycles of products S takes 384 instead of 256 (a product 128 x 64 x 16 reads 6 KB), V is
 // read in 128, and the copies write 32 KB in 256: 768, and 720 to 790 measured; 4 prompts of 512 to 4096
-// tokens over up to 8192 774 to 787 us, 1350 TFLOP/s.  Tried against that, and not faster: tiles of 128
+// tokens over up to 8192 756 to 800 us, 1320 to 1400 TFLOP/s.  Tried against that, and not faster: tiles of 128
 // keys with one buffer of scores (the chain of scores, softmax, output then is the bound), two row tiles
 // in a CTA, and products of a pair's 256 rows (cta_group::2, half the keys and values in each CTA: 830
 // us; the weights of both CTAs have to reach the one that issues, 0.8 us a tile for the chain).

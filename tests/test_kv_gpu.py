@@ -579,6 +579,40 @@ def test_attention_waits_of_pairs_are_bounded(D, limit):
     _check(c)
 
 
+@pytest.mark.parametrize("dtype,H,Hkv,D,new,ctx", [
+    (BF, 5, 1, 64, [20011, 3, 4096], [100, 70000, 0]), (BF, 8, 1, 128, [9001, 517], [33, 64]),
+    (BF, 1, 1, 64, [30000], [0]), (F32, 3, 1, 64, [3001, 1], [65, 5000]),
+])
+def test_attention_long_prompts_are_means(dtype, H, Hkv, D, new, ctx):
+    """Chains of many row tiles, which runs begin and end in anywhere.  With queries of zero every weight is one: a token's
+    output is the mean of the values up to it, and its lse the logarithm of their number.  Sums of n terms in fp32 are
+    off by n 2^-24 of the mean magnitude at most, before the output's own rounding."""
+    rng = np.random.default_rng(51)
+    g = torch.Generator(device=DEV).manual_seed(51)
+    T, b = sum(new), 16
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    table, total, _ = F.rand_pages(ctx, b, -(-max(ctx) // b) + 1, 1, rng)
+    kc = torch.randn(total, b, Hkv, D, generator=g, device=DEV).to(dtype)
+    vc, k, v = torch.randn_like(kc), *(torch.randn(T, Hkv, D, generator=g, device=DEV).to(dtype) for _ in range(2))
+    q = torch.zeros(T, H, D, dtype=dtype, device=DEV)
+    err = _err()
+    out, lse = ssd.kv_tree_attention(q, k, v, kc, vc, _i(cu), _i(ctx), _i(table), max(new), return_lse=True, err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    for r in range(len(new)):
+        pages = torch.from_numpy(table[r, :-(-ctx[r] // b)].astype(np.int64)).to(DEV)
+        cached = vc[pages].reshape(-1, Hkv, D)[:ctx[r]].double()
+        mine = torch.cat([cached, v[cu[r]:cu[r + 1]].double()])
+        count = torch.arange(1, len(mine) + 1, device=DEV, dtype=torch.float64)[:, None, None]
+        want, mag = (mine.cumsum(0) / count)[ctx[r]:], (mine.abs().cumsum(0) / count)[ctx[r]:]
+        n = count[ctx[r]:]
+        tol = (2 * n + 8) * F.U32 * mag + (F.UBF if dtype == BF else F.U32) * want.abs()
+        got = out[cu[r]:cu[r + 1]].double().unflatten(1, (Hkv, H // Hkv))
+        assert ((got - want[:, :, None]).abs() <= tol[:, :, None]).all()
+        want_lse = n[:, 0].log()
+        assert ((lse[cu[r]:cu[r + 1]].double() - want_lse).abs() <= 16 * F.U32 * (1 + want_lse)).all()
+
+
 def test_attention_pairs_do_not_depend_on_the_hint():
     """Tiles of as many tokens as a request is said to have, two of them side by side; and a batch where two tiles would
     work together, but no token belongs to a request."""
