@@ -20,7 +20,6 @@ constexpr int kRowTile = 16;
 constexpr int kKeyShift = 5;
 constexpr int kKeyTile = 1 << kKeyShift;
 constexpr int kOverhead = 1;  // of an item, in key tiles
-constexpr int kMinUnits = 2;
 constexpr int ctas_per_sm(int nv) { return nv <= 2 ? 4 : nv <= 4 ? 3 : 2; }  // by registers
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -72,7 +71,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NV))
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join kernel may be set up
     kvs::Walk w;
-    if (!kvs::find_run(a, g, kMinUnits, blockIdx.x, gridDim.x, find, parts.borders, w)) return;
+    if (!kvs::find_run(a, g, blockIdx.x, gridDim.x, find, parts.borders, w)) return;
     const float c = a.scale * kLog2e;
     constexpr int kPer = 16 / (int)sizeof(T);  // entries of 16 bytes
     const int pieces = D / kPer;
@@ -298,7 +297,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NV))
 // request: 38): the CTA's four warps then share a row's.
 constexpr int kJoinThreads = 128;
 constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kFewRows = 32;     // tiles of at most so many rows
 constexpr int kAloneParts = 4;   // items of at most so many parts have a warp a row there, too (16 fp32 requests of
                                  // up to 2000 keys 29.2 us, 30.5 with up to 8; one of 777 14.3 us with up to 16)
 constexpr int kFlight = 4;       // parts in flight
@@ -401,7 +399,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const kv_attentio
 template <typename T, int NV>
 cudaError_t launch_join(const kv_attention_args &a, const kvs::Parts &p, int grid, const kvs::Tiling &g, cudaStream_t s) {
     // a programmatic dependent of the attention kernel: its CTAs may be set up while that ends
-    const bool few = g.rows <= kFewRows;
+    const bool few = g.rows <= kvs::kFewRows;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)(few ? g.rows : kvs::ceil_div(g.rows, kJoinWarps)));
     cfg.blockDim = dim3(kJoinThreads);
@@ -415,7 +413,11 @@ cudaError_t launch_join(const kv_attention_args &a, const kvs::Parts &p, int gri
                : cudaLaunchKernelEx(&cfg, kv_join_kernel<T, NV, false>, a, p, g);
 }
 
-kvs::Tiling simt_tiling(const kv_attention_args &a) { return kvs::tiling(a, kRowTile, kKeyShift, kOverhead); }
+kvs::Tiling simt_tiling(const kv_attention_args &a) {
+    kvs::Tiling g = kvs::tiling(a, kRowTile, kKeyShift, kOverhead, 1);
+    g.min_units = 2;
+    return g;
+}
 
 // 32-float pieces of a row that the kernel for this head size covers
 int pieces_of(int D) { return D <= 64 ? 2 : D <= 128 ? 4 : 8; }
@@ -427,7 +429,7 @@ int smem_of(const kv_attention_args &a) {
 int simt_grid(const kv_attention_args &a, const kvs::Tiling &g) {
     const int by_smem = (227 * 1024) / (smem_of(a) + 3 * 1024);  // with what a CTA takes besides
     const int ctas = ctas_per_sm(pieces_of(a.headdim));
-    return kvs::grid_of(a, g, kMinUnits, (by_smem < ctas ? by_smem : ctas) * device_sms());
+    return kvs::grid_of(a, g, (by_smem < ctas ? by_smem : ctas) * device_sms());
 }
 
 template <typename T, int NV>

@@ -54,7 +54,6 @@ constexpr int kThreads = 192;
 constexpr int kLoadWarp = 4, kMmaWarp = 5;
 constexpr int kStages = 5;
 constexpr int kOverhead = 3;  // of an item, in key tiles
-constexpr int kMinUnits = 1;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;  // growth of a maximum (base 2) that is let stand
@@ -225,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     kvs::Walk w;
     const bool work =
-        kvs::find_run(a, p.g, kMinUnits, worker, gridDim.x / kPair, *reinterpret_cast<kvs::FindSmem *>(smem + L::kFind),
+        kvs::find_run(a, p.g, worker, gridDim.x / kPair, *reinterpret_cast<kvs::FindSmem *>(smem + L::kFind),
                       p.parts.borders, w);
     const bool aligned = (smem_u32(smem) & 1023u) == 0;  // the swizzled tiles need a 1024-byte aligned base
     if (!aligned && tid == 0) report(a.err_word, SSD_DEVERR_INTERNAL);
@@ -563,8 +562,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                     } else if (tok >= 0) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4)
-                            *reinterpret_cast<uint4 *>(sums + d + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        for (int j = 0; j < 32; j += 8) st_global_32(sums + d + j, o + j);  // whole sectors: trees 188 to 184 us
                     }
                 }
                 if (tok >= 0) {
@@ -603,16 +601,11 @@ int pair_for(const kv_attention_args &a) {
     return many && (a.mask_words > 0 || 2 * (kRows / group) <= kKeys) ? 2 : 1;
 }
 
-kvs::Tiling tc_tiling(const kv_attention_args &a) {
-    kvs::Tiling g = kvs::tiling(a, kRows, kKeyShift, kOverhead);
-    g.tokens *= pair_for(a);
-    g.rows *= pair_for(a);
-    return g;
-}
+kvs::Tiling tc_tiling(const kv_attention_args &a) { return kvs::tiling(a, kRows, kKeyShift, kOverhead, pair_for(a)); }
 
 // workers: CTAs or pairs
 int tc_workers(const kv_attention_args &a, const kvs::Tiling &g) {
-    return kvs::grid_of(a, g, kMinUnits, 2 * device_sms() / pair_for(a));
+    return kvs::grid_of(a, g, 2 * device_sms() / pair_for(a));
 }
 
 template <int D, int kPair> cudaError_t launch(const kv_attention_args &a, void *ws, cudaStream_t s) {

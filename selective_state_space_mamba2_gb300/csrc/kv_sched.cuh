@@ -27,6 +27,14 @@ __device__ __forceinline__ unsigned long long quotient(unsigned long long n, uns
     return (n | d) >> 32 ? n / d : (uint32_t)n / (uint32_t)d;
 }
 
+// Square root, of whatever accuracy; the rounded one's special cases cost the kernels registers all along (trees
+// 177 to 183 us).
+__device__ __forceinline__ float root(float v) {
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // `total` units cut into `runs` runs: the first `rem` of them have base + 1, the others base.
 struct Cut {
     unsigned long long base, rem;
@@ -63,6 +71,8 @@ __device__ __forceinline__ Request request(const kv_attention_args &a, int32_t r
     return q;
 }
 
+constexpr int kFewRows = 32;  // tiles of at most so many rows are decode's: the join shares their parts over warps
+
 struct Tiling {
     int32_t tokens;     // tokens of a row tile
     int32_t heads;      // query heads of a row tile (the last part of a token may have fewer)
@@ -70,6 +80,8 @@ struct Tiling {
     int32_t key_shift;  // key tiles of 2^key_shift
     int32_t overhead;   // units an item counts besides its key tiles
     int32_t rows;       // rows a tile is given in the workspace: tokens * heads
+    int32_t min_units;  // a run is at least about that long
+    float part_cost;    // what a part costs in the join, in units
 };
 
 __host__ __device__ __forceinline__ int32_t ceil_div(int32_t n, int32_t d) { return n / d + (n % d != 0); }
@@ -168,16 +180,22 @@ struct Walk {
 
 struct FindSmem {
     unsigned long long sum[32];
+    uint32_t longest[32];
     Walk w;
 };
 
 // Called by all threads of the CTA (blockDim.x a multiple of 32): the run of worker `me` of `of` (a CTA,
-// or a pair of them that share their runs), or false when it has none.  min_units: a run is at least
-// about that long.  Latency is all that counts here: lengths are read once, S / blockDim.x requests a thread,
-// sums over a prompt's token blocks are closed forms (prompts of up to 4096 tokens 5.2 to 3.6 us), and where a
-// run starts is worked out by the one thread that has its request.
-__device__ __forceinline__ bool find_run(const kv_attention_args &a, const Tiling &g, int32_t min_units, int32_t me,
-                                         int32_t of, FindSmem &sm, Border *borders, Walk &w) {
+// or a pair of them that share their runs), or false when it has none.  Latency is all that counts here:
+// lengths are read once, S / blockDim.x requests a thread, sums over a prompt's token blocks are closed forms
+// (prompts of up to 4096 tokens 5.2 to 3.6 us), and where a run starts is worked out by the one thread that has
+// its request.
+//
+// Shortest run.  An item of L units cut into runs of u takes u + c L / u, with a part's cost c in the join: least at
+// u = sqrt(c L).  With runs of 1 / 4 units 2 requests of 20 to 31 tokens over 5419, 8 query heads, take 28.4 /
+// 19.4 us (c = 0.4: 5.9), one of 200 tokens 19.0 / 15.3 (min_units), 5 of up to 4 tokens over 2287 16.6 / 13.4
+// (c = 0.1: 1.9), but one token over 777 10.5 / 12.7 (1.3).
+__device__ __forceinline__ bool find_run(const kv_attention_args &a, const Tiling &g, int32_t me, int32_t of,
+                                         FindSmem &sm, Border *borders, Walk &w) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nwarp = nthr >> 5;
     const int S = a.num_seqs;
     const unsigned long long heads = (unsigned long long)a.kv_heads;
@@ -185,27 +203,32 @@ __device__ __forceinline__ bool find_run(const kv_attention_args &a, const Tilin
     Request q;
     unsigned long long per_head = 0, own = 0;
     q.q0 = q.n = q.c = 0;
+    uint32_t longest = 0;
     for (int r = r0; r < r1; ++r) {
         q = request(a, r, blockIdx.x == 0);
         per_head = (unsigned long long)units_of(a, q, g);
         own += per_head * heads;
+        if (q.n > 0) longest = max(longest, (uint32_t)(g.overhead + tiles_of(g, q.c) + tiles_of(g, q.n)));
     }
+    longest = __reduce_max_sync(~0u, longest);
     unsigned long long sum = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const unsigned long long v = __shfl_up_sync(~0u, sum, o);
         if (lane >= o) sum += v;
     }
-    if (lane == 31) sm.sum[warp] = sum;
+    if (lane == 31) sm.sum[warp] = sum, sm.longest[warp] = longest;
     __syncthreads();
     unsigned long long before = sum - own, total = 0;
     for (int i = 0; i < nwarp; ++i) {
         const unsigned long long v = sm.sum[i];
         if (i < warp) before += v;
         total += v;
+        longest = max(longest, sm.longest[i]);
     }
-    const unsigned long long most = quotient(total + min_units - 1, min_units);
-    const uint32_t runs = (uint32_t)(most < (unsigned)of ? most : (unsigned)of);
+    const uint32_t shortest = max((uint32_t)root(g.part_cost * (float)longest), (uint32_t)g.min_units);
+    // (more units than 32 bits hold are enough for all)
+    const uint32_t runs = total >> 31 ? (uint32_t)of : min(((uint32_t)total + shortest - 1) / shortest, (uint32_t)of);
     if ((uint32_t)me >= runs) {
         if (tid == 0) borders[me].parts = 0;
         return false;
@@ -236,7 +259,7 @@ __device__ __forceinline__ bool find_run(const kv_attention_args &a, const Tilin
             // units before block b are about parts (b^2 t / 2K + b (fixed + t / 2K + 1/2)): the root, then the last step
             const float half = 0.5f * (float)g.tokens / (float)(1 << g.key_shift), c = (float)fixed + half + 0.5f;
             const float u = (float)off / (float)g.parts;
-            w.b = min((int32_t)(2.f * u / (c + sqrtf(c * c + 4.f * half * u))), w.blocks - 1);
+            w.b = min((int32_t)(2.f * u / (c + root(c * c + 4.f * half * u))), w.blocks - 1);
             while (w.b > 0 && (unsigned long long)units_before(a, q, g, w.b) > off) --w.b;
             while (w.b + 1 < w.blocks && (unsigned long long)units_before(a, q, g, w.b + 1) <= off) ++w.b;
         }
@@ -288,8 +311,9 @@ inline Parts parts_at(void *ws, int grid, int rows, int D) {
     return o;
 }
 
-// How a kernel with `rows` rows and 2^key_shift keys to a tile cuts these heads.
-inline Tiling tiling(const kv_attention_args &a, int rows, int key_shift, int overhead) {
+// How a kernel with `rows` rows and 2^key_shift keys to a tile cuts these heads; `side` row tiles are worked on
+// side by side.
+inline Tiling tiling(const kv_attention_args &a, int rows, int key_shift, int overhead, int side) {
     const int group = a.nheads / a.kv_heads;
     Tiling g;
     g.key_shift = key_shift;
@@ -303,16 +327,19 @@ inline Tiling tiling(const kv_attention_args &a, int rows, int key_shift, int ov
         const int hint = a.max_new_tokens > 0 ? a.max_new_tokens : 1;
         if (hint < g.tokens) g.tokens = hint;
     }
+    g.tokens *= side;
     g.rows = g.tokens * g.heads;
+    g.min_units = g.rows > rows ? 4 : 1;
+    g.part_cost = g.rows > kFewRows ? 0.4f : 0.1f;
     return g;
 }
 
 // CTAs to launch: `most` at most, fewer where the host's bounds say that there cannot be as many
 // units.
-inline int grid_of(const kv_attention_args &a, const Tiling &g, int min_units, int most) {
+inline int grid_of(const kv_attention_args &a, const Tiling &g, int most) {
     const double blocks = (double)a.total_tokens / g.tokens + (a.num_seqs < a.total_tokens ? a.num_seqs : a.total_tokens);
     const double keys = ((double)a.table_cols * a.block_size + a.total_tokens) / (1 << g.key_shift) + 2;
-    const double units = blocks * g.parts * (g.overhead + keys) * a.kv_heads / min_units;
+    const double units = blocks * g.parts * (g.overhead + keys) * a.kv_heads / g.min_units;
     return units < (double)most ? (int)(units < 1 ? 1 : units + 1) : most;
 }
 

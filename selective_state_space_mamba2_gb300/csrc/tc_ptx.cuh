@@ -108,6 +108,14 @@ __device__ __forceinline__ float2 fma_f2(float2 a, float2 b, float2 c) {
     return f2_from(r);
 }
 
+// ------------------------------------------------------- wide stores ----
+// 32 bytes, a whole sector, to a 32-byte aligned address.
+__device__ __forceinline__ void st_global_32(void *p, const uint32_t *v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // ---------------------------------------------------------------- fences ----
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
