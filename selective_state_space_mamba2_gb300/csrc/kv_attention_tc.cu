@@ -25,7 +25,7 @@
 // of 4 tokens over up to 8192 cached 663 to 690 us, 6.6 to 6.8 TB/s.  Prompts and large trees: shared memory.  Of a
 // tile's 512 cycles of products S takes 384 instead of 256 (a product 128 x 64 x 16 reads 6 KB), V is
 // read in 128, and the copies write 32 KB in 256: 768, and 720 to 790 measured; 4 prompts of 512 to 4096
-// tokens over up to 8192 756 to 800 us, 1320 to 1400 TFLOP/s.  Tried against that, and not faster: tiles of 128
+// tokens over up to 8192 738 to 800 us, 1320 to 1430 TFLOP/s.  Tried against that, and not faster: tiles of 128
 // keys with one buffer of scores (the chain of scores, softmax, output then is the bound), two row tiles
 // in a CTA, and products of a pair's 256 rows (cta_group::2, half the keys and values in each CTA: 830
 // us; the weights of both CTAs have to reach the one that issues, 0.8 us a tile for the chain).
@@ -590,10 +590,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 // CTAs that share an item, by a rule on sizes: a pair where the requests have more rows than a tile
 // takes on the average, and its two row tiles see the same keys but for one tile of them at most: with a
 // mask, or where they are 64 tokens or fewer.  Measured alone / in pairs: 4 prompts of 512 to 4096 tokens
-// over up to 8192 cached, 4 query heads to a key head, 818 / 765 us (1 query head, nothing cached: 176 /
-// 188); 24 trees of 33 to 64 tokens over up to 16384, 8 query heads, 219 / 189 us, of 33 to 48 with 4
-// heads 302 / 203; 2 times 512 tokens over 65536 557 / 430; but a prompt of 512 tokens beside 64 single
-// tokens 183 / 224, since one CTA of the pair then has no rows most of the time.  Clusters of four that load
+// over up to 8192 cached, 4 query heads to a key head, 775 / 738 us (1 query head, nothing cached: 159 /
+// 173); 24 trees of 33 to 64 tokens over up to 16384, 8 query heads, 218 / 181 us, of 33 to 48 with 4
+// heads 304 / 195; 2 times 512 tokens over 65536 568 / 433; but a prompt of 512 tokens beside 64 single
+// tokens 187 / 221, since one CTA of the pair then has no rows most of the time.  Clusters of four that load
 // for one another: 1320 us for the prompts.
 int pair_for(const kv_attention_args &a) {
     const int64_t group = a.nheads / a.kv_heads;
