@@ -292,14 +292,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NV))
 // parts are added up, that of CTA b - 1 (which began the item) and those of the CTAs from b on:
 //   out = sum_i 2^(m_i - m) O_i / L,  L = sum_i 2^(m_i - m) l_i,  m = max_i m_i.
 // A warp sums a row.  Bound by the latency of dependent reads, border, statistics and sums, so the first sums
-// are read while the statistics are on their way; for prompts by the bytes of the parts in L2 (four rows a
+// are read while the statistics are on their way; for prompts by instructions, hence a short form for few parts
+// (trees 178 to 176 us), and the bytes of the parts in L2 (four rows a
 // warp: the same).  In tiles of few rows (decode) an item may be in dozens of parts (65536 keys of one
 // request: 38): the CTA's four warps then share a row's.
 constexpr int kJoinThreads = 128;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kAloneParts = 4;   // items of at most so many parts have a warp a row there, too (16 fp32 requests of
                                  // up to 2000 keys 29.2 us, 30.5 with up to 8; one of 777 14.3 us with up to 16)
-constexpr int kFlight = 4;       // parts in flight
 
 template <typename T, int NV, bool kFew>  // NV: 128-float pieces of a row
 __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const kv_attention_args a, const kvs::Parts parts,
@@ -313,72 +313,99 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const kv_attentio
     const bool alone = !kFew || n <= kAloneParts;
     const int row = kFew ? blockIdx.y + (alone ? warp : 0) : blockIdx.y * kJoinWarps + warp;
     if (n == 0 || row >= rows || (kFew && alone && blockIdx.y % kJoinWarps != 0)) return;
-    const int share = alone ? 0 : warp, step = alone ? 1 : kJoinWarps;  // parts of this warp
     // part k: of CTA b - 1 + k
     auto part_row = [&](int k) { return ((int64_t)(b - 1 + k) * 2 + (k == 0 ? 1 : 0)) * g.rows + row; };
-    float4 v[kFlight][NV];
-    auto read = [&](int k) {  // the last ones repeated
-#pragma unroll
-        for (int i = 0; i < kFlight; ++i) {
-            const float *src = parts.sums + part_row(k + i * step < n ? k + i * step : k) * D;
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                v[i][j] = 128 * j + 4 * lane < D ? *reinterpret_cast<const float4 *>(src + 128 * j + 4 * lane)
-                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-    };
-    if (share < n) read(share);
-    float2 st = lane < n ? parts.stats[part_row(lane)] : make_float2(-INFINITY, 0.f);  // a lane a part
-    float top = st.x;
-    for (int k = lane + 32; k < n; k += 32) {
-        const float m = parts.stats[part_row(k)].x;
-        top = m > top || m != m ? m : top;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float m = __shfl_xor_sync(~0u, top, o);
-        top = m > top || m != m ? m : top;
-    }
-    const float from = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
+    float top = -INFINITY, sum = 0.f;
     float4 acc[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < n; k0 += 32) {
-        if (k0 > 0) st = k0 + lane < n ? parts.stats[part_row(k0 + lane)] : make_float2(-INFINITY, 0.f);
-        const float f = k0 + lane < n ? exp2f(st.x - from) : 0.f;
-        sum = fmaf(f, st.y, sum);
-        for (int k = k0 + share; k < min(n, k0 + 32); k += kFlight * step) {
-            if (k > share) read(k);
+    auto read = [&](int k, float4 (&v)[NV]) {
+        const float *src = parts.sums + part_row(k) * D;
 #pragma unroll
-            for (int i = 0; i < kFlight; ++i) {
-                const float fk = __shfl_sync(~0u, f, (k + i * step) & 31);
-                if (k + i * step < n) {
+        for (int j = 0; j < NV; ++j)
+            v[j] = 128 * j + 4 * lane < D ? *reinterpret_cast<const float4 *>(src + 128 * j + 4 * lane)
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    auto add = [&](float f, const float4 (&v)[NV]) {
 #pragma unroll
-                    for (int j = 0; j < NV; ++j) {
-                        acc[j].x = fmaf(fk, v[i][j].x, acc[j].x);
-                        acc[j].y = fmaf(fk, v[i][j].y, acc[j].y);
-                        acc[j].z = fmaf(fk, v[i][j].z, acc[j].z);
-                        acc[j].w = fmaf(fk, v[i][j].w, acc[j].w);
-                    }
+        for (int j = 0; j < NV; ++j) {
+            acc[j].x = fmaf(f, v[j].x, acc[j].x);
+            acc[j].y = fmaf(f, v[j].y, acc[j].y);
+            acc[j].z = fmaf(f, v[j].z, acc[j].z);
+            acc[j].w = fmaf(f, v[j].w, acc[j].w);
+        }
+    };
+    if (!kFew && n <= kAloneParts) {  // every lane has all statistics: with many rows the instructions count
+        float4 v[kAloneParts][NV];
+        float2 st[kAloneParts];
+#pragma unroll
+        for (int k = 0; k < kAloneParts; ++k) {
+            if (k >= n) break;
+            read(k, v[k]);
+            st[k] = parts.stats[part_row(k)];
+        }
+#pragma unroll
+        for (int k = 0; k < kAloneParts; ++k) {
+            if (k >= n) break;
+            top = st[k].x > top || st[k].x != st[k].x ? st[k].x : top;
+        }
+        const float from = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int k = 0; k < kAloneParts; ++k) {
+            if (k >= n) break;
+            const float f = exp2f(st[k].x - from);
+            sum = fmaf(f, st[k].y, sum);
+            add(f, v[k]);
+        }
+    } else {
+        constexpr int kFlight = 4;  // parts in flight
+        const int share = alone ? 0 : warp, step = alone ? 1 : kJoinWarps;  // parts of this warp
+        float4 v[kFlight][NV];
+        auto read_some = [&](int k) {  // the last ones repeated
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) read(k + i * step < n ? k + i * step : k, v[i]);
+        };
+        if (share < n) read_some(share);
+        float2 st = lane < n ? parts.stats[part_row(lane)] : make_float2(-INFINITY, 0.f);  // a lane a part
+        top = st.x;
+        for (int k = lane + 32; k < n; k += 32) {
+            const float m = parts.stats[part_row(k)].x;
+            top = m > top || m != m ? m : top;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float m = __shfl_xor_sync(~0u, top, o);
+            top = m > top || m != m ? m : top;
+        }
+        const float from = top == -INFINITY ? 0.f : top;
+        for (int k0 = 0; k0 < n; k0 += 32) {
+            if (k0 > 0) st = k0 + lane < n ? parts.stats[part_row(k0 + lane)] : make_float2(-INFINITY, 0.f);
+            const float f = k0 + lane < n ? exp2f(st.x - from) : 0.f;
+            sum = fmaf(f, st.y, sum);
+            for (int k = k0 + share; k < min(n, k0 + 32); k += kFlight * step) {
+                if (k > share) read_some(k);
+#pragma unroll
+                for (int i = 0; i < kFlight; ++i) {
+                    const float fk = __shfl_sync(~0u, f, (k + i * step) & 31);
+                    if (k + i * step < n) add(fk, v[i]);
                 }
             }
         }
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    if (!alone) {
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        if (!alone) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) quarters[warp][j * 32 + lane] = acc[j];
-        __syncthreads();
-        if (warp > 0) return;
+            for (int j = 0; j < NV; ++j) quarters[warp][j * 32 + lane] = acc[j];
+            __syncthreads();
+            if (warp > 0) return;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+            for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int w = 1; w < kJoinWarps; ++w) {
-                const float4 q = quarters[w][j * 32 + lane];
-                acc[j].x += q.x, acc[j].y += q.y, acc[j].z += q.z, acc[j].w += q.w;
-            }
+                for (int w = 1; w < kJoinWarps; ++w) {
+                    const float4 q = quarters[w][j * 32 + lane];
+                    acc[j].x += q.x, acc[j].y += q.y, acc[j].z += q.z, acc[j].w += q.w;
+                }
+        }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that saw nothing: zeros
     const int64_t out_row = (int64_t)(me.token0 + row / me.heads) * a.nheads + me.head0 + row % me.heads;
