@@ -21,10 +21,13 @@ namespace {
 // rotation apart, whole lanes of entries), or anywhere (read again from memory).
 enum { kPairInside = 0, kPairLane = 1, kPairLoad = 2 };
 
-constexpr int kQkThreads = 128;
+constexpr int kQkShift = 7, kQkThreads = 1 << kQkShift;
 // CTAs of an SM: what hides the loads' latency is warps (65536 tokens of 32 + 8 heads of 128, bf16: 312,
 // 296, 295, 280 and 308 us with 4 to 8); fp32 and partners read again need more registers each.
 constexpr int qk_ctas_per_sm(int pair, int elem) { return pair == kPairLoad || elem == 4 ? 5 : 7; }
+
+// query rows that a lane group has in flight
+constexpr int qk_rows(int pair, int elem) { return (pair == kPairLoad ? 2 : 4) / (elem == 4 ? 2 : 1); }
 
 // 8 entries of a row as they lie in memory; get and set go by pairs, for packed fp32 arithmetic.
 template <typename T> struct Row8;
@@ -114,14 +117,17 @@ __device__ __forceinline__ void angles(const kv_qk_args &a, int32_t pos, int e0,
 // A row (head) is `width` lanes, 8 entries each (width: headdim / 8 rounded up to a power of two;
 // WIDTH where the kernel is made for it, else 0).  A lane group loads its first key and value row and W
 // query rows before it computes the first.
-template <typename T, int PAIR, int WIDTH>
-__global__ void __launch_bounds__(kQkThreads, qk_ctas_per_sm(PAIR, sizeof(T))) kv_qk_kernel(const kv_qk_args a, const int any_width) {
-    constexpr int W = (PAIR == kPairLoad ? 2 : 4) / (sizeof(T) == 4 ? 2 : 1);  // query rows in flight
+template <typename T, int PAIR, int WIDTH, bool kMany>
+__global__ void __launch_bounds__(kQkThreads, qk_ctas_per_sm(PAIR, sizeof(T))) kv_qk_kernel(const kv_qk_args a, const int any_width, const int any_side) {
+    constexpr int W = qk_rows(PAIR, sizeof(T));
     constexpr int kWords = 2 * (int)sizeof(T);  // 32-bit words of 8 entries
     __shared__ __align__(16) float weights[4][256];  // of q's entries and their partners, of k's
     const int width = WIDTH ? WIDTH : any_width;
     const int D = a.headdim, R = a.rotary_dim, half = R / 2;
-    const int sub = threadIdx.x & (width - 1), group = threadIdx.x / width, groups = kQkThreads / width;
+    // kMany: 2^side_shift tokens side by side, whole warps each
+    const int side_shift = kMany ? any_side : 0;
+    const int per_shift = kQkShift - side_shift, in_token = threadIdx.x & ((1 << per_shift) - 1);
+    const int sub = threadIdx.x & (width - 1), group = in_token / width, groups = (1 << per_shift) / width;
     const int e0 = sub * 8;
     const bool live = e0 < D;
     const bool want_k = a.k_out || a.k_cache;
@@ -210,22 +216,24 @@ __global__ void __launch_bounds__(kQkThreads, qk_ctas_per_sm(PAIR, sizeof(T))) k
         return y;
     };
 
-    int t = blockIdx.x;
+    int t = (blockIdx.x << side_shift) + (threadIdx.x >> per_shift);
+    const int stride = gridDim.x << side_shift;
+    if (t >= a.total_tokens) return;
     int32_t pos = R > 0 ? a.positions[t] : 0;
     int32_t slot = a.k_cache ? a.slots[t] : -1;
     while (true) {
-        const bool more = t < a.total_tokens - (int)gridDim.x;
-        const int t_next = more ? t + gridDim.x : t;
+        const bool more = t < a.total_tokens - stride;
+        const int t_next = more ? t + stride : t;
         const int32_t pos_next = R > 0 ? a.positions[t_next] : 0;
         const int32_t slot_next = a.k_cache ? a.slots[t_next] : -1;
-        if (R > 0 && (pos < 0 || pos >= a.max_position)) {  // the same for the whole CTA
-            if (threadIdx.x == 0) report(a.err_word, SSD_DEVERR_METADATA);
+        if (R > 0 && (pos < 0 || pos >= a.max_position)) {  // the same for whole warps
+            if (in_token == 0) report(a.err_word, SSD_DEVERR_METADATA);
         } else {
             T *kc = nullptr, *vc = nullptr;
             if (slot >= 0) {
                 const int32_t blk = slot / a.block_size;
                 if (blk >= a.num_blocks) {
-                    if (threadIdx.x == 0) report(a.err_word, SSD_DEVERR_SLOT);
+                    if (in_token == 0) report(a.err_word, SSD_DEVERR_SLOT);
                 } else {
                     const int64_t at = (int64_t)blk * a.cache_block_stride +
                                        (int64_t)(slot - blk * a.block_size) * a.kv_heads * D;
@@ -286,6 +294,9 @@ __global__ void __launch_bounds__(kQkThreads, qk_ctas_per_sm(PAIR, sizeof(T))) k
                 }
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
+                    // no row is left for any lane group (where all rows are full the test itself costs 1 %, or, with
+                    // interleaved pairs, gains 14)
+                    if ((kMany || PAIR == kPairInside) && j > 0 && h0 + j * groups >= a.nheads) break;
                     const int h = h0 + group + j * groups;
                     const Row8<T> o = turn(xq[j], oq[PAIR == kPairLoad ? j : 0], fa, fb, a.q_weight != nullptr);
                     if (h < a.nheads && live) o.store(out + h * D + e0);
@@ -301,11 +312,19 @@ template <typename T, int PAIR> cudaError_t launch_qk(const kv_qk_args &a, cudaS
     int width = 1;
     while (width * 8 < a.headdim) width *= 2;
     const int most = qk_ctas_per_sm(PAIR, sizeof(T)) * device_sms();
-    const dim3 grid((unsigned)(a.total_tokens < most ? a.total_tokens : most));
-    if (width == 16)  // headdim 72 to 128, the common ones: the reduction unrolled
-        kv_qk_kernel<T, PAIR, 16><<<grid, kQkThreads, 0, s>>>(a, width);
-    else
-        kv_qk_kernel<T, PAIR, 0><<<grid, kQkThreads, 0, s>>>(a, width);
+    // Tokens of few heads go side by side, as many as have all their query rows in flight in the CTA, where there are
+    // more tokens than CTAs: 8192 tokens of 8 heads of 64 29.1 to 11.2 us, 16384 of 32 62 to 45, 4096 of 16
+    // heads of 128 18.6 to 13.7 (in the kernel for one token the shift would cost 65536 tokens of 32 281 to 314).
+    int side_shift = 0;
+    while (side_shift < 2 && a.total_tokens > most << side_shift &&
+           a.nheads <= (kQkThreads / width >> (side_shift + 1)) * qk_rows(PAIR, sizeof(T)))
+        ++side_shift;
+    const int ctas = (a.total_tokens + (1 << side_shift) - 1) >> side_shift;
+    const dim3 grid((unsigned)(ctas < most ? ctas : most));
+    const auto kernel = width == 16  // headdim 72 to 128, the common ones: the reduction unrolled
+                            ? (side_shift ? kv_qk_kernel<T, PAIR, 16, true> : kv_qk_kernel<T, PAIR, 16, false>)
+                            : (side_shift ? kv_qk_kernel<T, PAIR, 0, true> : kv_qk_kernel<T, PAIR, 0, false>);
+    kernel<<<grid, kQkThreads, 0, s>>>(a, width, side_shift);
     return cudaGetLastError();
 }
 

@@ -206,6 +206,44 @@ def test_norm_rope_more_tokens_than_ctas(dtype, D, rot, inter):
     assert torch.equal(kc.flatten(0, 1)[rows], ko[keep.to(DEV)]) and torch.equal(vc.flatten(0, 1)[rows], k[keep.to(DEV)])
 
 
+@pytest.mark.parametrize("dtype,D,rot,inter,H,Hkv", [
+    (BF, 64, 64, False, 8, 2), (BF, 64, 16, True, 20, 4), (BF, 128, 128, False, 16, 16), (BF, 64, 40, False, 4, 1),
+    (F32, 64, 64, False, 8, 1), (F32, 128, 12, True, 4, 4), (BF, 8, 8, True, 33, 1), (BF, 256, 256, False, 8, 4),
+])
+def test_norm_rope_tokens_side_by_side(dtype, D, rot, inter, H, Hkv):
+    """Few heads and many tokens, of which a CTA has several at a time: the last ones alone, in place, some without a slot,
+    with a slot or a position that is none."""
+    T = 4803
+    g = torch.Generator(device=DEV).manual_seed(D + H)
+    q, k = torch.randn(T, H, D, generator=g, device=DEV).to(dtype), torch.randn(T, Hkv, D, generator=g, device=DEV).to(dtype)
+    v = torch.randn(T, Hkv, D, generator=g, device=DEV).to(dtype)
+    w = torch.randn(D, generator=g, device=DEV)
+    cs = torch.randn(5000, rot, generator=g, device=DEV)
+    at = np.arange(T) + 17
+    at[[5, 2402]] = [-1, 5000]
+    kc, vc = F.poison((T // 8 + 2, 8, Hkv, D), dtype, DEV), F.poison((T // 8 + 2, 8, Hkv, D), dtype, DEV)
+    slots = np.random.default_rng(1).permutation(T)
+    slots[[3, 4800]] = -1
+    slots[4000] = (T // 8 + 2) * 8
+    err, was = _err(), (q.clone(), k.clone())
+    qo, ko = ssd.kv_qk_norm_rope(q, k, _i(at), cs, w, w, 1e-6, inter, v, kc, vc, _i(slots), q_out=q, k_out=k, err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == ssd.DEVERR_METADATA | ssd.DEVERR_SLOT
+    keep = torch.ones(T, dtype=torch.bool)
+    keep[[5, 2402]] = False
+    at[[5, 2402]] = 0
+    for got, x in ((qo, was[0]), (ko, was[1])):
+        want, mag = F.norm_rope(x, w, cs, _i(at), 1e-6, inter)
+        assert ((got.double().cpu() - want).abs() <= F.rope_bound(want, mag, D, dtype))[keep].all()
+        assert torch.equal(got[~keep.to(DEV)], x[~keep.to(DEV)])
+    keep[[3, 4800, 4000]] = False
+    rows = torch.from_numpy(slots[keep.numpy()]).to(DEV)
+    assert torch.equal(kc.flatten(0, 1)[rows], ko[keep.to(DEV)]) and torch.equal(vc.flatten(0, 1)[rows], v[keep.to(DEV)])
+    rest = torch.ones(kc.shape[0] * 8, dtype=torch.bool, device=DEV)
+    rest[rows] = False
+    assert torch.isnan(kc.flatten(0, 1)[rest]).all() and torch.isnan(vc.flatten(0, 1)[rest]).all()
+
+
 @pytest.mark.parametrize("rot", [64, 40])
 def test_norm_rope_in_place_and_without_norm(rot):
     T, H, Hkv, D = 9, 3, 3, 64
