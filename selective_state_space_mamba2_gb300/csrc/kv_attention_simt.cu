@@ -440,11 +440,7 @@ cudaError_t launch_join(const kv_attention_args &a, const kvs::Parts &p, int gri
                : cudaLaunchKernelEx(&cfg, kv_join_kernel<T, NV, false>, a, p, g);
 }
 
-kvs::Tiling simt_tiling(const kv_attention_args &a) {
-    kvs::Tiling g = kvs::tiling(a, kRowTile, kKeyShift, kOverhead, 1);
-    g.min_units = 2;
-    return g;
-}
+kvs::Tiling simt_tiling(const kv_attention_args &a) { return kvs::tiling(a, kRowTile, kKeyShift, kOverhead, 1); }
 
 // 32-float pieces of a row that the kernel for this head size covers
 int pieces_of(int D) { return D <= 64 ? 2 : D <= 128 ? 4 : 8; }
