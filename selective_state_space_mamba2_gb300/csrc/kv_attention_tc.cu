@@ -15,17 +15,15 @@
 // warps 0-3 softmax and output, warp 4 TMA loads, warp 5 the products.  Keys and values pass
 // through one ring of 64-row tiles in the order they are used: K0 K1 V0 K2 V1 ...
 //
-// Requests of more rows than a tile takes (prompts, larger trees) are worked on by pairs of CTAs, a
-// cluster of two: an item is then two row tiles, one a CTA, and both walk over the same keys.  CTA 0
-// of the pair loads each tile of keys into both CTAs' shared memory (TMA multicast), CTA 1 each
-// tile of values, so a pair reads from L2 what one CTA alone would; a slot of the ring is loaded again
-// when the products of both have read it (tcgen05.commit to both CTAs' barriers).
+// Requests of more rows than a tile takes (prompts, larger trees) are worked on by pairs of CTAs: an item
+// is then two row tiles, one a CTA, and both walk over the same keys at about the same time, so that the
+// one that comes second finds them in L2.  Neither waits for the other.
 //
 // What bounds it.  Few rows a request (decode steps, short drafts): the bytes of the cache, 256 requests
 // of 4 tokens over up to 8192 cached 663 to 690 us, 6.6 to 6.8 TB/s.  Prompts and large trees: shared memory.  Of a
 // tile's 512 cycles of products S takes 384 instead of 256 (a product 128 x 64 x 16 reads 6 KB), V is
 // read in 128, and the copies write 32 KB in 256: 768, and 720 to 790 measured; 4 prompts of 512 to 4096
-// tokens over up to 8192 738 to 800 us, 1320 to 1430 TFLOP/s.  Tried against that, and not faster: tiles of 128
+// tokens over up to 8192 747 to 777 us, 1360 to 1410 TFLOP/s.  Tried against that, and not faster: tiles of 128
 // keys with one buffer of scores (the chain of scores, softmax, output then is the bound), two row tiles
 // in a CTA, and products of a pair's 256 rows (cta_group::2, half the keys and values in each CTA: 830
 // us; the weights of both CTAs have to reach the one that issues, 0.8 us a tile for the chain).
@@ -196,8 +194,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const kv_attention_args &a = p.a;
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
     const int group = a.nheads / a.kv_heads;
-    const int rank = kPair > 1 ? (int)cluster_rank() : 0, worker = blockIdx.x / kPair;
-    constexpr uint16_t kBoth = 3;
+    const int rank = blockIdx.x % kPair, worker = blockIdx.x / kPair;
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + L::kBars);
     uint32_t *sTmem = reinterpret_cast<uint32_t *>(smem + L::kMisc);
     volatile int *dead = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
@@ -217,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         tma_prefetch_desc(&tmKn);
         tma_prefetch_desc(&tmVn);
         for (int i = 0; i < NUM_BARS; ++i)
-            mbar_init(&bar[i], i == P_READY0 || i == P_READY1 ? 4 : i >= KV_EMPTY0 ? kPair : 1);
+            mbar_init(&bar[i], i == P_READY0 || i == P_READY1 ? 4 : 1);
         fence_mbar_init();
         *dead = 0;
         dirty[0] = dirty[1] = 0;
@@ -229,10 +226,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool aligned = (smem_u32(smem) & 1023u) == 0;  // the swizzled tiles need a 1024-byte aligned base
     if (!aligned && tid == 0) report(a.err_word, SSD_DEVERR_INTERNAL);
     tc_fence_before();
-    if (kPair > 1)
-        cluster_sync();  // both CTAs' barriers are set up
-    else
-        __syncthreads();
+    __syncthreads();
     tc_fence_after();
     const uint32_t tm = *sTmem;
     const Waiter wait{dead, a.err_word, p.wait_limit};
@@ -281,7 +275,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int boxes = (min(kKeys, (cached ? w.q.c : w.new_seen) - base) + (1 << shift) - 1) >> shift;
             if (lane == 0) mbar_arrive_expect_tx(full, (boxes * kHalves * 128) << shift);
             __syncwarp();
-            if (kPair > 1 && rank != value) return;
             if (cached && my_box < boxes) {
                 int32_t id = g.id;
                 if (id < 0 || id >= a.num_blocks) {
@@ -290,18 +283,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 uint8_t *to = dst + my_half * (kKeys * 128) + (my_box << shift) * 128;
                 const CUtensorMap *map = value ? &tmVc : &tmKc;
-                if (kPair == 1)
-                    tma_load_5d(to, map, 0, g.off, my_half, w.h, id, full);
-                else
-                    tma_load_5d_multi(to, map, 0, g.off, my_half, w.h, id, full, kBoth);
+                tma_load_5d(to, map, 0, g.off, my_half, w.h, id, full);
             } else if (!cached && new_box < boxes) {
                 uint8_t *to = dst + new_half * (kKeys * 128) + (new_box << shift) * 128;
                 const CUtensorMap *map = value ? &tmVn : &tmKn;
-                const int32_t row = w.q.q0 + base + (new_box << shift);
-                if (kPair == 1)
-                    tma_load_4d(to, map, 0, row, new_half, w.h, full);
-                else
-                    tma_load_4d_multi(to, map, 0, row, new_half, w.h, full, kBoth);
+                tma_load_4d(to, map, 0, w.q.q0 + base + (new_box << shift), new_half, w.h, full);
             }
             __syncwarp();
         };
@@ -327,15 +313,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             load(true, w.t1 - 1, before);
             more = w.next(a, p.g);
         }
-        // stages used, their last phases: st's was one round ago
-        const auto last_phase = [&](uint32_t k) { return phase ^ (k >= st); };
         if (__any_sync(~0u, *dead)) {  // copies in flight land before the CTA may go
-            for (uint32_t k = 0; k < kStages && k < slots; ++k) mbar_wait(&bar[KV_FULL0 + k], last_phase(k), 20000000ll);
+            // stages used, their last phases: st's was one round ago
+            for (uint32_t k = 0; k < kStages && k < slots; ++k) mbar_wait(&bar[KV_FULL0 + k], phase ^ (k >= st), 20000000ll);
             mbar_wait(&bar[Q_FULL], (items - 1) & 1, 20000000ll);
-            if (kPair > 1)  // and so do those that the other CTA has sent here without this one's asking
-                for (const long long t0 = clock64(); clock64() - t0 < 200000;) __nanosleep(1000);
-        } else if (kPair > 1) {  // nor does the other's last commit arrive at a CTA that is gone
-            for (uint32_t k = 0; k < kStages && k < slots; ++k) wait(&bar[KV_EMPTY0 + k], last_phase(k));
         }
     } else if (warp == kMmaWarp) {
         // ---- products --------------------------------------------------------------
@@ -357,19 +338,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         auto advance = [&]() {
             if (++st == kStages) st = 0, phase ^= 1;
         };
-        // A CTA that gave up says nothing more to the other of its pair, which then gives up too, instead of
-        // counting arrivals that stand for nothing.
-        auto alive = [&]() { return kPair == 1 || !__any_sync(~0u, *dead); };
-        auto let_go = [&](uint32_t stage, bool tell) {
-            if (kPair == 1)
-                mma_commit(&bar[KV_EMPTY0 + stage]);
-            else if (tell)
-                mma_commit_multi(&bar[KV_EMPTY0 + stage], kBoth);
-        };
         auto scores = [&](uint32_t g, bool last) {  // of tile number g, the item's last or not
             wait(&bar[KV_FULL0 + st], phase);
             tc_fence_after();
-            const bool tell = alive();
             const uint32_t sg = __shfl_sync(~0u, st, 0), gg = __shfl_sync(~0u, g, 0);
             const uint64_t k0 = desc_at(dK, sg * L::kTile);
             const uint32_t d = tmu + COL_S + 64 * (gg & 1);
@@ -379,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     mma_ss(d, desc_at(dQ, (k >> 2) * (kRows * 128) + (k & 3) * 32),
                            desc_at(k0, (k >> 2) * (kKeys * 128) + (k & 3) * 32), kIdS, k > 0);
                 mma_commit(&bar[S_FULL0 + (gg & 1)]);
-                let_go(sg, tell);
+                mma_commit(&bar[KV_EMPTY0 + sg]);
                 if (last) mma_commit(&bar[Q_EMPTY]);
             }
             __syncwarp();
@@ -392,13 +363,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint32_t p0 = tmu + COL_S + 64 * (gg & 1);
             wait(&bar[P_READY0 + (g & 1)], (g >> 1) & 1);
             tc_fence_after();
-            const bool tell = alive();
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
                     mma_ts(tmu + COL_O, p0 + 8 * k, desc_at(v0, 2048 * k), kIdO, k > 0 ? 1u : add);
                 mma_commit(&bar[O_DONE0 + (gg & 1)]);
-                let_go(sg, tell);
+                mma_commit(&bar[KV_EMPTY0 + sg]);
             }
             __syncwarp();
             advance();
@@ -577,10 +547,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     }
     tc_fence_before();
-    if (kPair > 1)
-        cluster_sync();  // the other CTA's copies and commits come here, too
-    else
-        __syncthreads();
+    __syncthreads();
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tm, kTmemCols);
@@ -590,11 +557,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 // CTAs that share an item, by a rule on sizes: a pair where the requests have more rows than a tile
 // takes on the average, and its two row tiles see the same keys but for one tile of them at most: with a
 // mask, or where they are 64 tokens or fewer.  Measured alone / in pairs: 4 prompts of 512 to 4096 tokens
-// over up to 8192 cached, 4 query heads to a key head, 775 / 738 us (1 query head, nothing cached: 159 /
-// 173); 24 trees of 33 to 64 tokens over up to 16384, 8 query heads, 218 / 181 us, of 33 to 48 with 4
-// heads 304 / 195; 2 times 512 tokens over 65536 568 / 433; but a prompt of 512 tokens beside 64 single
-// tokens 187 / 221, since one CTA of the pair then has no rows most of the time.  Clusters of four that load
-// for one another: 1320 us for the prompts.
+// over up to 8192 cached, 4 query heads to a key head, 771 / 747 to 777 us; 24 trees of 33 to 64 tokens over up
+// to 16384, 8 query heads, 209 / 184 to 188 us, of 33 to 48 with 4 heads 297 / 184; 2 times 512 tokens over 65536
+// 553 / 444; 64 requests of 1 to 600 over up to 8192 1632 / 1210; but a prompt of 512 tokens beside 64 single
+// tokens 187 / 221, since one CTA of the pair then has no rows most of the time.
 int pair_for(const kv_attention_args &a) {
     const int64_t group = a.nheads / a.kv_heads;
     const bool many = (int64_t)a.total_tokens * group > (int64_t)kRows * a.num_seqs;
@@ -646,18 +612,8 @@ template <int D, int kPair> cudaError_t launch(const kv_attention_args &a, void 
     const auto kernel = kv_attention_tc_kernel<D, kPair>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(workers * kPair));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kPair;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = kPair > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, kernel, q, kc, vc, kn, vn, p);
+    kernel<<<workers * kPair, kThreads, smem, s>>>(q, kc, vc, kn, vn, p);
+    e = cudaGetLastError();
     return e != cudaSuccess ? e : kvs::join_launch(a, p.parts, workers, p.g, s);
 }
 

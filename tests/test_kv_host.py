@@ -1,6 +1,7 @@
 """Host-side refusals of the attention-side calls (no GPU): every argument check returns before anything is launched, and
 the binding refuses wrong shapes, types and host tensors."""
 import ctypes
+import os
 
 import pytest
 import torch
@@ -135,3 +136,12 @@ def test_binding_refuses_host_tensors():
         ssd.kv_tree_attention(x, x, x, kc, kc, torch.zeros(2, dtype=torch.int32), i[:1], i[:1].view(1, 1), 2)
     with pytest.raises(ValueError, match="CUDA tensor"):
         ssd.kv_commit_tokens(x, x, kc, kc, i)
+
+
+def test_no_load_goes_to_several_ctas():
+    """One library serves every rank of a run on several GPUs, and the caller's pointers say whose memory is read: the kernels
+    hold no multicast load, and no CTA's shared memory is written by another's copies."""
+    src = os.path.join(os.path.dirname(os.path.abspath(ssd.__file__)), "csrc")
+    for name in sorted(os.listdir(src)):
+        with open(os.path.join(src, name)) as f:
+            assert "multicast" not in f.read(), name
