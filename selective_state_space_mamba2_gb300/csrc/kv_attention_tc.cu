@@ -235,8 +235,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         // nothing to do
     } else if (warp == kLoadWarp) {
         // ---- loads -----------------------------------------------------------------
-        uint32_t st = 0, phase = 0, slots = 0;  // ring stage, its phase, stages used
+        uint32_t st = 0, phase = 0;         // ring stage, its phase
         uint32_t items = 0;
+        uint32_t asked = 0, asked_q = 0;    // tiles and query tiles whose copies were asked for: all up to a wait that gave up
         // one copy brings both halves of the columns where it brings all rows
         const int per = kHalves / p.box_halves, my_box = lane / per, my_half = lane % per;
         const int new_per = kHalves / p.new_halves, new_box = lane / new_per, new_half = lane % new_per;
@@ -266,9 +267,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             wait(&bar[KV_EMPTY0 + st], phase ^ 1);
             uint8_t *dst = smem + L::kRing + st * L::kTile;
             uint64_t *full = &bar[KV_FULL0 + st];
-            ++slots;
             if (++st == kStages) st = 0, phase ^= 1;
             if (__any_sync(~0u, *dead)) return;
+            ++asked;
             const bool cached = t < w.cached_tiles;
             const int base = (cached ? t : t - w.cached_tiles) * kKeys;
             const int shift = cached ? p.box_shift : p.new_shift;
@@ -297,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             wait(&bar[Q_EMPTY], (items & 1) ^ 1);
             ++items;
             if (!__any_sync(~0u, *dead)) {
+                asked_q = items;
                 if (lane == 0) mbar_arrive_expect_tx(&bar[Q_FULL], kHalves * p.tile_tokens * group * 128);
                 __syncwarp();
                 if (lane < kHalves)
@@ -313,11 +315,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             load(true, w.t1 - 1, before);
             more = w.next(a, p.g);
         }
-        if (__any_sync(~0u, *dead)) {  // copies in flight land before the CTA may go
-            // stages used, their last phases: st's was one round ago
-            for (uint32_t k = 0; k < kStages && k < slots; ++k) mbar_wait(&bar[KV_FULL0 + k], phase ^ (k >= st), 20000000ll);
-            mbar_wait(&bar[Q_FULL], (items - 1) & 1, 20000000ll);
-        }
+        // The copies asked for land before the CTA may go, whether a wait gave up before the last was asked for, gives
+        // up after it, or none does (then the products have waited for them).
+        for (uint32_t k = 0; k < kStages && k < asked; ++k)
+            mbar_wait(&bar[KV_FULL0 + k], (asked - 1 - k) / kStages & 1, 20000000ll);
+        if (asked_q > 0) mbar_wait(&bar[Q_FULL], (asked_q - 1) & 1, 20000000ll);
     } else if (warp == kMmaWarp) {
         // ---- products --------------------------------------------------------------
         // The whole warp walks along, one lane issues.  Order: S of tile 0, then for every tile t

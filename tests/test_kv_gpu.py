@@ -617,6 +617,24 @@ def test_attention_waits_of_pairs_are_bounded(D, limit):
     _check(c)
 
 
+@pytest.mark.parametrize("H,D,new,ctx", [(8, 64, [2, 1, 30], [300, 40, 90]), (4, 128, [1] * 40, [100] * 40),
+                                         (8, 128, [40, 30, 64, 17], [300, 400, 0, 90])])
+def test_attention_that_gave_up_leaves_nothing_behind(H, D, new, ctx):
+    """Waits that give up at any time, in runs of so few tiles that all copies are asked for before: the next call, queued at
+    once, gets the shared memory that copies of the one before would still be written to, and is right."""
+    c = _attn(BF, H, 1, D, 16, new, ctx, False, seed=45)
+    good, lse = _run(c, _err())
+    errs, outs = [], []
+    for limit in [1, 20, 100, 300] + list(range(500, 6000, 250)):
+        errs.append(_err())
+        _run(c, errs[-1], wait_limit_cycles=limit)
+        outs.append(_run(c, None))
+    torch.cuda.synchronize()
+    assert all(int(e.item()) in (0, ssd.DEVERR_TIMEOUT) for e in errs) and int(errs[0].item()) == ssd.DEVERR_TIMEOUT
+    for o, l in outs:
+        assert torch.equal(o, good) and torch.equal(l, lse)
+
+
 @pytest.mark.parametrize("dtype,H,Hkv,D,new,ctx", [
     (BF, 5, 1, 64, [20011, 3, 4096], [100, 70000, 0]), (BF, 8, 1, 128, [9001, 517], [33, 64]),
     (BF, 1, 1, 64, [30000], [0]), (F32, 3, 1, 64, [3001, 1], [65, 5000]),
