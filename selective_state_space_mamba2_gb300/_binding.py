@@ -578,7 +578,8 @@ def mamba1_state_update(x, dt, A, B, C, state_cache, state_indices, num_accepted
 #
 # These calls are made between kernels of a few microseconds, so their arguments are checked and
 # marshalled by a compiled module (csrc/kv_calls.cpp) instead of ctypes; the structures above are the
-# same ABI for callers that fill them themselves.
+# same ABI for callers that fill them themselves.  All tensors of a call, and its stream, are on one
+# device, which the call makes the current one while it runs.
 
 _calls = None
 

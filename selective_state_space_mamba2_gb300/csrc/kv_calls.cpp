@@ -10,6 +10,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <Python.h>
 #include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -38,10 +39,21 @@ std::string shape_text(at::IntArrayRef s) {
     return o + "]";
 }
 
+// The device of a call is that of its first tensor; every other one has to be there too.
+thread_local int call_device = -1;
+
+void on_call_device(int index, const char *name) {
+    if (call_device < 0) call_device = index;
+    if (index != call_device)
+        refuse(std::string(name) + " is on cuda:" + std::to_string(index) + ", other arguments are on cuda:" +
+               std::to_string(call_device));
+}
+
 const at::Tensor &tensor(PyObject *o, const char *name) {
     if (!THPVariable_Check(o)) refuse(std::string(name) + (o == Py_None ? " is required" : " must be a CUDA tensor"));
     const at::Tensor &t = THPVariable_Unpack(o);
     if (!t.is_cuda()) refuse(std::string(name) + " must be a CUDA tensor");
+    on_call_device(t.get_device(), name);
     return t;
 }
 
@@ -143,6 +155,13 @@ uint32_t *error_word(PyObject *o) { return o == Py_None ? nullptr : static_cast<
 ssd_stream_t stream_of(PyObject *o, const at::Tensor &like) {
     if (o == Py_None)
         return reinterpret_cast<ssd_stream_t>(c10::cuda::getCurrentCUDAStream(like.get_device()).stream());
+    if (PyObject_HasAttrString(o, "device_index")) {
+        PyObject *index = PyObject_GetAttrString(o, "device_index");
+        const long i = index ? PyLong_AsLong(index) : -1;
+        Py_XDECREF(index);
+        if (PyErr_Occurred()) throw PythonError{};
+        on_call_device((int)i, "stream");
+    }
     PyObject *p = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream") : PyNumber_Index(o);
     if (!p) throw PythonError{};
     const unsigned long long v = PyLong_AsUnsignedLongLong(p);
@@ -176,6 +195,7 @@ PyObject *status(ssd_status_t s) { return PyLong_FromLong((long)s); }
 
 PyObject *block_tables(PyObject *const *a, PyObject *) {
     const at::Tensor &ctx = tensor(a[0], "context_lens");
+    const c10::cuda::CUDAGuard guard(ctx.device());
     const int64_t S = ctx.numel();
     kv_tables_args p = {};
     p.num_reqs = size32(S, "requests");
@@ -252,6 +272,7 @@ PyObject *block_tables(PyObject *const *a, PyObject *) {
 
 PyObject *norm_rope(PyObject *const *a, PyObject *) {
     const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k");
+    const c10::cuda::CUDAGuard guard(q.device());
     if (q.dim() != 3 || k.dim() != 3) refuse("q and k must be [T, heads, D]");
     const int64_t T = q.size(0), H = q.size(1), D = q.size(2), G = k.size(1);
     const ScalarType type = q.scalar_type();
@@ -311,6 +332,7 @@ PyObject *norm_rope(PyObject *const *a, PyObject *) {
 
 PyObject *tree_attention(PyObject *const *a, PyObject *) {
     const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k_new");
+    const c10::cuda::CUDAGuard guard(q.device());
     if (q.dim() != 3 || k.dim() != 3) refuse("q and k_new must be [T, heads, D]");
     const int64_t T = q.size(0), H = q.size(1), D = q.size(2), G = k.size(1);
     const ScalarType type = q.scalar_type();
@@ -378,6 +400,7 @@ PyObject *tree_attention(PyObject *const *a, PyObject *) {
 
 PyObject *commit_tokens(PyObject *const *a, PyObject *) {
     const at::Tensor &k = tensor(a[0], "k_new");
+    const c10::cuda::CUDAGuard guard(k.device());
     if (k.dim() != 3) refuse("k_new must be [T, heads, D]");
     const int64_t T = k.size(0), H = k.size(1), D = k.size(2);
     const ScalarType type = k.scalar_type();
@@ -428,12 +451,21 @@ PyObject *commit_tokens(PyObject *const *a, PyObject *) {
     return Py_NewRef(out);
 }
 
+// The device that a call with tensors on the devices of these two indices runs on (the check that tensor() makes, for
+// machines without a second one).
+PyObject *device_of_call(PyObject *const *a, PyObject *) {
+    on_call_device(int32(a[0], "index"), "first");
+    on_call_device(int32(a[1], "index"), "second");
+    return PyLong_FromLong(call_device);
+}
+
 template <PyObject *(*Fn)(PyObject *const *, PyObject *), Py_ssize_t kArgs>
 PyObject *guarded(PyObject *self, PyObject *const *args, Py_ssize_t n) {
     if (n != kArgs) {
         PyErr_Format(PyExc_TypeError, "%zd arguments expected, got %zd", kArgs, n);
         return nullptr;
     }
+    call_device = -1;
     try {
         return Fn(args, self);
     } catch (const PythonError &) {
@@ -449,6 +481,7 @@ PyObject *guarded(PyObject *self, PyObject *const *args, Py_ssize_t n) {
     {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<fn, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {KV_METHOD("block_tables", block_tables, 13), KV_METHOD("norm_rope", norm_rope, 16),
                          KV_METHOD("tree_attention", tree_attention, 18), KV_METHOD("commit_tokens", commit_tokens, 12),
+                         KV_METHOD("device_of_call", device_of_call, 2),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kv_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

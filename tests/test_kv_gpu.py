@@ -746,6 +746,19 @@ def test_commit_all_tokens_and_errors():
     assert torch.equal(flat[7], k[7]) and torch.equal(flat[9], k[10])
 
 
+# ------------------------------------------------------------------ binding --
+
+def test_a_stream_of_another_device_is_refused():
+    class Elsewhere:
+        cuda_stream, device_index = 0, torch.cuda.current_device() + 1
+
+    k, kc = torch.zeros(2, 1, 8, device=DEV), torch.zeros(1, 2, 1, 8, device=DEV)
+    with pytest.raises(ValueError, match="stream is on cuda"):
+        ssd.kv_commit_tokens(k, k, kc, kc.clone(), _i([0, 1]), stream=Elsewhere())
+    torch.cuda.synchronize()
+    assert (kc == 0).all()
+
+
 # ----------------------------------------------------------------- together --
 
 def test_hybrid_tree_decode_example():

@@ -145,3 +145,13 @@ def test_no_load_goes_to_several_ctas():
     for name in sorted(os.listdir(src)):
         with open(os.path.join(src, name)) as f:
             assert "multicast" not in f.read(), name
+
+
+def test_tensors_of_two_devices_are_refused():
+    """The check of every tensor's device, on indices; a call after a refused one starts anew."""
+    calls = B._kv()
+    assert calls.device_of_call(0, 0) == 0
+    for a, b in ((0, 1), (3, 0)):
+        with pytest.raises(ValueError, match="second is on cuda:%d, other arguments are on cuda:%d" % (b, a)):
+            calls.device_of_call(a, b)
+    assert calls.device_of_call(1, 1) == 1
