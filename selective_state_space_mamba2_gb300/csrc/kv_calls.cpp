@@ -149,7 +149,14 @@ Pages pages(PyObject *ko, PyObject *vo, int64_t H, int64_t D, ScalarType type) {
             nb > 1 ? k.stride(0) : bs * H * D};
 }
 
-uint32_t *error_word(PyObject *o) { return o == Py_None ? nullptr : static_cast<uint32_t *>(tensor(o, "err_word").data_ptr()); }
+// The kernels or 32 bits into it.
+uint32_t *error_word(PyObject *o) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor &t = tensor(o, "err_word");
+    if ((t.scalar_type() != at::kInt && t.scalar_type() != at::kUInt32) || t.numel() < 1)
+        refuse("err_word must be int32 of one element");
+    return static_cast<uint32_t *>(t.data_ptr());
+}
 
 // The caller's stream (a torch stream or its pointer as a number), or the current one of the device.
 ssd_stream_t stream_of(PyObject *o, const at::Tensor &like) {

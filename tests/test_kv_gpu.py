@@ -748,6 +748,14 @@ def test_commit_all_tokens_and_errors():
 
 # ------------------------------------------------------------------ binding --
 
+@pytest.mark.parametrize("word", [torch.zeros(0, dtype=torch.int32), torch.zeros(1, dtype=torch.int16),
+                                  torch.zeros(1, dtype=torch.uint8), torch.zeros(1)])
+def test_an_error_word_is_32_bits(word):
+    k, kc = torch.zeros(2, 1, 8, device=DEV), torch.zeros(1, 2, 1, 8, device=DEV)
+    with pytest.raises(ValueError, match="err_word"):
+        ssd.kv_commit_tokens(k, k, kc, kc.clone(), _i([0, 1]), err_word=word.to(DEV))
+
+
 def test_a_stream_of_another_device_is_refused():
     class Elsewhere:
         cuda_stream, device_index = 0, torch.cuda.current_device() + 1
