@@ -389,6 +389,7 @@ PyObject *tree_attention(PyObject *const *a, PyObject *) {
         room = empty((int64_t)kv_tree_attention_workspace_size(&p), at::kByte, q);
     } else {
         room = tensor(a[14], "workspace");
+        if (!room.is_contiguous()) refuse("workspace must be contiguous");
     }
     const ssd_stream_t stream = stream_of(a[16], q);
     const ssd_status_t s = kv_tree_attention(&p, room.data_ptr(), (size_t)room.nbytes(), stream);

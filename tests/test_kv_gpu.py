@@ -756,6 +756,19 @@ def test_an_error_word_is_32_bits(word):
         ssd.kv_commit_tokens(k, k, kc, kc.clone(), _i([0, 1]), err_word=word.to(DEV))
 
 
+def test_a_workspace_with_gaps_is_refused():
+    """Its bytes do not lie side by side: the kernels would write between them, and beyond the last."""
+    c = _attn(BF, 4, 1, 64, 16, [2], [20], False, seed=46)
+    room = torch.empty(1 << 24, dtype=torch.uint8, device=DEV)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        _run(c, None, workspace=room[::2])
+    with pytest.raises(ssd.SSDError):
+        _run(c, None, workspace=room[:1])
+    out, _ = _run(c, None, workspace=room)
+    torch.cuda.synchronize()
+    assert torch.isfinite(out).all()
+
+
 def test_a_stream_of_another_device_is_refused():
     class Elsewhere:
         cuda_stream, device_index = 0, torch.cuda.current_device() + 1
