@@ -27,6 +27,15 @@ using at::ScalarType;
 
 struct PythonError {};  // an exception is set already
 
+// An owned reference.
+struct Held {
+    PyObject *o = nullptr;
+    Held() = default;
+    Held(const Held &) = delete;
+    Held &operator=(const Held &) = delete;
+    ~Held() { Py_XDECREF(o); }
+};
+
 [[noreturn]] void refuse(const std::string &what) { throw std::invalid_argument(what); }
 
 const char *type_name(ScalarType t) {
@@ -229,6 +238,7 @@ PyObject *block_tables(PyObject *const *a, PyObject *) {
     const int64_t sizes[7] = {S + 1, S, S, 2, p.max_tokens, p.max_tokens, p.max_tokens};
     int32_t *ptr[7] = {};
     PyObject *out = a[10];
+    Held given[7];  // a mapping may make its values on access: they live until the call is queued
     at::Tensor room;
     if (out == Py_None) {
         // one allocation, each output at a 64-byte boundary of it
@@ -249,13 +259,12 @@ PyObject *block_tables(PyObject *const *a, PyObject *) {
         }
     } else {
         for (int i = 0; i < 7; ++i) {
-            PyObject *t = PyObject_GetItem(out, names[i]);
+            PyObject *t = given[i].o = PyObject_GetItem(out, names[i]);
             if (!t) {
-                if (i < 6) throw PythonError{};
+                if (i < 6 || !PyErr_ExceptionMatches(PyExc_KeyError)) throw PythonError{};
                 PyErr_Clear();  // token_req may be left out
                 continue;
             }
-            Py_DECREF(t);  // the mapping keeps it
             if (i < 6 || t != Py_None) ptr[i] = const_cast<int32_t *>(ints(t, keys[i], sizes[i]));
         }
         Py_INCREF(out);

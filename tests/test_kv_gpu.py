@@ -769,6 +769,46 @@ def test_a_workspace_with_gaps_is_refused():
     assert torch.isfinite(out).all()
 
 
+class _Fresh(dict):
+    """A mapping whose values live no longer than who asks for them keeps them: views of one buffer, counted."""
+    alive = 0
+
+    class View(torch.Tensor):
+        def __del__(self):
+            _Fresh.alive -= 1
+
+    def __getitem__(self, key):
+        if key == "ring_state":
+            _Fresh.seen = _Fresh.alive  # of the values asked for before
+        v = super().__getitem__(key).view(-1).as_subclass(self.View)
+        _Fresh.alive += 1
+        return v
+
+
+def test_outputs_made_on_access_are_kept_for_the_call():
+    """Values of ``out`` are held until the call is queued, and an error in looking one up is the caller's to see."""
+    args = (_i([3, 0]), _i([2, 1]), _i([3, 0]), _i([[1, 0], [0, 0]]), _i([2, 3, 4]), _i([0, 3]), 4, 9, 5)
+    want = ssd.kv_block_tables(*args)
+    args = args[:3] + (_i([[1, 0], [0, 0]]),) + args[4:]
+    room = _Fresh({k: torch.zeros_like(v) for k, v in want.items()})
+    assert ssd.kv_block_tables(*args, out=room) is room and _Fresh.seen == 3 and _Fresh.alive == 0
+    torch.cuda.synchronize()
+    for k, v in want.items():
+        assert torch.equal(dict.__getitem__(room, k), v), k
+    del room["token_req"]
+    ssd.kv_block_tables(*args, out=room)
+    torch.cuda.synchronize()
+
+    class Broken(dict):
+        def __getitem__(self, key):
+            if key == "token_req":
+                raise RuntimeError("no access")
+            return super().__getitem__(key)
+
+    with pytest.raises(RuntimeError, match="no access"):
+        ssd.kv_block_tables(*args, out=Broken(room))
+
+
 def test_a_stream_of_another_device_is_refused():
     class Elsewhere:
         cuda_stream, device_index = 0, torch.cuda.current_device() + 1
