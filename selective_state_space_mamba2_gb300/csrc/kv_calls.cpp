@@ -89,6 +89,12 @@ float real(PyObject *o) {
     return (float)v;
 }
 
+bool truth(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw PythonError{};
+    return v == 1;
+}
+
 int32_t dtype_code(const at::Tensor &t, const char *name) {
     const ScalarType s = t.scalar_type();
     if (s == at::kBFloat16) return SSD_BF16;
@@ -309,7 +315,7 @@ PyObject *norm_rope(PyObject *const *a, PyObject *) {
     if (a[4] != Py_None) p.q_weight = static_cast<const float *>(dense(a[4], "q_weight", wide, at::kFloat));
     if (a[5] != Py_None) p.k_weight = static_cast<const float *>(dense(a[5], "k_weight", wide, at::kFloat));
     p.eps = real(a[6]);
-    p.interleaved = PyObject_IsTrue(a[7]) == 1;
+    p.interleaved = truth(a[7]);
     if (a[9] != Py_None || a[10] != Py_None || a[11] != Py_None) {
         const Pages c = pages(a[9], a[10], G, D, type);
         p.k_cache = c.k, p.v_cache = c.v, p.num_blocks = c.blocks, p.block_size = c.block_size;
@@ -385,7 +391,7 @@ PyObject *tree_attention(PyObject *const *a, PyObject *) {
     } else {
         p.out = dense(a[11], "out", shape, type);
     }
-    const bool with_lse = a[12] != Py_None || PyObject_IsTrue(a[13]) == 1;
+    const bool with_lse = a[12] != Py_None || truth(a[13]);
     if (a[12] != Py_None) {
         p.lse = static_cast<float *>(dense(a[12], "lse", lse_shape, at::kFloat));
     } else if (with_lse) {

@@ -809,6 +809,17 @@ def test_outputs_made_on_access_are_kept_for_the_call():
         ssd.kv_block_tables(*args, out=Broken(room))
 
 
+def test_a_flag_without_a_truth_value_is_refused():
+    """The exception is the flag's own, and nothing is queued."""
+    q = torch.zeros(1, 1, 8, device=DEV)
+    with pytest.raises(ValueError, match="truth value"):
+        ssd.kv_qk_norm_rope(q, q, interleaved=np.zeros(2))
+    c = _attn(BF, 4, 1, 64, 16, [2], [20], False, seed=46)
+    with pytest.raises(ValueError, match="truth value"):
+        ssd.kv_tree_attention(c["q"], c["k"], c["v"], c["kc"], c["vc"], _i(c["cu"]), _i(c["ctx"]), _i(c["table"]), 2,
+                              return_lse=np.zeros(2))
+
+
 def test_a_stream_of_another_device_is_refused():
     class Elsewhere:
         cuda_stream, device_index = 0, torch.cuda.current_device() + 1
