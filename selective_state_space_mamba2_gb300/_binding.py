@@ -630,6 +630,11 @@ def kv_qk_norm_rope(q, k, positions=None, cos_sin=None, q_weight=None, k_weight=
         err_word, stream))
 
 
+def _stride(t):
+    """Elements from one row (block) of ``t`` to the next; of a single one, whose stride says nothing, its own."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1:].numel()
+
+
 def attention_args(q, k_new, v_new, k_cache, v_cache, cu_seqlens, context_lens, block_table, out, max_new_tokens,
                    tree_mask=None, scale=None, lse=None, err_word=None, wait_limit_cycles=0):
     """Fills an ``AttentionArgs`` from the tensors' sizes and pointers (for
@@ -641,8 +646,8 @@ def attention_args(q, k_new, v_new, k_cache, v_cache, cu_seqlens, context_lens, 
     a.table_cols, a.max_new_tokens = block_table.shape[1], int(max_new_tokens)
     a.mask_words = 0 if tree_mask is None else tree_mask.shape[1]
     a.scale = float(D ** -0.5 if scale is None else scale)
-    a.q_stride, a.k_stride, a.v_stride = q.stride(0), k_new.stride(0), v_new.stride(0)
-    a.cache_block_stride, a.wait_limit_cycles = k_cache.stride(0), int(wait_limit_cycles)
+    a.q_stride, a.k_stride, a.v_stride = _stride(q), _stride(k_new), _stride(v_new)
+    a.cache_block_stride, a.wait_limit_cycles = _stride(k_cache), int(wait_limit_cycles)
     for f, t in (("q", q), ("k_new", k_new), ("v_new", v_new), ("k_cache", k_cache), ("v_cache", v_cache),
                  ("cu_seqlens", cu_seqlens), ("context_lens", context_lens), ("block_table", block_table),
                  ("tree_mask", tree_mask), ("out", out), ("lse", lse), ("err_word", err_word)):

@@ -155,3 +155,22 @@ def test_tensors_of_two_devices_are_refused():
         with pytest.raises(ValueError, match="second is on cuda:%d, other arguments are on cuda:%d" % (b, a)):
             calls.device_of_call(a, b)
     assert calls.device_of_call(1, 1) == 1
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,blocks", [(1, 5), (3, 1), (1, 1), (3, 5)])
+def test_workspace_size_of_single_rows_and_blocks(lib, dtype, T, blocks):
+    """The stride of a dimension of one entry says nothing: the size is that of the same call with dense tensors."""
+    H, G, D, b = 4, 2, 64, 16
+
+    def made(n, *row, odd):
+        return torch.empty(row[0], 1, *row[1:], dtype=dtype).transpose(0, 1) if odd and n == 1 else torch.empty(n, *row, dtype=dtype)
+
+    def size(odd):
+        q, k, v, kc, vc = (made(n, *row, odd=odd) for n, row in
+                           ((T, (H, D)), (T, (G, D)), (T, (G, D)), (blocks, (b, G, D)), (blocks, (b, G, D))))
+        a = ssd.attention_args(q, k, v, kc, vc, torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32),
+                               torch.zeros(1, 3, dtype=torch.int32), torch.empty(T, H, D, dtype=dtype), T)
+        return ssd.kv_tree_attention_workspace_size(a)
+
+    assert size(True) == size(False) > 0
