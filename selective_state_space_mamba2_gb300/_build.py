@@ -67,9 +67,26 @@ def _torch_dir() -> str:
     return os.path.dirname(torch.__file__)
 
 
+def _calls_key() -> str:
+    """What the marshalling module is compiled against besides this repository's sources."""
+    import torch
+    return "\n".join([torch.__version__, _torch_dir(), "cxx11abi %d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+                      sysconfig.get_config_var("EXT_SUFFIX") or "", sysconfig.get_paths()["include"]])
+
+
+def _read(path: str) -> str:
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def _compile_calls() -> str:
     obj, srcp = os.path.join(BUILD, CALLS + ".o"), os.path.join(CSRC, CALLS)
-    if os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(srcp), _headers_mtime()):
+    key, keyp = _calls_key(), os.path.join(BUILD, CALLS + ".key")
+    if (os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(srcp), _headers_mtime())
+            and _read(keyp) == key):
         return obj
     import torch
     inc = os.path.join(_torch_dir(), "include")
@@ -83,6 +100,9 @@ def _compile_calls() -> str:
     if res.returncode != 0:
         raise RuntimeError("g++ failed for %s:\n%s\n%s" % (CALLS, res.stdout, res.stderr))
     os.replace(tmp, obj)
+    with open(tmp, "w") as f:
+        f.write(key)
+    os.replace(tmp, keyp)
     return obj
 
 

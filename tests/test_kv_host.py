@@ -174,3 +174,20 @@ def test_workspace_size_of_single_rows_and_blocks(lib, dtype, T, blocks):
         return ssd.kv_tree_attention_workspace_size(a)
 
     assert size(True) == size(False) > 0
+
+
+def test_marshalling_module_is_rebuilt_for_another_torch(lib, monkeypatch):
+    """Its object is kept for the torch and the interpreter it was compiled against, and for no other."""
+    from selective_state_space_mamba2_gb300 import _build
+
+    class Started(Exception):
+        pass
+
+    def run(*args, **kwargs):
+        raise Started
+
+    monkeypatch.setattr(_build.subprocess, "run", run)
+    _build._compile_calls()  # nothing to do
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + "x")
+    with pytest.raises(Started):
+        _build._compile_calls()
