@@ -202,8 +202,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NV))
             if (sub == 0) shrinks[row] = shrink;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+                // -1 marks what is not seen: a weight may be 0 by underflow, and its value counts all the same
                 const float p = sees[j] ? exp2f(s[j] - from) : 0.f;
-                sp[(sub + 8 * j) * kKeyPitch + row] = p;
+                sp[(sub + 8 * j) * kKeyPitch + row] = sees[j] ? p : -1.f;
                 sum += p;
             }
             __syncthreads();
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NV))
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 p2 = make_float2(pk[i], pk[i]);
-                        if (all || pk[i] != 0.f) {  // not seen (weight 0): its value stays out, whatever it is
+                        if (all || !(pk[i] < 0.f)) {  // not seen: its value stays out, whatever it is
                             acc[i][v][0] = tc::fma_f2(p2, make_float2(y.x, y.y), acc[i][v][0]);
                             acc[i][v][1] = tc::fma_f2(p2, make_float2(y.z, y.w), acc[i][v][1]);
                         }

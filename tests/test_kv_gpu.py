@@ -453,6 +453,32 @@ def test_attention_infinite_values(dtype):
         assert torch.isfinite(row[:, keep]).all()
 
 
+@pytest.mark.parametrize("dtype,D", [(BF, 64), (BF, 96), (F32, 64)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_attention_values_of_vanishing_weights_count(dtype, D, bad):
+    """A key that is seen, but so far below the others that its weight is zero in fp32: its value is no number, and neither
+    is the result of those that see it; the others' columns and rows are."""
+    c = _attn(dtype, 4, 1, D, 16, [6, 2], [20, 5], True, seed=47)
+    c["mask"][:] = [[0b1], [0b11], [0b101], [0b1001], [0b10011], [0b100101], [0b1], [0b11]]
+    c["q"][..., 0] = 1000.0
+    far = c["k"][:, 0, 0]
+    far.fill_(0.0)
+    for r in range(2):
+        for page in c["table"][r, :-(-c["ctx"][r] // 16)]:
+            c["kc"][int(page), :, 0, 0] = torch.where(torch.isnan(c["kc"][int(page), :, 0, 0]), float("nan"), 0.0)
+    far[1] = -1000.0  # seen by tokens 1 and 4
+    c["v"][1, 0, 3] = bad
+    last = c["kc"][int(c["table"][1, 0]), 4, 0]  # the second request's last cached token
+    last[0] = -1000.0
+    c["vc"][int(c["table"][1, 0]), 4, 0, 7] = bad
+    out, lse = _run(c, _err())
+    torch.cuda.synchronize()
+    sees = torch.zeros_like(out, dtype=torch.bool)
+    sees[[1, 4], :, 3] = True
+    sees[6:, :, 7] = True
+    assert torch.equal(~torch.isfinite(out), sees) and torch.isfinite(lse).all()
+
+
 @pytest.mark.parametrize("dtype,gain", [(BF, 60.0), (F32, 60.0), (BF, 0.0), (F32, 1e-3)])
 def test_attention_score_ranges(dtype, gain):
     """Peaked scores (hundreds apart, so running maxima jump), and equal ones."""
