@@ -192,8 +192,18 @@ ssd_stream_t stream_of(PyObject *o, const at::Tensor &like) {
     return reinterpret_cast<ssd_stream_t>(v);
 }
 
-at::Tensor empty(at::IntArrayRef shape, ScalarType type, const at::Tensor &like) {
-    return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
+// Memory of the call's stream, on which it is written: memory of the current one, where that is another, could still have
+// work of that stream to come, of whoever had it before.  What the current stream may do with it later is waited
+// for before it is handed out again.
+at::Tensor empty(at::IntArrayRef shape, ScalarType type, const at::Tensor &like, ssd_stream_t s) {
+    const auto dev = like.get_device();
+    const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(dev);
+    if (reinterpret_cast<cudaStream_t>(s) == now.stream())
+        return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
+    const c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(s), dev));
+    at::Tensor t = at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
+    c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), now);
+    return t;
 }
 
 // A dense int32 tensor of n entries in `room`'s memory, from entry `at` on.
@@ -202,15 +212,6 @@ at::Tensor piece_of(const at::Tensor &room, int64_t n, int64_t at) {
     t.unsafeGetTensorImpl()->set_storage_offset(at);
     t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
     return t;
-}
-
-// Memory made here on the current stream and used on another: not handed out again before that other
-// stream is done with it.
-void used_on(const at::Tensor &t, ssd_stream_t s) {
-    const auto dev = t.get_device();
-    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
-    if (cs != c10::cuda::getCurrentCUDAStream(dev).stream())
-        c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), c10::cuda::getStreamFromExternal(cs, dev));
 }
 
 PyObject *status(ssd_status_t s) { return PyLong_FromLong((long)s); }
@@ -243,6 +244,8 @@ PyObject *block_tables(PyObject *const *a, PyObject *) {
         if (!(names[i] = PyUnicode_InternFromString(keys[i]))) throw PythonError{};
     const int64_t sizes[7] = {S + 1, S, S, 2, p.max_tokens, p.max_tokens, p.max_tokens};
     int32_t *ptr[7] = {};
+    p.err_word = error_word(a[11]);
+    const ssd_stream_t stream = stream_of(a[12], ctx);
     PyObject *out = a[10];
     Held given[7];  // a mapping may make its values on access: they live until the call is queued
     at::Tensor room;
@@ -250,7 +253,7 @@ PyObject *block_tables(PyObject *const *a, PyObject *) {
         // one allocation, each output at a 64-byte boundary of it
         int64_t at[7], all = 0;
         for (int i = 0; i < 7; ++i) at[i] = all, all += (sizes[i] + 15) / 16 * 16;
-        room = empty(all, at::kInt, ctx);
+        room = empty(all, at::kInt, ctx, stream);
         out = PyDict_New();
         if (!out) throw PythonError{};
         for (int i = 0; i < 7; ++i) {
@@ -277,16 +280,7 @@ PyObject *block_tables(PyObject *const *a, PyObject *) {
     }
     p.cu_seqlens = ptr[0], p.seq_lens = ptr[1], p.reserved_out = ptr[2], p.ring_out = ptr[3];
     p.slots = ptr[4], p.positions = ptr[5], p.token_req = ptr[6];
-    ssd_status_t s;
-    try {
-        p.err_word = error_word(a[11]);
-        const ssd_stream_t stream = stream_of(a[12], ctx);
-        s = kv_block_tables(&p, stream);
-        if (room.defined()) used_on(room, stream);
-    } catch (...) {
-        Py_DECREF(out);
-        throw;
-    }
+    const ssd_status_t s = kv_block_tables(&p, stream);
     if (s == SSD_OK) return out;
     Py_DECREF(out);
     return status(s);
@@ -324,25 +318,23 @@ PyObject *norm_rope(PyObject *const *a, PyObject *) {
         p.v = rv.p, p.v_stride = rv.stride;
         p.slots = ints(a[11], "slots", T);
     }
+    p.err_word = error_word(a[14]);
+    const ssd_stream_t stream = stream_of(a[15], q);
     const int64_t qs[3] = {T, H, D}, ks[3] = {T, G, D};
     at::Tensor q_new, k_new;
     if (a[12] == Py_None) {
-        q_new = empty(qs, type, q);
+        q_new = empty(qs, type, q, stream);
         p.q_out = q_new.data_ptr();
     } else {
         p.q_out = dense(a[12], "q_out", qs, type);
     }
     if (a[13] == Py_None) {
-        k_new = empty(ks, type, q);
+        k_new = empty(ks, type, q, stream);
         p.k_out = k_new.data_ptr();
     } else {
         p.k_out = dense(a[13], "k_out", ks, type);
     }
-    p.err_word = error_word(a[14]);
-    const ssd_stream_t stream = stream_of(a[15], q);
     const ssd_status_t s = kv_qk_norm_rope(&p, stream);
-    for (const at::Tensor *t : {&q_new, &k_new})
-        if (t->defined()) used_on(*t, stream);
     if (s != SSD_OK) return status(s);
     PyObject *qo = a[12] == Py_None ? THPVariable_Wrap(std::move(q_new)) : Py_NewRef(a[12]);
     PyObject *ko = a[13] == Py_None ? THPVariable_Wrap(std::move(k_new)) : Py_NewRef(a[13]);
@@ -383,10 +375,12 @@ PyObject *tree_attention(PyObject *const *a, PyObject *) {
         p.mask_words = size32(words, "tree_mask words");
     }
     p.scale = a[10] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : real(a[10]);
+    p.err_word = error_word(a[15]);
+    const ssd_stream_t stream = stream_of(a[16], q);
     const int64_t shape[3] = {T, H, D}, lse_shape[2] = {T, H};
     at::Tensor out, lse, room;
     if (a[11] == Py_None) {
-        out = empty(shape, type, q);
+        out = empty(shape, type, q, stream);
         p.out = out.data_ptr();
     } else {
         p.out = dense(a[11], "out", shape, type);
@@ -395,22 +389,17 @@ PyObject *tree_attention(PyObject *const *a, PyObject *) {
     if (a[12] != Py_None) {
         p.lse = static_cast<float *>(dense(a[12], "lse", lse_shape, at::kFloat));
     } else if (with_lse) {
-        lse = empty(lse_shape, at::kFloat, q);
+        lse = empty(lse_shape, at::kFloat, q, stream);
         p.lse = static_cast<float *>(lse.data_ptr());
     }
-    p.err_word = error_word(a[15]);
     p.wait_limit_cycles = integer(a[17]);
     if (a[14] == Py_None) {
-        room = empty((int64_t)kv_tree_attention_workspace_size(&p), at::kByte, q);
+        room = empty((int64_t)kv_tree_attention_workspace_size(&p), at::kByte, q, stream);
     } else {
         room = tensor(a[14], "workspace");
         if (!room.is_contiguous()) refuse("workspace must be contiguous");
     }
-    const ssd_stream_t stream = stream_of(a[16], q);
     const ssd_status_t s = kv_tree_attention(&p, room.data_ptr(), (size_t)room.nbytes(), stream);
-    if (a[14] == Py_None) used_on(room, stream);
-    for (const at::Tensor *t : {&out, &lse})
-        if (t->defined()) used_on(*t, stream);
     if (s != SSD_OK) return status(s);
     PyObject *oo = a[11] == Py_None ? THPVariable_Wrap(std::move(out)) : Py_NewRef(a[11]);
     if (!with_lse || !oo) return oo;
@@ -454,21 +443,20 @@ PyObject *commit_tokens(PyObject *const *a, PyObject *) {
         p.max_path = size32(width, "path columns");
         p.path_lens = ints(a[8], "path_lens", S);
     }
+    p.err_word = error_word(a[10]);
+    const ssd_stream_t stream = stream_of(a[11], k);
     at::Tensor made;
     PyObject *out = a[9];
     if (a[6] != Py_None) {
         p.context_lens = ints(a[6], "context_lens", S);
         if (out == Py_None) {
-            made = empty(S, at::kInt, k);
+            made = empty(S, at::kInt, k, stream);
             p.context_out = static_cast<int32_t *>(made.data_ptr());
         } else {
             p.context_out = const_cast<int32_t *>(ints(out, "context_out", S));
         }
     }
-    p.err_word = error_word(a[10]);
-    const ssd_stream_t stream = stream_of(a[11], k);
     const ssd_status_t s = kv_commit_tokens(&p, stream);
-    if (made.defined()) used_on(made, stream);
     if (s != SSD_OK) return status(s);
     if (made.defined()) return THPVariable_Wrap(std::move(made));
     return Py_NewRef(out);

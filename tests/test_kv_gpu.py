@@ -846,6 +846,42 @@ def test_a_flag_without_a_truth_value_is_refused():
                               return_lse=np.zeros(2))
 
 
+def _four_calls(stream):
+    """The four calls on the same inputs; everything that they allocate."""
+    g = torch.Generator(device=DEV).manual_seed(50)
+    k = torch.randn(3, 2, 64, generator=g, device=DEV)
+    kc = torch.randn(4, 16, 2, 64, generator=g, device=DEV)
+    q = torch.randn(3, 4, 64, generator=g, device=DEV)
+    cu, ctx, table, one = _i([0, 1, 3]), _i([20, 9]), _i([[1, 2], [3, 0]]), _i([1, 2])
+    args = (ctx, one, ctx, table.clone(), _i([2, 3, 4]), _i([0, 3]), 16, 9, 5)
+    slots, kn, vn = _i([5, 7, 9]), kc.clone(), kc.clone()
+    torch.cuda.synchronize()
+
+    def run():
+        tables = ssd.kv_block_tables(*args, stream=stream)
+        return [tables[key] for key in sorted(tables)] + list(ssd.kv_qk_norm_rope(q, k, stream=stream)) + \
+            list(ssd.kv_tree_attention(q, k, k, kc, kc, cu, ctx, table, 2, return_lse=True, stream=stream)) + \
+            [ssd.kv_commit_tokens(k, k, kn, vn, slots, cu, ctx, stream=stream)]
+    return run
+
+
+@pytest.mark.parametrize("as_number", [False, True])
+def test_outputs_for_another_stream_have_no_work_to_come(as_number):
+    """Memory that the current stream has yet to write for its last owner is not what a call on another stream gets."""
+    want = _four_calls(None)()
+    s = torch.cuda.Stream()
+    run = _four_calls(s.cuda_stream if as_number else s)
+    torch.cuda.empty_cache()
+    torch.cuda._sleep(40_000_000)
+    for _ in range(4):  # freed at once, filled when the current stream gets there
+        last = [torch.full((n,), 7, dtype=torch.int32, device=DEV) for n in (4, 100, 128, 300, 500, 1000, 1 << 16, 1 << 20)]
+        del last
+    got = run()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 def test_a_stream_of_another_device_is_refused():
     class Elsewhere:
         cuda_stream, device_index = 0, torch.cuda.current_device() + 1
