@@ -655,7 +655,9 @@ SSD_API ssd_status_t kv_qk_norm_rope(const kv_qk_args *args, ssd_stream_t stream
  * rows, in rejected drafts).  Softmax statistics and sums are fp32.
  * bf16 with headdim 64 or 128, at most 128 query heads to a key head, block_size
  * a multiple of 8 and a positive scale runs on the tensor cores, its probabilities
- * rounded to bf16; everything else, fp32 above all, on the CUDA cores in fp32.
+ * held as two bf16 parts (to 2^-15) where min(max_new_tokens, 128 / group) * group <= 32,
+ * group = nheads / kv_heads (decode steps, short drafts), and rounded to bf16 (2^-8)
+ * otherwise; everything else, fp32 above all, on the CUDA cores in fp32.
  *
  * Work is cut into equal shares over the GPU along requests, heads, query
  * tiles and keys, from lengths the kernel reads on the device; a share that

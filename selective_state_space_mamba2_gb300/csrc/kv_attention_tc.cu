@@ -8,8 +8,16 @@
 // with the running maximum m and the sum of the weights in registers (fp32).  O stays in TMEM; it
 // is only rescaled when a row's maximum grows by more than 2^8 (the weights are then at most
 // 2^8, exact powers of two apart from what they would be, and the sum is kept to the same m).
-// P's rounding to bf16 is that of the product's operand type: V is bf16, and both operands of a
-// product have one type; the sum of the weights takes them before the rounding.
+// V is bf16, and both operands of a product have one type, so P is, too.  In tiles of at most 32 rows (decode
+// steps, short drafts), whose bytes or latency are the bound, it is held in two parts, high and low, side by side
+// in the columns that the scores leave, and multiplied by V twice: 2^-15 is lost of a weight instead of 2^-8.  The
+// high part is cut off and the low one lifted by 2^-24 of the weight, so that both are above 0 where the weight
+// is, and an infinite value gives infinity, not the difference of two.  256 requests of 4 tokens over up to 8192
+// 649 us with two parts / 668 with one, one token over 65536 50.1 / 49.4, one over 777 10.8 / 10.3, 16 of 4
+// over up to 1000 18.3 / 16.9, 4 single tokens of 64 heads over 4000 17.8 / 16.0.  Tiles of more rows have P rounded
+// to bf16, an error of the order of the output's own rounding (0.0018 to 0.0020 of the outputs' norm, 0.0015 without);
+// two parts there make 4 prompts 1010 us from 770, a tree of 32 tokens over 4000 24.3 from 20.7.  The sum of the
+// weights takes them before any rounding.
 //
 // Roles (192 threads, two CTAs per SM so that one's softmax runs beside the other's products):
 // warps 0-3 softmax and output, warp 4 TMA loads, warp 5 the products.  Keys and values pass
@@ -20,7 +28,7 @@
 // one that comes second finds them in L2.  Neither waits for the other.
 //
 // What bounds it.  Few rows a request (decode steps, short drafts): the bytes of the cache, 256 requests
-// of 4 tokens over up to 8192 cached 663 to 690 us, 6.6 to 6.8 TB/s.  Prompts and large trees: shared memory.  Of a
+// of 4 tokens over up to 8192 cached 649 to 651 us, 7.0 TB/s.  Prompts and large trees: shared memory.  Of a
 // tile's 512 cycles of products S takes 384 instead of 256 (a product 128 x 64 x 16 reads 6 KB), V is
 // read in 128, and the copies write 32 KB in 256: 768, and 720 to 790 measured; 4 prompts of 512 to 4096
 // tokens over up to 8192 747 to 777 us, 1360 to 1410 TFLOP/s.  Tried against that, and not faster: tiles of 128
@@ -54,6 +62,7 @@ constexpr int kStages = 5;
 constexpr int kOverhead = 3;  // of an item, in key tiles
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLift = 1.f / (1 << 24);  // see the top
 constexpr float kSlack = 8.f;  // growth of a maximum (base 2) that is let stand
 
 struct TcParams {
@@ -181,7 +190,8 @@ __device__ __noinline__ void add_nonfinite(const kv_attention_args &a, const kvs
     }
 }
 
-template <int D, int kPair>
+// kFew: tiles of at most kvs::kFewRows rows, with weights in two parts
+template <int D, int kPair, bool kFew>
 __global__ void __launch_bounds__(kThreads, 2)
     kv_attention_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKc,
                            const __grid_constant__ CUtensorMap tmVc, const __grid_constant__ CUtensorMap tmKn,
@@ -369,6 +379,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
                     mma_ts(tmu + COL_O, p0 + 8 * k, desc_at(v0, 2048 * k), kIdO, k > 0 ? 1u : add);
+                if (kFew) {  // the low parts
+#pragma unroll
+                    for (int k = 0; k < kKeys / 16; ++k)
+                        mma_ts(tmu + COL_O, p0 + 32 + 8 * k, desc_at(v0, 2048 * k), kIdO, 1u);
+                }
                 mma_commit(&bar[O_DONE0 + (gg & 1)]);
                 mma_commit(&bar[KV_EMPTY0 + sg]);
             }
@@ -459,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const float from = top == -INFINITY ? 0.f : top;
                     const float2 c2 = make_float2(c, c), m2 = make_float2(-from, -from);
                     float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    uint32_t pk[32];
+                    uint32_t pk[32], lo[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         float2 v = make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
@@ -467,10 +482,20 @@ __global__ void __launch_bounds__(kThreads, 2)
                         v.x = ex2(v.x);
                         v.y = ex2(v.y);
                         add[j & 1] = add_f2(add[j & 1], v);
-                        pk[j] = pack_bf16(v.x, v.y);
+                        if (kFew) {
+                            const uint32_t x = __float_as_uint(v.x), y = __float_as_uint(v.y);
+                            pk[j] = __byte_perm(x, y, 0x7632);
+                            const float2 high = make_float2(__uint_as_float(x & 0xFFFF0000u), __uint_as_float(y & 0xFFFF0000u));
+                            const float2 rest = fma_f2(high, make_float2(-1.f, -1.f), v);
+                            v = fma_f2(v, make_float2(kLift, kLift), rest);
+                            lo[j] = pack_bf16(v.x, v.y);
+                        } else {
+                            pk[j] = pack_bf16(v.x, v.y);
+                        }
                     }
                     sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
                     tmem_st32(s_col, pk);
+                    if (kFew) tmem_st32(s_col + 32, lo);
                     tmem_st_wait();
                 }
                 if (partial) {
@@ -576,7 +601,7 @@ int tc_workers(const kv_attention_args &a, const kvs::Tiling &g) {
     return kvs::grid_of(a, g, 2 * device_sms() / pair_for(a));
 }
 
-template <int D, int kPair> cudaError_t launch(const kv_attention_args &a, void *ws, cudaStream_t s) {
+template <int D, int kPair, bool kFew> cudaError_t launch(const kv_attention_args &a, void *ws, cudaStream_t s) {
     TcParams p;
     p.a = a;
     p.g = tc_tiling(a);
@@ -611,12 +636,17 @@ template <int D, int kPair> cudaError_t launch(const kv_attention_args &a, void 
                     make_tmap_16bit<4>(&vn, kType, a.v_new, new_dims, vn_strides, new_box);
     if (!ok) return cudaErrorInvalidValue;
     constexpr int smem = Layout<D>::kBytes;
-    const auto kernel = kv_attention_tc_kernel<D, kPair>;
+    const auto kernel = kv_attention_tc_kernel<D, kPair, kFew>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     kernel<<<workers * kPair, kThreads, smem, s>>>(q, kc, vc, kn, vn, p);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : kvs::join_launch(a, p.parts, workers, p.g, s);
+}
+
+template <int D> cudaError_t launch_dim(const kv_attention_args &a, void *ws, cudaStream_t s) {
+    if (pair_for(a) > 1) return launch<D, 2, false>(a, ws, s);
+    return tc_tiling(a).rows <= kvs::kFewRows ? launch<D, 1, true>(a, ws, s) : launch<D, 1, false>(a, ws, s);
 }
 
 }  // namespace
@@ -636,8 +666,7 @@ size_t kv_attention_tc_workspace(const kv_attention_args &a) {
 }
 
 cudaError_t kv_attention_tc_launch(const kv_attention_args &a, void *ws, cudaStream_t s) {
-    if (pair_for(a) == 1) return a.headdim == 64 ? launch<64, 1>(a, ws, s) : launch<128, 1>(a, ws, s);
-    return a.headdim == 64 ? launch<64, 2>(a, ws, s) : launch<128, 2>(a, ws, s);
+    return a.headdim == 64 ? launch_dim<64>(a, ws, s) : launch_dim<128>(a, ws, s);
 }
 
 }  // namespace ssd

@@ -453,6 +453,62 @@ def test_attention_infinite_values(dtype):
         assert torch.isfinite(row[:, keep]).all()
 
 
+@pytest.mark.parametrize("H,D,new,ctx,tree", [
+    (4, 128, [1], [777], False), (1, 64, [1, 2, 4], [63, 0, 129], True), (8, 128, [4, 4], [20000, 70], False),
+    (32, 64, [1] * 40, list(range(40, 1640, 40)), False), (4, 64, [8, 3, 0, 5], [0, 300, 7, 64], True),
+])
+def test_attention_few_rows_keep_their_weights(H, D, new, ctx, tree):
+    """Tiles of at most 32 rows hold the weights to 2^-15 (8 bits cut off, what is left rounded to 8).  Half of the keys have a weight that bf16 rounds down and
+    values of 1, half one that it rounds up and values of -1: the outputs nearly cancel, and 8 bits would leave 2^-8 of
+    the weights' sum, beside a rounding of the outputs of 2^-8 of their own, much smaller, size."""
+    c = _attn(BF, H, 1, D, 16, new, ctx, tree, seed=48, scale=1.0)
+    c["q"].zero_()
+    c["q"][..., 0], c["q"][..., 1] = 1.0, 2.0 ** -8
+    scores = [np.log(0.5 * (1 + f / 128)) for f in (0.4, 0.6)]
+
+    def fill(k, v, at):  # rows at positions `at` of a request
+        for odd in (0, 1):
+            rows = [i for i, p in enumerate(at) if p % 2 == odd]
+            first = torch.tensor(scores[odd]).to(BF)
+            k[rows] = 0.0
+            k[rows, :, 0] = first.to(DEV)
+            k[rows, :, 1] = float((scores[odd] - first.double()) * 256)
+            v[rows] = 1.0 - 2.0 * odd
+    for r, n in enumerate(ctx):
+        for j in range(-(-n // 16)):
+            page, here = int(c["table"][r, j]), min(16, n - 16 * j)
+            fill(c["kc"][page, :here], c["vc"][page, :here], range(16 * j, 16 * j + here))
+            if j == 0:  # one key of weight 1 sets the maximum
+                c["kc"][page, 0], c["vc"][page, 0] = 0.0, 0.0
+        fill(c["k"][c["cu"][r]:c["cu"][r + 1]], c["v"][c["cu"][r]:c["cu"][r + 1]], range(n, n + new[r]))
+    c["k"][c["cu"][:-1][np.array(new) > 0]] = 0.0  # here too, of the first new token
+    c["v"][c["cu"][:-1][np.array(new) > 0]] = 0.0
+    err = _err()
+    out, _ = _run(c, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    want, wlse, mag, big, keys = F.attention(c["q"], c["k"], c["v"], c["kc"], c["vc"], c["cu"], c["ctx"], c["table"],
+                                             c["mask"], c["scale"])
+    _, rel = F.attention_bound(want, wlse, mag, big, keys, D, F32)
+    tol = 1.01 * (rel + 2.0 ** -15)[..., None] * mag + 1.01 * F.UBF * want.abs() + 1e-30
+    assert ((out.double().cpu() - want).abs() <= tol).all(), float(((out.double().cpu() - want).abs() / tol).max())
+
+
+@pytest.mark.parametrize("dtype,H,D,new", [(BF, 4, 128, [1, 3]), (BF, 8, 64, [4, 1]), (BF, 8, 128, [30, 9]), (F32, 4, 64, [2, 2])])
+def test_attention_infinite_cached_values(dtype, H, D, new):
+    """An infinite value of the cache gives infinity in its column, whatever its weight's parts: one, none or several of
+    them, and their signs."""
+    c = _attn(dtype, H, 1, D, 16, new, [200, 1000], False, seed=49)
+    for r, (pos, col, inf) in enumerate([(70, 3, float("inf")), (999, 40, float("-inf"))]):
+        c["vc"][int(c["table"][r, pos // 16]), pos % 16, 0, col] = inf
+    out, _ = _run(c, _err())
+    torch.cuda.synchronize()
+    first = out[:new[0]], out[new[0]:]
+    for part, col, inf in ((first[0], 3, float("inf")), (first[1], 40, float("-inf"))):
+        assert (part[..., col] == inf).all()
+        assert torch.isfinite(part[..., :col]).all() and torch.isfinite(part[..., col + 1:]).all()
+
+
 @pytest.mark.parametrize("dtype,D", [(BF, 64), (BF, 96), (F32, 64)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_attention_values_of_vanishing_weights_count(dtype, D, bad):
