@@ -372,6 +372,7 @@ PyObject *tree_attention(PyObject *const *a, PyObject *) {
     if (a[9] != Py_None) {
         int64_t words = 0;
         p.tree_mask = reinterpret_cast<const uint32_t *>(table(a[9], "tree_mask", T, words));
+        if (T > 0 && words == 0) refuse("tree_mask must have a word at least");  // it has no pointer: a chain
         p.mask_words = size32(words, "tree_mask words");
     }
     p.scale = a[10] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : real(a[10]);

@@ -938,6 +938,16 @@ def test_outputs_for_another_stream_have_no_work_to_come(as_number):
         assert torch.equal(a, b)
 
 
+def test_a_mask_without_words_is_refused():
+    """A tensor of no elements has no pointer: it is not a chain's missing mask."""
+    c = _attn(BF, 4, 1, 64, 16, [2, 3], [20, 0], True, seed=52)
+    c["mask"] = c["mask"][:, :0].copy()
+    with pytest.raises(ValueError, match="tree_mask must have a word"):
+        _run(c, None)
+    out, lse = _run(_attn(BF, 4, 1, 64, 16, [0, 0], [20, 0], False, seed=52) | dict(mask=np.zeros((0, 0), np.uint32)), None)
+    assert out.shape[0] == 0 and lse.shape[0] == 0
+
+
 def test_a_stream_of_another_device_is_refused():
     class Elsewhere:
         cuda_stream, device_index = 0, torch.cuda.current_device() + 1
