@@ -724,14 +724,14 @@ typedef struct kv_commit_args {
     int32_t kv_heads, headdim;
     int32_t dtype;
     int32_t block_size, num_blocks;
-    int32_t max_path;     /* columns of path (0 with path NULL) */
+    int32_t max_path;     /* columns of path (0: no path, every token is copied) */
     int64_t k_stride, v_stride;  /* elements from one token to the next */
     int64_t cache_block_stride;  /* elements from one block to the next */
     /* device pointers */
     const void *k_new, *v_new;   /* [T, kv_heads, D] */
     const int32_t *slots;        /* [T] */
     const int32_t *cu_seqlens;   /* [S+1] */
-    const int32_t *path;         /* [S, max_path] or NULL */
+    const int32_t *path;         /* [S, max_path]; NULL with max_path 0, and where S is 0 */
     const int32_t *path_lens;    /* [S] (NULL with path NULL) */
     const int32_t *context_lens; /* [S] or NULL */
     int32_t *context_out;        /* [S] or NULL (both or neither) */

@@ -118,7 +118,8 @@ ssd_status_t check_commit(const kv_commit_args *a) {
         !stride_ok(a->v_stride, row, a->dtype) ||
         !pages_ok(a->block_size, a->num_blocks, a->cache_block_stride, row, a->dtype))
         return SSD_ERR_INVALID_ARG;
-    if ((a->path == nullptr) != (a->path_lens == nullptr) || (a->path == nullptr) != (a->max_path == 0) ||
+    if ((a->path == nullptr) != (a->path_lens == nullptr) || (a->path && a->max_path == 0) ||
+        (!a->path && a->max_path > 0 && a->num_seqs > 0) ||  // without requests there is nothing to point at
         (a->context_lens == nullptr) != (a->context_out == nullptr))
         return SSD_ERR_INVALID_ARG;
     if ((int64_t)a->num_seqs * a->max_path >= (int64_t{1} << 31)) return SSD_ERR_INVALID_ARG;
@@ -168,5 +169,6 @@ extern "C" ssd_status_t kv_tree_attention(const kv_attention_args *a, void *work
 extern "C" ssd_status_t kv_commit_tokens(const kv_commit_args *a, ssd_stream_t stream) {
     const ssd_status_t st = check_commit(a);
     if (st != SSD_OK || (a->total_tokens == 0 && (a->num_seqs == 0 || !a->context_out))) return st;
+    if (a->num_seqs == 0 && a->max_path > 0) return st;  // no paths
     return from_cuda(ssd::kv_commit_launch(*a, reinterpret_cast<cudaStream_t>(stream)));
 }

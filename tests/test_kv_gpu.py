@@ -828,6 +828,13 @@ def test_commit_all_tokens_and_errors():
     assert torch.equal(flat[7], k[7]) and torch.equal(flat[9], k[10])
 
 
+def test_commit_of_paths_without_requests():
+    k, kc = torch.ones(3, 1, 8, device=DEV), torch.zeros(1, 4, 1, 8, device=DEV)
+    out = ssd.kv_commit_tokens(k, k, kc, kc.clone(), _i([0, 1, 2]), _i([0]), _i([]), _i(np.zeros((0, 2))), _i([]))
+    torch.cuda.synchronize()
+    assert out.shape == (0,) and (kc == 0).all()
+
+
 # ------------------------------------------------------------------ binding --
 
 @pytest.mark.parametrize("word", [torch.zeros(0, dtype=torch.int32), torch.zeros(1, dtype=torch.int16),

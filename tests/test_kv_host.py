@@ -191,3 +191,10 @@ def test_marshalling_module_is_rebuilt_for_another_torch(lib, monkeypatch):
     monkeypatch.setattr(torch, "__version__", torch.__version__ + "x")
     with pytest.raises(Started):
         _build._compile_calls()
+
+
+def test_commit_of_paths_without_requests_is_a_no_op(lib):
+    """Tensors of no elements have no pointers; without requests, paths say that nothing is copied."""
+    none = dict(num_seqs=0, path=None, path_lens=None, context_lens=None, context_out=None)
+    assert lib.kv_commit_tokens(ctypes.byref(_commit(**none)), None) == B.SSD_OK
+    assert lib.kv_commit_tokens(ctypes.byref(_commit(total_tokens=0, **none)), None) == B.SSD_OK
