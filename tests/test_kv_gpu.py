@@ -966,6 +966,118 @@ def test_a_stream_of_another_device_is_refused():
     assert (kc == 0).all()
 
 
+def _refused(call, good, over, error, match):
+    """The call with good arguments passes; with some of them replaced it is refused by the right exception."""
+    call(**good)
+    with pytest.raises(error, match=match):
+        call(**{**good, **over(good)})
+    torch.cuda.synchronize()
+
+
+def _gaps(t):  # the same values, with rows that are not dense
+    return torch.stack([t, t], -1)[..., 0]
+
+
+@pytest.mark.parametrize("over,error,match", [
+    (lambda a: dict(new_lens=_i([1])), ValueError, "new_lens must be int32 of shape"),
+    (lambda a: dict(context_lens=a["context_lens"].long()), ValueError, "context_lens must be int32"),
+    (lambda a: dict(block_table=a["block_table"][0]), ValueError, "block_table must be int32"),
+    (lambda a: dict(block_table=_gaps(a["block_table"])), ValueError, "block_table must be contiguous"),
+    (lambda a: dict(ring_state=_i([0, 3, 0])), ValueError, "ring_state"),
+    (lambda a: dict(max_tokens=-1), ValueError, "max_tokens must not be negative"),
+    (lambda a: dict(max_tokens=1 << 40), ValueError, "max_tokens must fit 32 bits"),
+    (lambda a: dict(block_size=0), ssd.SSDError, "kv_block_tables"),
+    (lambda a: dict(block_size="16"), TypeError, "integer"),
+    (lambda a: dict(out={}), KeyError, "cu_seqlens"),
+    (lambda a: dict(reserved_lens=a["reserved_lens"].cpu()), ValueError, "reserved_lens must be a CUDA tensor"),
+    (lambda a: dict(free_ring=None), ValueError, "free_ring is required"),
+])
+def test_tables_refuse_bad_tensors(over, error, match):
+    good = dict(context_lens=_i([3, 0]), new_lens=_i([2, 1]), reserved_lens=_i([3, 0]), block_table=_i([[1, 0], [0, 0]]),
+                free_ring=_i([2, 3, 4]), ring_state=_i([0, 3]), block_size=4, num_blocks=9, max_tokens=5)
+    _refused(ssd.kv_block_tables, good, over, error, match)
+
+
+@pytest.mark.parametrize("over,error,match", [
+    (lambda a: dict(q=a["q"][0]), ValueError, "q and k must be"),
+    (lambda a: dict(q=a["q"].half()), ValueError, "q must be bfloat16 or float32"),
+    (lambda a: dict(k=a["k"].float()), ValueError, "k must be bfloat16"),
+    (lambda a: dict(k=a["k"][:2]), ValueError, "k must be"),
+    (lambda a: dict(q=_gaps(a["q"])), ValueError, "rows of q must be dense"),
+    (lambda a: dict(v=a["v"].transpose(1, 2).contiguous().transpose(1, 2)), ValueError, "rows of v must be dense"),
+    (lambda a: dict(q=torch.zeros(5 * 4 * 64 + 1, dtype=BF, device=DEV)[1:].view(5, 4, 64)), ssd.SSDError, "kv_qk_norm_rope"),
+    (lambda a: dict(q=torch.zeros(5, 4 * 64 + 4, dtype=BF, device=DEV)[:, :256].unflatten(1, (4, 64))), ssd.SSDError, "kv_qk"),
+    (lambda a: dict(q=torch.zeros(5, 3, 64, dtype=BF, device=DEV)), ssd.SSDError, "kv_qk_norm_rope"),
+    (lambda a: dict(positions=a["positions"].long()), ValueError, "positions must be int32"),
+    (lambda a: dict(positions=None), ValueError, "positions is required"),
+    (lambda a: dict(cos_sin=a["cos_sin"].to(BF)), ValueError, "cos_sin must be float32"),
+    (lambda a: dict(cos_sin=a["cos_sin"][:, :63].contiguous()), ssd.SSDError, "kv_qk_norm_rope"),
+    (lambda a: dict(q_weight=a["q_weight"][:32].contiguous()), ValueError, "q_weight must be float32"),
+    (lambda a: dict(k_weight=a["k_weight"].to(BF)), ValueError, "k_weight must be float32"),
+    (lambda a: dict(slots=a["slots"][:4]), ValueError, "slots must be int32"),
+    (lambda a: dict(v_cache=None), ValueError, "v_cache is required"),
+    (lambda a: dict(v_cache=a["v_cache"].float()), ValueError, "k_cache and v_cache must be"),
+    (lambda a: dict(k_cache=a["k_cache"].transpose(1, 2).contiguous().transpose(1, 2)), ValueError, "blocks of k_cache"),
+    (lambda a: dict(k_cache=torch.zeros(4, 8, 2, 64, dtype=BF, device=DEV)[:, :4]), ValueError, "same block stride"),
+    (lambda a: dict(q_out=torch.zeros(5, 4, 64, device=DEV)), ValueError, "q_out must be bfloat16"),
+    (lambda a: dict(k_out=_gaps(a["k"])), ValueError, "k_out must be contiguous"),
+    (lambda a: dict(eps="x"), TypeError, "real number|float"),
+])
+def test_norm_rope_refuses_bad_tensors(over, error, match):
+    x = torch.zeros(5, 8, 64, dtype=BF, device=DEV)
+    good = dict(q=x[:, :4], k=x[:, 4:6], v=x[:, 6:], positions=_i(range(5)), cos_sin=torch.ones(8, 64, device=DEV),
+                q_weight=torch.ones(64, device=DEV), k_weight=torch.ones(64, device=DEV), slots=_i(range(5)),
+                k_cache=torch.zeros(4, 4, 2, 64, dtype=BF, device=DEV), v_cache=torch.zeros(4, 4, 2, 64, dtype=BF, device=DEV))
+    _refused(ssd.kv_qk_norm_rope, good, over, error, match)
+
+
+@pytest.mark.parametrize("over,error,match", [
+    (lambda a: dict(q=a["q"][0]), ValueError, "q and k_new must be"),
+    (lambda a: dict(k_new=a["k_new"].float()), ValueError, "k_new must be bfloat16"),
+    (lambda a: dict(v_new=a["v_new"][:2]), ValueError, "v_new must be"),
+    (lambda a: dict(q=_gaps(a["q"])), ValueError, "rows of q must be dense"),
+    (lambda a: dict(k_cache=a["k_cache"][:, :, :1]), ValueError, "k_cache and v_cache must be"),
+    (lambda a: dict(cu_seqlens=_i([])), ValueError, "cu_seqlens must have an entry more"),
+    (lambda a: dict(cu_seqlens=_i([0, 1, 3, 3])), ValueError, "context_lens must be int32"),
+    (lambda a: dict(context_lens=a["context_lens"].long()), ValueError, "context_lens must be int32"),
+    (lambda a: dict(block_table=a["block_table"][:1]), ValueError, "block_table must be int32"),
+    (lambda a: dict(tree_mask=a["tree_mask"][:2]), ValueError, "tree_mask must be int32"),
+    (lambda a: dict(tree_mask=a["tree_mask"].long()), ValueError, "tree_mask must be int32"),
+    (lambda a: dict(max_new_tokens=-1), ssd.SSDError, "kv_tree_attention"),
+    (lambda a: dict(max_new_tokens=1 << 31), ValueError, "max_new_tokens must fit 32 bits"),
+    (lambda a: dict(scale=float("inf")), ssd.SSDError, "kv_tree_attention"),
+    (lambda a: dict(wait_limit_cycles=-1), ssd.SSDError, "kv_tree_attention"),
+    (lambda a: dict(out=torch.zeros(3, 4, 64, device=DEV)), ValueError, "out must be bfloat16"),
+    (lambda a: dict(lse=torch.zeros(3, 3, device=DEV)), ValueError, "lse must be float32"),
+])
+def test_attention_refuses_bad_tensors(over, error, match):
+    x, c = torch.zeros(3, 8, 64, dtype=BF, device=DEV), torch.zeros(4, 8, 2, 64, dtype=BF, device=DEV)
+    good = dict(q=x[:, :4], k_new=x[:, 4:6], v_new=x[:, 6:], k_cache=c, v_cache=c.clone(), cu_seqlens=_i([0, 1, 3]),
+                context_lens=_i([9, 0]), block_table=_i([[1, 2], [3, 0]]), max_new_tokens=2, tree_mask=_i([[1], [1], [3]]))
+    _refused(ssd.kv_tree_attention, good, over, error, match)
+
+
+@pytest.mark.parametrize("over,error,match", [
+    (lambda a: dict(k_new=a["k_new"][0]), ValueError, "k_new must be"),
+    (lambda a: dict(v_new=a["v_new"].float()), ValueError, "v_new must be bfloat16"),
+    (lambda a: dict(slots=a["slots"][:2]), ValueError, "slots must have an entry for each"),
+    (lambda a: dict(slots=a["slots"].long()), ValueError, "slots must be int32"),
+    (lambda a: dict(cu_seqlens=None), ValueError, "cu_seqlens is required"),
+    (lambda a: dict(cu_seqlens=_i([])), ValueError, "cu_seqlens must have an entry more"),
+    (lambda a: dict(path=a["path"][:, :0].contiguous()), ValueError, "path must have a column"),
+    (lambda a: dict(path=a["path"][:1]), ValueError, "path must be int32"),
+    (lambda a: dict(path_lens=None), ValueError, "path_lens is required"),
+    (lambda a: dict(context_lens=_i([1])), ValueError, "context_lens must be int32"),
+    (lambda a: dict(context_out=_i([1, 2, 3])), ValueError, "context_out must be int32"),
+    (lambda a: dict(v_cache=a["v_cache"][:3]), ValueError, "k_cache and v_cache must be"),
+])
+def test_commit_refuses_bad_tensors(over, error, match):
+    x, c = torch.zeros(3, 4, 64, dtype=BF, device=DEV), torch.zeros(4, 8, 2, 64, dtype=BF, device=DEV)
+    good = dict(k_new=x[:, :2], v_new=x[:, 2:], k_cache=c, v_cache=c.clone(), slots=_i([1, 2, 3, -1]), cu_seqlens=_i([0, 1, 3]),
+                context_lens=_i([9, 0]), path=_i([[0], [1]]), path_lens=_i([1, 1]))
+    _refused(ssd.kv_commit_tokens, good, over, error, match)
+
+
 # ----------------------------------------------------------------- together --
 
 def test_hybrid_tree_decode_example():
