@@ -678,7 +678,8 @@ typedef struct kv_attention_args {
     int32_t nheads, kv_heads, headdim;
     int32_t dtype;        /* ssd_dtype_t of q, k_new, v_new, the cache and out */
     int32_t block_size, num_blocks, table_cols;
-    int32_t max_new_tokens; /* most new tokens of a request: sizes the tiles, results do not depend on it */
+    int32_t max_new_tokens; /* most new tokens of a request: sizes the tiles.  Whatever it is, results differ by
+                               their rounding only */
     int32_t mask_words;     /* 32-bit words of a tree_mask row (0 with tree_mask NULL) */
     float scale;
     int64_t q_stride, k_stride, v_stride; /* elements from one token to the next */

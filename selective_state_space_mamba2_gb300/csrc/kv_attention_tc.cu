@@ -6,8 +6,8 @@
 //   P = exp2(c S - m)  one row per thread (TMEM lane), written over S in TMEM as bf16
 //   O += P V           tcgen05, 128 x headdim, K = 64, P from TMEM, V MN-major
 // with the running maximum m and the sum of the weights in registers (fp32).  O stays in TMEM; it
-// is only rescaled when a row's maximum grows by more than 2^8 (the weights are then at most
-// 2^8, exact powers of two apart from what they would be, and the sum is kept to the same m).
+// is only rescaled when a row's maximum grows by more than 2^8.  Up to then the weights, at most 2^8,
+// and their sum go by the same older m, which cancels but for the rounding of the weights.
 // V is bf16, and both operands of a product have one type, so P is, too.  In tiles of at most 32 rows (decode
 // steps, short drafts), whose bytes or latency are the bound, it is held in two parts, high and low, side by side
 // in the columns that the scores leave, and multiplied by V twice: 2^-15 is lost of a weight instead of 2^-8.  The
@@ -28,10 +28,10 @@
 // one that comes second finds them in L2.  Neither waits for the other.
 //
 // What bounds it.  Few rows a request (decode steps, short drafts): the bytes of the cache, 256 requests
-// of 4 tokens over up to 8192 cached 649 to 651 us, 7.0 TB/s.  Prompts and large trees: shared memory.  Of a
+// of 4 tokens over up to 8192 cached 647 to 651 us, 7.0 TB/s.  Prompts and large trees: shared memory.  Of a
 // tile's 512 cycles of products S takes 384 instead of 256 (a product 128 x 64 x 16 reads 6 KB), V is
 // read in 128, and the copies write 32 KB in 256: 768, and 720 to 790 measured; 4 prompts of 512 to 4096
-// tokens over up to 8192 747 to 777 us, 1360 to 1410 TFLOP/s.  Tried against that, and not faster: tiles of 128
+// tokens over up to 8192 741 to 777 us, 1360 to 1425 TFLOP/s.  Tried against that, and not faster: tiles of 128
 // keys with one buffer of scores (the chain of scores, softmax, output then is the bound), two row tiles
 // in a CTA, and products of a pair's 256 rows (cta_group::2, half the keys and values in each CTA: 830
 // us; the weights of both CTAs have to reach the one that issues, 0.8 us a tile for the chain).

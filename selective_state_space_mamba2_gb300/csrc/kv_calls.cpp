@@ -2,7 +2,7 @@
 //
 // A decode step makes these calls between kernels of a few microseconds; checking a dozen tensors
 // and filling a ctypes structure takes the interpreter 15 to 35 us a call, several times the
-// kernel, and here 3 to 6.  No numeric step runs in this file: it checks shapes, types and strides,
+// kernel, and here 4 to 9.  No numeric step runs in this file: it checks shapes, types and strides,
 // allocates outputs that the caller did not give, and calls the C ABI of ssd.h.  An argument that
 // is refused raises ValueError; a status other than SSD_OK comes back as a Python int, which the
 // binding raises as SSDError.

@@ -193,7 +193,9 @@ struct FindSmem {
 // Shortest run.  An item of L units cut into runs of u takes u + c L / u, with a part's cost c in the join: least at
 // u = sqrt(c L).  With runs of 1 / 4 units 2 requests of 20 to 31 tokens over 5419, 8 query heads, take 28.4 /
 // 19.4 us (c = 0.4: 5.9), one of 200 tokens 19.0 / 15.3 (min_units), 5 of up to 4 tokens over 2287 16.6 / 13.4
-// (c = 0.1: 1.9), but one token over 777 10.5 / 12.7 (1.3).
+// (c = 0.1: 1.9), but one token over 777 10.5 / 12.7 (1.3).  Where the root says less, a run is one key tile, on
+// the CUDA cores (tiles of 32 keys) as on the tensor cores; with runs of two / one there 4 single tokens over up to 274 take
+// 12.1 / 10.1 us, 13 of up to 5 over 260 12.4 / 11.2, one over 2000 12.2 / 13.0.
 __device__ __forceinline__ bool find_run(const kv_attention_args &a, const Tiling &g, int32_t me, int32_t of,
                                          FindSmem &sm, Border *borders, Walk &w) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nwarp = nthr >> 5;
