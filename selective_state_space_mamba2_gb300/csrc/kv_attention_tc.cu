@@ -16,8 +16,8 @@
 // 649 us with two parts / 668 with one, one token over 65536 50.1 / 49.4, one over 777 10.8 / 10.3, 16 of 4
 // over up to 1000 18.3 / 16.9, 4 single tokens of 64 heads over 4000 17.8 / 16.0.  Tiles of more rows have P rounded
 // to bf16, an error of the order of the output's own rounding (0.0018 to 0.0020 of the outputs' norm, 0.0015 without);
-// two parts there make 4 prompts 1010 us from 770, a tree of 32 tokens over 4000 24.3 from 20.7.  The sum of the
-// weights takes them before any rounding.
+// two parts there make 4 prompts 960 to 1000 us from 735 to 755, 24 trees 242 from 186, a tree of 32 tokens over 4000
+// 24.3 from 21.9.  The sum of the weights takes them before any rounding.
 //
 // Roles (192 threads, two CTAs per SM so that one's softmax runs beside the other's products):
 // warps 0-3 softmax and output, warp 4 TMA loads, warp 5 the products.  Keys and values pass
