@@ -424,10 +424,8 @@ def run(s):
                                         path=s.get("path"), path_lens=s.get("lens"))
         return [s["kc"], s["ks"], s["vc"], s["vs"], lens]
     if op == "read":
-        if "rows" not in s:  # a number that a program has at hand, not a part of its call
-            s["rows"] = sum(_lens(s["case"])[0])
         return list(ssd.kv_read_tokens_fp8(s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["cu"], s["ctx"],
-                                           total_tokens=s["rows"], dtype=TYPES[s["case"]["type"]]))
+                                           total_tokens=int(sum(_lens(s["case"])[0])), dtype=TYPES[s["case"]["type"]]))
     if op == "attn":
         return list(ssd.kv_tree_attention_fp8(s["q"], s["k"], s["v"], s["kc"], s["vc"], s["ks"], s["vs"], s["cu"], s["ctx"],
                                               s["table"], max_new_tokens=s["most"], tree_mask=s["mask"], return_lse=True))
