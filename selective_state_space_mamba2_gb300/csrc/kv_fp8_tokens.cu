@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     const int tok0 = lane / pieces, piece0 = lane - tok0 * pieces, tok_step = team / pieces, piece_step = team - tok_step * pieces;
     const int64_t in_step = tok_step * stride, out_step = tok_step * row;
     Eight<T> x[kHold];
+    int turn = 0;  // which of the two places for maxima: changes with every item worked on, not with those that are empty
     for (int item = 0; item < items; ++item) {
         const Item m = found[item];
         const int count = m.rows * pieces;
@@ -223,10 +224,11 @@ __global__ void __launch_bounds__(kThreads, kCtas)
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        if (team > 32) {  // (two places: a warp is an item ahead of another at most)
-            if ((tid & 31) == 0) tops[item & 1][tid >> 5] = top;
+        if (team > 32) {  // (two places: a warp is a barrier ahead of another at most)
+            if ((tid & 31) == 0) tops[turn][tid >> 5] = top;
             asm volatile("bar.sync %0, %1;" ::"r"(tid / team + 1), "r"(team) : "memory");
-            for (int w = 0; w < team / 32; ++w) top = fmaxf(top, tops[item & 1][tid / team * (team / 32) + w]);
+            for (int w = 0; w < team / 32; ++w) top = fmaxf(top, tops[turn][tid / team * (team / 32) + w]);
+            turn ^= 1;
         }
         float now = fp8::scale_for(top);
         if (m.fill > 0) {
