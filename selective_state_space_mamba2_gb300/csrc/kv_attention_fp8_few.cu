@@ -3,20 +3,23 @@
 //
 // With few query rows the keys are the long side, so they are the rows of the products (TMEM lanes), in tiles of 128:
 //   S^T = K Q^T        e4m3, 128 x 2R, K = headdim: the codes as they are; queries as two parts, high and low, side by side
-//   P   = 2^(t - m)    t = s (c / u) ks + log2 vs; one key per thread, its R weights as two e4m3 parts to shared memory
-//   O^T += V^T P       e4m3, headdim x 2R, K = 128: both parts at once, each to its own columns
+//   P   = 2^(t - m)    t = s (c / u) ks + log2 vs; one key per thread, its R weights as four e5m2 parts to shared memory
+//   O^T += V^T P       e4m3 times e5m2, headdim x 4R, K = 128: all parts at once, each to its own columns
 // R is 16 or 32.  A key's scales ks, vs are constants of its thread; u is the row's unit, the power of two that puts its
 // largest query entry in [128, 256).  A tile's codes are read once for each product, 16 KB and 16 KB, whatever the rows
 // (with the queries as rows, padded to 128 of them, a product read them, too: 642 cycles of an SM for 64 keys, here 320 for
 // 128), and a thread has R weights to make for 128 keys, not 64 for 64.
 //
-// m belongs to a row.  It is 2^3 below the row's largest weight when it is set, and a tile is taken by it as long as no
-// weight passes 256 (e4m3 ends at 448), which the threads find out by one barrier that votes; only where one does (an
+// m belongs to a row.  It is 2^12 below the row's largest weight when it is set, and a tile is taken by it as long as no
+// weight passes 2^15 (fp16 ends at 2^16), which the threads find out by one barrier that votes; only where one does (an
 // item's first tile, seldom later) the maxima are reduced, and O^T and the sums rescaled.  A value's scale is part of its
 // weight; the sum of the weights takes them without.  Sums stay with the threads, a row's 128 of them are added up at the end.
 //
-// Rounding.  Queries in two parts lose at most 2^-17 of the row's largest entry (kv_attention_fp8_tc.cu).  Weights in two
-// parts, the low one in units of 1/16, are off by 2^-8 of themselves, or 2^-17 of the largest.
+// Rounding.  Queries in two parts lose at most 2^-17 of the row's largest entry (kv_attention_fp8_tc.cu).  Weights are
+// rounded to fp16: off by 2^-11 of themselves, or 2^-37 of the largest that m was set by.  e5m2 is fp16 without its last 8
+// bits, so a part takes a weight's first three significant bits as they stand, and the next one what is left times 8: the four,
+// in units of 1, 1/8, 1/64 and 1/512, hold an fp16 number exactly, down to its smallest step.  (Two e4m3 parts reach
+// only 2^-17 below the largest weight: where one key has 0.9 of it, 8192 others lost 7 % of theirs.)
 //
 // New tokens' tiles are bf16 with the queries as they were given: 64-column halves of 128 keys, and 64 keys' values, in a
 // ring stage each; weights as two bf16 parts.
@@ -49,10 +52,11 @@ constexpr int kOverhead = 2;          // of an item, in key tiles
 constexpr int kScaleRing = 4;         // tiles whose scales are kept: the ring lets keys come three tiles ahead
 constexpr int kStage = kKeys * 128;   // bytes of a ring stage
 constexpr int kBoxes = kKeys / 8;     // most boxes of a tile
-constexpr float kBelow = 3.f;         // m is so far (base 2) below the largest weight when it is set
-constexpr float kMost = 8.f;          // weights stay at most 2^8
+constexpr float kBelow = 12.f;        // m is so far (base 2) below the largest weight when it is set
+constexpr float kMost = 15.f;         // weights stay at most 2^15
 constexpr float kSlack = 2.f;         // of the rows whose m could be set, those are that have grown by so much
-constexpr float kLow = 16.f;          // units of the low part
+constexpr int kPieces = 4;            // e5m2 parts of a weight
+constexpr float kUnit = 8.f;          // of a part, against the next one
 constexpr uint32_t kSoftmaxBar = 1, kVoteBar = 2;
 
 struct Params {
@@ -67,6 +71,7 @@ struct Params {
 };
 
 template <int R> constexpr int kStages = R == 16 ? 5 : 4;
+template <int R> constexpr int kPlaces = R == 16 ? 2 : 1;  // tiles whose weights are kept
 
 template <int R> struct Bars {
     enum {
@@ -78,8 +83,9 @@ template <int R> struct Bars {
 template <int D, int R> struct Layout {
     static constexpr int kParts = 0;                              // [2R] rows of D bytes: high parts, low parts
     static constexpr int kQ = kParts + 2 * R * D;                 // queries: [D / 64][R] rows of 128 bytes
-    static constexpr int kP = kQ + R * D * 2;                     // weights, two tiles': [128] rows of 2R bytes
-    static constexpr int kRing = kP + 2 * kKeys * 2 * R;
+    static constexpr int kP = kQ + R * D * 2;                     // weights: [128] rows of 4R bytes, a part after the other
+    static constexpr int kPlace = kKeys * kPieces * R;            // (of new tokens: two tiles of 2R bytes, high and low parts)
+    static constexpr int kRing = kP + kPlaces<R> * kPlace;
     static constexpr int kScales = kRing + kStages<R> * kStage;   // [kScaleRing][2][kBoxes]: ks, vs of a tile's boxes
     static constexpr int kFactors = kScales + kScaleRing * 2 * kBoxes * 4;  // [2][R]: c / u of an item's rows
     static constexpr int kTops = kFactors + 2 * R * 4;            // [R]: m
@@ -122,15 +128,25 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// Four values in two e4m3 parts, the low one times `unit` (two fp16 of it).
-__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t unit, uint32_t &high, uint32_t &low) {
+// Four values in two e4m3 parts.
+__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t &high, uint32_t &low) {
     const uint32_t x = cvt_f16x2(a, b), y = cvt_f16x2(c, d);
     const uint32_t hx = e4m3x2(x), hy = e4m3x2(y);
     high = __byte_perm(hx, hy, 0x5410);
-    low = __byte_perm(e4m3x2(hmul2_u32(sub_f16x2(x, f16x2_of(hx)), unit)), e4m3x2(hmul2_u32(sub_f16x2(y, f16x2_of(hy)), unit)),
-                      0x5410);
+    low = __byte_perm(e4m3x2(sub_f16x2(x, f16x2_of(hx))), e4m3x2(sub_f16x2(y, f16x2_of(hy))), 0x5410);
 }
-constexpr uint32_t kOne16 = 0x3C003C00u, kLow16 = 0x4C004C00u;  // 1 and 16, twice
+// Four weights, as fp16, in e5m2 parts: an fp16 number's first byte, and the rest times 8 (neither rounds).
+__device__ __forceinline__ void pieces4(float2 a, float2 b, uint32_t (&part)[kPieces]) {
+    constexpr uint32_t kFirst = 0xFF00FF00u, kEight = 0x48004800u;  // first bytes; 8, twice
+    uint32_t x = cvt_f16x2(a.x, a.y), y = cvt_f16x2(b.x, b.y);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        part[i] = __byte_perm(x, y, 0x7531);
+        if (i + 1 == kPieces) break;
+        x = hmul2_u32(sub_f16x2(x, x & kFirst), kEight);
+        y = hmul2_u32(sub_f16x2(y, y & kFirst), kEight);
+    }
+}
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
@@ -221,7 +237,7 @@ template <int D, int R> __device__ __forceinline__ void split_queries(uint8_t *s
         if (top == 0) unit = 1.f;
         uint32_t hi, lo;
         split4(__uint_as_float(x.x << 16) * unit, __uint_as_float(x.x & 0xFFFF0000u) * unit, __uint_as_float(x.y << 16) * unit,
-               __uint_as_float(x.y & 0xFFFF0000u) * unit, kOne16, hi, lo);
+               __uint_as_float(x.y & 0xFFFF0000u) * unit, hi, lo);
         uint8_t *to = smem + L::kParts;
         *reinterpret_cast<uint32_t *>(to + row_offset<D>(row, sub >> 2) + (sub & 3) * 4) = hi;
         *reinterpret_cast<uint32_t *>(to + row_offset<D>(R + row, sub >> 2) + (sub & 3) * 4) = lo;
@@ -239,7 +255,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     using B = Bars<R>;
     constexpr int kHalves = D / 64, kRing = kStages<R>;
     constexpr uint32_t kTmemCols = R == 16 ? 128 : 256;
-    constexpr uint32_t COL_S = 0, COL_O = 4 * R;  // two score tiles of 2R columns, the output
+    constexpr uint32_t COL_S = 0, COL_O = 4 * R;  // two score tiles of 2R columns, the output's 4R
+    static_assert(kTmemCols == 4 * R + kPieces * R, "columns");
     const kv_attention_args &a = p.a;
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
     const int group = a.nheads / a.kv_heads;
@@ -445,13 +462,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         // In the order of kv_attention_tc.cu, and as there: the warp walks along, an elected lane issues from uniform
         // values, and a wait that gave up does not stop it.
         const uint32_t tmu = __shfl_sync(~0u, tm, 0);
-        constexpr uint32_t kIdS8 = idesc_e4m3(128, 2 * R, 0, 0), kIdO8 = idesc_e4m3(128, 2 * R, 1, 1);
+        constexpr uint32_t kIdS8 = idesc_e4m3(128, 2 * R, 0, 0), kIdO8 = idesc_e4m3_e5m2(128, kPieces * R, 1, 1);
         constexpr uint32_t kIdS = idesc_bf16(128, R, 0, 0), kIdO = idesc_bf16(128, R, 1, 1);
         // values of 64 columns: their columns twice (the second 64 rows of O^T are not used)
         const uint64_t dParts = row_desc<D>(smem + L::kParts, 16), dQ = row_desc<128>(smem + L::kQ, 16);
         const uint64_t dK8 = row_desc<D>(smem + L::kRing, 16), dV8 = row_desc<D>(smem + L::kRing, 0);
         const uint64_t dK = row_desc<128>(smem + L::kRing, 16), dV = row_desc<128>(smem + L::kRing, kHalves == 2 ? 8192 : 0);
-        const uint64_t dP = row_desc<2 * R>(smem + L::kP, 0);
+        const uint64_t dP8 = row_desc<kPieces * R>(smem + L::kP, 0), dP = row_desc<2 * R>(smem + L::kP, 0);
         uint32_t st = 0, phase = 0;  // ring stage and its phase
         uint32_t tile = 0, items = 0, split = 0;  // split: items whose queries were split
         auto take = [&]() {  // waits for the next stage; its number, uniform
@@ -485,23 +502,23 @@ __global__ void __launch_bounds__(kThreads, 2)
         };
         auto output = [&](uint32_t g, bool cached, uint32_t add) {  // of tile number g
             const uint32_t s0 = take(), s1 = !cached && kHalves > 1 ? take() : s0;
-            const uint32_t gg = __shfl_sync(~0u, g, 0);
+            const uint32_t gg = __shfl_sync(~0u, g, 0), place = gg % kPlaces<R> * L::kPlace;
             wait(&bar[B::P_READY0 + (g & 1)], (g >> 1) & 1);
             tc_fence_after();
             if (elect_one()) {
                 if (cached) {
-                    const uint64_t v0 = desc_at(dV8, s0 * kStage), p0 = desc_at(dP, (gg & 1) * (kKeys * 2 * R));
+                    const uint64_t v0 = desc_at(dV8, s0 * kStage), p0 = desc_at(dP8, place);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma8_ss(tmu + COL_O, desc_at(v0, 32 * D * k), desc_at(p0, 64 * R * k), kIdO8, k > 0 ? 1u : add);
+                        mma8_ss(tmu + COL_O, desc_at(v0, 32 * D * k), desc_at(p0, 32 * kPieces * R * k), kIdO8, k > 0 ? 1u : add);
                 } else {
-                    // 64 keys in a stage, or all 128 of 64 columns; high parts, then low ones in the other place for weights
+                    // 64 keys in a stage, or all 128 of 64 columns; high parts to the first columns, low ones to the next
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             mma_ss(tmu + COL_O + R * part, desc_at(dV, (kHalves > 1 && k > 3 ? s1 * kStage + 2048 * (k - 4) : s0 * kStage + 2048 * k)),
-                                   desc_at(dP, part * (kKeys * 2 * R) + 32 * R * k), kIdO, k > 0 ? 1u : add);
+                                   desc_at(dP, place + part * (kKeys * 2 * R) + 32 * R * k), kIdO, k > 0 ? 1u : add);
                 }
                 mma_commit(&bar[B::O_DONE0 + (gg & 1)]);
                 mma_commit(&bar[B::KV_EMPTY0 + s0]);
@@ -539,7 +556,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         float *red = reinterpret_cast<float *>(smem + L::kRed);
         uint32_t tile = 0, ring = 0, scaled = 0;  // tile number, ring stages used by earlier items, cached tiles
         int item = 0;
-        bool plain = true;  // the tile before was a cached one, or there was none: it has one place for weights
         auto factors_of = [&](int i) { return reinterpret_cast<float *>(smem + L::kFactors) + (i & 1) * R; };
         auto rows_of = [&](const kvs::Walk &v) { return v.tokens(p.g) * group; };
         // The queries of item number i in parts, if it has cached tiles.  The scores of the item before are done.
@@ -559,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             ++item;
             const int token0 = w.first_token(p.g), rows = rows_of(w), n_tiles = w.t1 - w.t0;
             const uint32_t row_bits = rows >= 32 ? ~0u : (1u << rows) - 1;
+            const int pieces = w.t0 < w.cached_tiles ? kPieces : 2;  // columns of O^T that are in use, in parts
             // ring stages of the item's first x tiles
             auto stages = [&](int x) { return x + (kHalves - 1) * max(0, x - max(0, w.cached_tiles - w.t0)); };
             // which rows see new token j
@@ -666,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         __syncwarp();
                         tc_fence_after();
 #pragma unroll 1
-                        for (int part = 0; part < 2; ++part) {
+                        for (int part = 0; part < pieces; ++part) {
                             uint32_t o[R];
                             tmem_ld<R>(lane_base + COL_O + part * R, o);
                             tmem_ld_wait();
@@ -691,32 +708,28 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     sum[r] = fma_f2(v[r], make_float2(inv, inv), sum[r]);
                 }
-                // where the weights go is free: a cached tile has one of two places, a new one both
-                if (cached && plain) {
-                    if (tile > 1) wait(&bar[B::O_DONE0 + (tile & 1)], ((tile - 2) >> 1) & 1);
-                } else if (tile > 0) {
-                    wait(&bar[B::O_DONE0 + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1);
-                }
-                plain = cached;
-                uint8_t *to = smem + L::kP + (cached ? (tile & 1) * (kKeys * 2 * R) : 0);
+                // where the weights go is free
+                if (tile >= kPlaces<R>)
+                    wait(&bar[B::O_DONE0 + ((tile - kPlaces<R>) & 1)], ((tile - kPlaces<R>) >> 1) & 1);
+                uint8_t *to = smem + L::kP + tile % kPlaces<R> * L::kPlace;
                 if (cached) {
-                    uint32_t hi[R / 4], lo[R / 4];
-#pragma unroll
-                    for (int i = 0; i < R / 4; ++i) split4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y, kLow16, hi[i], lo[i]);
 #pragma unroll
                     for (int i = 0; i < R / 16; ++i) {
-                        *reinterpret_cast<uint4 *>(to + row_offset<2 * R>(tid, i)) =
-                            make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-                        *reinterpret_cast<uint4 *>(to + row_offset<2 * R>(tid, R / 16 + i)) =
-                            make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+                        uint32_t part[4][kPieces];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) pieces4(v[8 * i + 2 * k], v[8 * i + 2 * k + 1], part[k]);
+#pragma unroll
+                        for (int k = 0; k < kPieces; ++k)
+                            *reinterpret_cast<uint4 *>(to + row_offset<kPieces * R>(tid, k * R / 16 + i)) =
+                                make_uint4(part[0][k], part[1][k], part[2][k], part[3][k]);
                     }
                 } else {
                     uint32_t hi[R / 2], lo[R / 2];
 #pragma unroll
                     for (int i = 0; i < R / 2; ++i) {
                         hi[i] = pack_bf16(v[i].x, v[i].y);
-                        lo[i] = pack_bf16((v[i].x - __uint_as_float(hi[i] << 16)) * kLow,
-                                          (v[i].y - __uint_as_float(hi[i] & 0xFFFF0000u)) * kLow);
+                        lo[i] = pack_bf16((v[i].x - __uint_as_float(hi[i] << 16)) * kUnit,
+                                          (v[i].y - __uint_as_float(hi[i] & 0xFFFF0000u)) * kUnit);
                     }
 #pragma unroll
                     for (int i = 0; i < R / 8; ++i) {
@@ -801,13 +814,19 @@ __global__ void __launch_bounds__(kThreads, 2)
             wait(&bar[B::O_DONE0 + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1);
             __syncwarp();
             tc_fence_after();
-            uint32_t o[2 * R];
-            tmem_ld<2 * R>(lane_base + COL_O, o);
-            tmem_ld_wait();
             float y[R];
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                y[r] = fmaf(__uint_as_float(o[R + r]), 1.f / kLow, __uint_as_float(o[r])) * shrinks[r];
+            for (int r = 0; r < R; ++r) y[r] = 0.f;
+#pragma unroll 1
+            for (int part = pieces - 1; part >= 0; --part) {  // the smallest first
+                uint32_t o[R];
+                tmem_ld<R>(lane_base + COL_O + part * R, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int r = 0; r < R; ++r) y[r] = fmaf(y[r], 1.f / kUnit, __uint_as_float(o[r]));
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) y[r] *= shrinks[r];
             const int d = D == 128 ? tid : tid & 63;  // column
             if (dirty[item & 1] == item) {
                 // values that were taken out, to the rows that see them: only decides between infinity and NaN

@@ -308,6 +308,11 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N, uint32
     return (1u << 4) | (a_mn_major << 15) | (b_mn_major << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+// ... with e4m3 A and e5m2 B (format 1): the kind takes its operands' formats apart.
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2(uint32_t M, uint32_t N, uint32_t a_mn_major, uint32_t b_mn_major) {
+    return idesc_e4m3(M, N, a_mn_major, b_mn_major) | (1u << 10);
+}
+
 // The descriptor with 64-byte swizzle (rows of 64 bytes).
 __device__ __forceinline__ uint64_t sw64_desc(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
     return (sw128_desc(saddr, lbo_bytes, sbo_bytes) & ~(7ull << 61)) | 4ull << 61;
