@@ -7,11 +7,12 @@
 // with ks, vs the scales of the key's block and u the row's unit: the power of two that puts its largest query entry in
 // [128, 256).  A value's scale is part of its weight, and the running maximum m is that of the scaled weights, so blocks of
 // any scale share the accumulators; the sum of the weights takes them without (1 / vs, once for the keys of a block).
-// m is 2^6 below the row's largest when it is set, which may grow by 2^9 before O is rescaled: weights stay below 2^15.
+// m is 2^11 below the row's largest when it is set, which may grow by 2^4 before O is rescaled: weights stay below 2^15.
 //
 // Rounding.  A bf16 query entry has 8 significant bits: the high part takes 4, what is left has 4 more, so both hold it
-// but for e4m3's smallest step, 2^-9 u: 2^-17 of the row's largest entry is lost at most.  Weights are rounded to 2^-11.
-// Sums and statistics are fp32.
+// but for e4m3's smallest step, 2^-9 u: 2^-17 of the row's largest entry is lost at most.  Weights are rounded to fp16:
+// off by 2^-11 of themselves, or 2^-36 of the largest that m was set by.  (With m 2^6 below it fp16's smallest step was 2^-31 of it:
+// 65536 equal keys beside one with 0.999 of the weight were off by 2 %, and by 22 % with 0.9999.)  Sums and statistics are fp32.
 //
 // New tokens are not in the cache: their tiles are bf16, multiplied as in kv_attention_tc.cu with the queries as they were
 // given.  A ring stage holds such a tile; a cached one takes half of it, values' codes the second half.
@@ -46,8 +47,8 @@ constexpr int kLoadWarp = 4, kMmaWarp = 5;
 constexpr int kOverhead = 3;    // of an item, in key tiles
 constexpr int kStages = 5;
 constexpr int kScaleRing = 4;   // tiles whose scales are kept: the ring lets keys come three tiles ahead
-constexpr float kBelow = 6.f;   // m is so far (base 2) below the largest weight when it is set
-constexpr float kSlack = 9.f;   // growth of the largest weight that is let stand: fp16 ends at 2^16
+constexpr float kBelow = 11.f;  // m is so far (base 2) below the largest weight when it is set
+constexpr float kSlack = 4.f;   // growth of the largest weight that is let stand: fp16 ends at 2^16
 
 struct Params {
     kv_attention_args a;

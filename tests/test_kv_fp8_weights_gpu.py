@@ -131,3 +131,11 @@ def test_one_key_in_a_batch(H, n, D, share):
     """So many requests that a CTA has all of one's keys, or of several requests'."""
     _check(_case(H, D, n, 8192, share, 0, 64, 1.0, seed=3), copies=700 if n < 5 else 200)
     _check(_case(H, D, n, 3000, share, 2000, 16, 2.0 ** -20, seed=4), copies=700 if n < 5 else 200)
+
+
+@pytest.mark.parametrize("H,n", [(8, 30), (4, 70), (4, 1), (8, 4)])
+@pytest.mark.parametrize("share", [0.999, 0.9999])
+def test_one_key_beside_very_many(H, n, share):
+    """Weights as far below the largest as long caches have them."""
+    _check(_case(H, 64, n, 65536, share, 100, 64, 2.0 ** -20, seed=5), copies=60 if n > 5 else 400)
+    _check(_case(H, 128, n, 65536, share, 65535, 16, 0.5, seed=6), copies=1)
