@@ -825,8 +825,10 @@ SSD_API ssd_status_t kv_read_tokens_fp8(const kv_read_fp8_args *args, ssd_stream
 /*
  * kv_tree_attention_fp8 -- kv_tree_attention over a cache in 8 bits: args as there (dtype is that of q, k_new, v_new and
  * out; cache_block_stride counts bytes), with the scales beside them.  The new tokens' keys and values are taken as they
- * are given.  Scales are positive, of any value between 2^-64 and 2^100; other ones give results without meaning
- * for the requests that use them.
+ * are given.  Scales are positive, between 2^-64 and 2^100, and the scales of values of one request and head at most 2^96
+ * apart, the 1 of its new tokens among them (-64 to 32 in powers of two, say: kv_commit_tokens_fp8 writes those for values up to
+ * 2^40); others give results without meaning for the requests that use them: fp32's exponents do not hold both the weights
+ * times the scales and their sum without.
  * On the tensor cores (bf16, the sizes of kv_tree_attention, block_size a multiple of 8, blocks a multiple of 16 bytes
  * apart) the codes of keys are operands as they are, and queries that meet them are sums of two e4m3 parts, which lose at
  * most 2^-17 of a row's largest entry; weights of cached values as sums of two e4m3 parts (row tiles of at most 32 rows: off by 2^-8 of themselves) or as

@@ -13,7 +13,8 @@
 // m belongs to a row.  It is 2^12 below the row's largest weight when it is set, and a tile is taken by it as long as no
 // weight passes 2^15 (fp16 ends at 2^16), which the threads find out by one barrier that votes; only where one does (an
 // item's first tile, seldom later) the maxima are reduced, and O^T and the sums rescaled.  A value's scale is part of its
-// weight; the sum of the weights takes them without.  Sums stay with the threads, a row's 128 of them are added up at the end.
+// weight; the sum of the weights takes them without, divided by it.  A weight below 2^-126 is lost to both: with scales of a request
+// at most 2^96 apart, it is 2^-42 of the largest or less.  Sums stay with the threads, a row's 128 of them are added up at the end.
 //
 // Rounding.  Queries in two parts lose at most 2^-17 of the row's largest entry (kv_attention_fp8_tc.cu).  Weights are
 // rounded to fp16: off by 2^-11 of themselves, or 2^-37 of the largest that m was set by.  e5m2 is fp16 without its last 8
