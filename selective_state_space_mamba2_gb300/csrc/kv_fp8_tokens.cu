@@ -125,7 +125,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
             r = fp8::last_at_most(a.num_seqs, (long long)blockIdx.x * items, first);
             if (tid < items)
                 while (r + 1 < a.num_seqs && first(r + 1) <= at) ++r;
-            k = max(at - first(r), 0ll);
+            k = at - first(r);
+            if (k < 0) r = a.num_seqs;  // before the first request's tokens
         }
         Item m = {};
         if (tid < items && r < a.num_seqs) {

@@ -53,3 +53,15 @@ def test_commit_long_prompts_of_several_blocks_a_cta(H, b):
     c = _commit_case(BF, H, 128, b, new, [0, 5, 3, 77, 64, 63, 500, 31], seed=b, loud=(3, 6))
     _repeats(c, 4)
     _check_commit(c)
+
+
+@pytest.mark.parametrize("path", [False, True])
+@pytest.mark.parametrize("b,dtype", [(16, BF), (4, F32), (1, BF)])
+@pytest.mark.parametrize("pad", [1, 17, 200])
+def test_commit_behind_rows_of_no_request(b, dtype, path, pad):
+    """cu_seqlens that does not begin with 0: the rows before its first entry are no request's, and every block is written once."""
+    c = _commit_case(dtype, 2, 64, b, [5, 3, 0, 9], [3, 2 * b + 1, 7, b - 1], seed=pad + b, path=path, loud=(0, 3))
+    c["kv"] = torch.cat([torch.full((pad, c["kv"].shape[1]), float("nan"), dtype=dtype), c["kv"], torch.full((2, c["kv"].shape[1]), float("nan"), dtype=dtype)])
+    c["cu"] = c["cu"] + np.int32(pad)
+    _repeats(c)
+    _check_commit(c)
