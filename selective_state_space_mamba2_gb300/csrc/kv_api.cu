@@ -170,7 +170,8 @@ ssd_status_t check_commit_fp8(const kv_commit_fp8_args *a) {
     // what one CTA writes, others read
     const int64_t list = 4ll * a->num_seqs;
     if (overlap(a->context_out, list, a->context_lens, list) || overlap(a->context_out, list, a->cu_seqlens, list + 4) ||
-        overlap(a->context_out, list, a->path_lens, list))
+        overlap(a->context_out, list, a->path_lens, list) || overlap(a->context_out, list, a->path, list * a->max_path) ||
+        overlap(a->context_out, list, a->block_table, list * a->table_cols))
         return SSD_ERR_INVALID_ARG;
     if (a->total_tokens == 0 || a->num_seqs == 0) return SSD_OK;
     if (!a->k_new || !a->v_new || !a->k_cache || !a->v_cache || !a->k_scale || !a->v_scale ||
