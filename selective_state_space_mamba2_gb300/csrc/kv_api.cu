@@ -167,6 +167,9 @@ ssd_status_t check_commit_fp8(const kv_commit_fp8_args *a) {
         return SSD_ERR_INVALID_ARG;
     if ((int64_t)a->block_size * a->headdim > INT32_MAX) return SSD_ERR_INVALID_ARG;  // pieces of a block are counted in 32 bits
     if (a->num_seqs > 0 && (!a->cu_seqlens || !a->context_lens)) return SSD_ERR_INVALID_ARG;
+    if (!aligned4(a->cu_seqlens) || !aligned4(a->context_lens) || !aligned4(a->path) || !aligned4(a->path_lens) ||
+        !aligned4(a->context_out) || !aligned4(a->err_word))
+        return SSD_ERR_INVALID_ARG;
     // what one CTA writes, others read
     const int64_t list = 4ll * a->num_seqs;
     if (overlap(a->context_out, list, a->context_lens, list) || overlap(a->context_out, list, a->cu_seqlens, list + 4) ||
@@ -189,6 +192,7 @@ ssd_status_t check_read_fp8(const kv_read_fp8_args *a) {
     if (!pages8_ok(a->block_size, a->num_blocks, a->cache_block_stride, row) || !table_ok(a->table_cols, a->block_size))
         return SSD_ERR_INVALID_ARG;
     if (a->num_seqs > 0 && !a->cu_seqlens) return SSD_ERR_INVALID_ARG;
+    if (!aligned4(a->cu_seqlens) || !aligned4(a->starts) || !aligned4(a->err_word)) return SSD_ERR_INVALID_ARG;
     if (a->total_tokens == 0 || a->num_seqs == 0) return SSD_OK;
     if (!a->k_cache || !a->v_cache || !a->k_scale || !a->v_scale || !a->k_out || !a->v_out ||
         (a->table_cols > 0 && !a->block_table) || !aligned16(a->k_cache) || !aligned16(a->v_cache) ||
@@ -206,6 +210,9 @@ ssd_status_t check_verify(const kv_verify_args *a) {
         return SSD_ERR_INVALID_ARG;
     if (a->num_seqs == 0) return SSD_OK;
     if (!a->cu_seqlens || !a->path || !a->path_lens || !a->accepted || !a->next_tokens) return SSD_ERR_INVALID_ARG;
+    if (!aligned4(a->cu_seqlens) || !aligned4(a->path) || !aligned4(a->path_lens) || !aligned4(a->accepted) ||
+        !aligned4(a->next_tokens) || !aligned4(a->err_word))
+        return SSD_ERR_INVALID_ARG;
     if (a->total_tokens == 0) return SSD_OK;
     const uintptr_t most = (uintptr_t)elem_bytes(a->dtype) - 1;
     if (!a->tokens || !a->uniform || !a->target_probs || (reinterpret_cast<uintptr_t>(a->target_probs) & most) ||
@@ -291,7 +298,9 @@ extern "C" ssd_status_t kv_tree_attention_fp8(const kv_attention_args *a, const 
     if (st != SSD_OK || empty(a)) return st;
     st = check_attention_pointers(a);
     if (st != SSD_OK) return st;
-    if (!k_scale || !v_scale || !aligned4(k_scale) || !aligned4(v_scale)) return SSD_ERR_INVALID_ARG;
+    if (!k_scale || !v_scale || !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(a->cu_seqlens) ||
+        !aligned4(a->context_lens) || !aligned4(a->err_word))
+        return SSD_ERR_INVALID_ARG;
     const bool tc = fp8_tc(a);
     const size_t need = tc ? ssd::kv_attention_fp8_tc_workspace(*a) : ssd::kv_attention_simt_workspace(*a);
     if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
