@@ -40,10 +40,19 @@ namespace ssd {
 namespace {
 
 using namespace tc;
+using fp8::max_u16x2;
+using kvtc::copies_arrive;
+using kvtc::copy4;
+using kvtc::cvt_f16x2;
 using kvtc::ex2;
 using kvtc::kLn2;
 using kvtc::kLog2e;
+using kvtc::log2_of;
+using kvtc::max3;
 using kvtc::nonfinite_bf16x2;
+using kvtc::reciprocal;
+using kvtc::split4;
+using kvtc::sub_f16x2;
 using kvtc::Waiter;
 
 constexpr int kThreads = 192;
@@ -109,33 +118,6 @@ template <int width> __device__ __forceinline__ uint64_t row_desc(const void *p,
     return width == 128 ? sw128_desc(at, lbo, 1024) : width == 64 ? sw64_desc(at, lbo, 512) : sw32_desc(at, lbo, 256);
 }
 
-__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t e4m3x2(uint32_t f16x2) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(f16x2));
-    return r;
-}
-__device__ __forceinline__ uint32_t f16x2_of(uint32_t codes) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
-    return r;
-}
-__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-// Four values in two e4m3 parts.
-__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t &high, uint32_t &low) {
-    const uint32_t x = cvt_f16x2(a, b), y = cvt_f16x2(c, d);
-    const uint32_t hx = e4m3x2(x), hy = e4m3x2(y);
-    high = __byte_perm(hx, hy, 0x5410);
-    low = __byte_perm(e4m3x2(sub_f16x2(x, f16x2_of(hx))), e4m3x2(sub_f16x2(y, f16x2_of(hy))), 0x5410);
-}
 // Four weights, as fp16, in e5m2 parts: an fp16 number's first byte, and the rest times 8 (neither rounds).
 __device__ __forceinline__ void pieces4(float2 a, float2 b, uint32_t (&part)[kPieces]) {
     constexpr uint32_t kFirst = 0xFF00FF00u, kEight = 0x48004800u;  // first bytes; 8, twice
@@ -149,26 +131,6 @@ __device__ __forceinline__ void pieces4(float2 a, float2 b, uint32_t (&part)[kPi
     }
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-__device__ __forceinline__ float log2_of(float v) {
-    float r;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-__device__ __forceinline__ float reciprocal(float v) {
-    float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 // Whether any of the softmax threads says so; all of them call it.
 __device__ __forceinline__ bool vote(bool mine) {
     uint32_t any;
@@ -177,12 +139,6 @@ __device__ __forceinline__ bool vote(bool mine) {
                  : "r"((uint32_t)mine), "n"(kVoteBar)
                  : "memory");
     return any != 0;
-}
-__device__ __forceinline__ void copies_arrive(uint64_t *bar) {  // when this thread's copies are done
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ void copy4(void *dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 template <int N> __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[N]) {
     if constexpr (N == 16)

@@ -34,6 +34,12 @@ __device__ __forceinline__ uint2 encode8(const float (&v)[8]) {
     return make_uint2(encode2(v[0], v[1]) | encode2(v[2], v[3]) << 16, encode2(v[4], v[5]) | encode2(v[6], v[7]) << 16);
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // The smallest power of two s with top <= 448 s (448 = 1.75 * 2^8), within the limits; top finite, not negative.
 __device__ __forceinline__ float scale_for(float top) {
     const uint32_t bits = __float_as_uint(top);

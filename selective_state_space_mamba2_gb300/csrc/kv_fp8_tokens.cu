@@ -4,11 +4,7 @@
 namespace ssd {
 namespace {
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
+using fp8::max_u16x2;
 
 // 8 values of a row in registers
 template <typename T> struct Eight;

@@ -1,5 +1,5 @@
-// What the tensor-core kernels of attention over pages share: tile sizes, waits, which keys a row sees, values that are
-// not finite.
+// What the tensor-core kernels of attention over pages share: tile sizes, waits, conversions, which keys a row sees, values
+// that are not finite.
 #pragma once
 #include "kv_sched.cuh"
 #include "tc_ptx.cuh"
@@ -42,6 +42,59 @@ __device__ __forceinline__ float ex2(float v) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
+}
+
+__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t f16x2) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(f16x2));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16x2_of(uint32_t codes) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
+    return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Four values in two e4m3 parts.
+__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t &high, uint32_t &low) {
+    const uint32_t x = cvt_f16x2(a, b), y = cvt_f16x2(c, d);
+    const uint32_t hx = e4m3x2(x), hy = e4m3x2(y);
+    high = __byte_perm(hx, hy, 0x5410);
+    low = __byte_perm(e4m3x2(sub_f16x2(x, f16x2_of(hx))), e4m3x2(sub_f16x2(y, f16x2_of(hy))), 0x5410);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float log2_of(float v) {
+    float r;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float reciprocal(float v) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// An arrival of this thread on `bar` when the asynchronous copies that it has asked for are done, without being counted up front.
+__device__ __forceinline__ void copies_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void copy4(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
 // bits [0, n) set, n clamped to 0 .. 64
