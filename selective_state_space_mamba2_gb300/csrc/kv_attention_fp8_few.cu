@@ -81,7 +81,6 @@ struct Params {
 };
 
 template <int R> constexpr int kStages = R == 16 ? 5 : 4;
-template <int R> constexpr int kPlaces = R == 16 ? 2 : 1;  // tiles whose weights are kept
 
 template <int R> struct Bars {
     enum {
@@ -94,8 +93,8 @@ template <int D, int R> struct Layout {
     static constexpr int kParts = 0;                              // [2R] rows of D bytes: high parts, low parts
     static constexpr int kQ = kParts + 2 * R * D;                 // queries: [D / 64][R] rows of 128 bytes
     static constexpr int kP = kQ + R * D * 2;                     // weights: [128] rows of 4R bytes, a part after the other
-    static constexpr int kPlace = kKeys * kPieces * R;            // (of new tokens: two tiles of 2R bytes, high and low parts)
-    static constexpr int kRing = kP + kPlaces<R> * kPlace;
+                                                                  // (of new tokens: two tiles of 2R bytes, high and low parts)
+    static constexpr int kRing = kP + kKeys * kPieces * R;
     static constexpr int kScales = kRing + kStages<R> * kStage;   // [kScaleRing][2][kBoxes]: ks, vs of a tile's boxes
     static constexpr int kFactors = kScales + kScaleRing * 2 * kBoxes * 4;  // [2][R]: c / u of an item's rows
     static constexpr int kTops = kFactors + 2 * R * 4;            // [R]: m
@@ -459,15 +458,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         };
         auto output = [&](uint32_t g, bool cached, uint32_t add) {  // of tile number g
             const uint32_t s0 = take(), s1 = !cached && kHalves > 1 ? take() : s0;
-            const uint32_t gg = __shfl_sync(~0u, g, 0), place = gg % kPlaces<R> * L::kPlace;
+            const uint32_t gg = __shfl_sync(~0u, g, 0);
             wait(&bar[B::P_READY0 + (g & 1)], (g >> 1) & 1);
             tc_fence_after();
             if (elect_one()) {
                 if (cached) {
-                    const uint64_t v0 = desc_at(dV8, s0 * kStage), p0 = desc_at(dP8, place);
+                    const uint64_t v0 = desc_at(dV8, s0 * kStage);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma8_ss(tmu + COL_O, desc_at(v0, 32 * D * k), desc_at(p0, 32 * kPieces * R * k), kIdO8, k > 0 ? 1u : add);
+                        mma8_ss(tmu + COL_O, desc_at(v0, 32 * D * k), desc_at(dP8, 32 * kPieces * R * k), kIdO8, k > 0 ? 1u : add);
                 } else {
                     // 64 keys in a stage, or all 128 of 64 columns; high parts to the first columns, low ones to the next
 #pragma unroll
@@ -475,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             mma_ss(tmu + COL_O + R * part, desc_at(dV, (kHalves > 1 && k > 3 ? s1 * kStage + 2048 * (k - 4) : s0 * kStage + 2048 * k)),
-                                   desc_at(dP, place + part * (kKeys * 2 * R) + 32 * R * k), kIdO, k > 0 ? 1u : add);
+                                   desc_at(dP, part * (kKeys * 2 * R) + 32 * R * k), kIdO, k > 0 ? 1u : add);
                 }
                 mma_commit(&bar[B::O_DONE0 + (gg & 1)]);
                 mma_commit(&bar[B::KV_EMPTY0 + s0]);
@@ -665,10 +664,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     sum[r] = fma_f2(v[r], make_float2(inv, inv), sum[r]);
                 }
-                // where the weights go is free
-                if (tile >= kPlaces<R>)
-                    wait(&bar[B::O_DONE0 + ((tile - kPlaces<R>) & 1)], ((tile - kPlaces<R>) >> 1) & 1);
-                uint8_t *to = smem + L::kP + tile % kPlaces<R> * L::kPlace;
+                // where the weights go is free (two places: no faster)
+                if (tile > 0) wait(&bar[B::O_DONE0 + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1);
+                uint8_t *to = smem + L::kP;
                 if (cached) {
 #pragma unroll
                     for (int i = 0; i < R / 16; ++i) {
