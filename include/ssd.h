@@ -760,7 +760,7 @@ SSD_API ssd_status_t kv_commit_tokens(const kv_commit_args *args, ssd_stream_t s
  *   need = the smallest 2^j, -64 <= j <= 119, with |x| <= 448 * 2^j for all finite new values (2^-64 without any)
  *   scale <- need, or max(scale, need) where the block has earlier rows (its first row is before the context's end)
  *   earlier rows, where the scale grew: code <- e4m3(code * old scale / new scale)
- *   new rows: code = e4m3(x / scale)
+ *   new rows: code = e4m3(x / scale) (a scale that another writer left and that is no power of two: x times its reciprocal)
  * e4m3() rounds to nearest, ties to even.  Values beyond 448 * 2^119 are held as that, infinities and NaN as NaN.
  * Rows behind the last written one keep what they hold.  Blocks written must be distinct: one that requests share (a
  * prefix) is copied before a request appends to it.
@@ -798,7 +798,7 @@ SSD_API ssd_status_t kv_commit_tokens_fp8(const kv_commit_fp8_args *args, ssd_st
 /*
  * kv_read_tokens_fp8 -- a stretch of each request's cached tokens, packed, in a token type:
  *   k_out[cu_seqlens[r] + i] = k of position starts[r] + i of request r,  i < cu_seqlens[r+1] - cu_seqlens[r],
- * v_out likewise; the product code * scale is rounded once.  Rows that no request has are left as they were.
+ * v_out likewise; the product code * scale is fp32's (exact for the scales that kv_commit_tokens_fp8 writes), then rounded.  Rows that no request has are left as they were.
  * SSD_DEVERR_METADATA: cu_seqlens entries that decrease or leave [0, T], a negative start, or positions beyond the table
  * row (that request's rows are left as they were; behind cu_seqlens entries that decrease, others' may be, too);
  * SSD_DEVERR_SLOT: a block id outside [0, num_blocks) (zeros).
@@ -831,8 +831,8 @@ SSD_API ssd_status_t kv_read_tokens_fp8(const kv_read_fp8_args *args, ssd_stream
  * times the scales and their sum without.
  * On the tensor cores (bf16, the sizes of kv_tree_attention, block_size a multiple of 8, blocks a multiple of 16 bytes
  * apart) the codes of keys are operands as they are, and queries that meet them are sums of two e4m3 parts, which lose at
- * most 2^-17 of a row's largest entry; weights of cached values as sums of two e4m3 parts (row tiles of at most 32 rows: off by 2^-8 of themselves) or as
- * fp16 (larger ones, 2^-11).  Everything else runs in fp32 on the CUDA cores.
+ * most 2^-17 of a row's largest entry.  Weights of cached values, each times its value's scale, are rounded to fp16: off by
+ * 2^-11 of themselves, or by 2^-36 of the row's largest.  Everything else runs in fp32 on the CUDA cores.
  * Errors, workspace and host checks as there; k_scale and v_scale are required.
  */
 SSD_API size_t kv_tree_attention_fp8_workspace_size(const kv_attention_args *args);

@@ -7,7 +7,7 @@
 //   O^T += V^T P       e4m3 times e5m2, headdim x 4R, K = 128: all parts at once, each to its own columns
 // R is 16 or 32.  A key's scales ks, vs are constants of its thread; u is the row's unit, the power of two that puts its
 // largest query entry in [128, 256).  A tile's codes are read once for each product, 16 KB and 16 KB, whatever the rows
-// (with the queries as rows, padded to 128 of them, a product read them, too: 642 cycles of an SM for 64 keys, here 320 for
+// (with the queries as rows, padded to 128 of them, a product read them, too: 642 cycles of an SM for 64 keys, here 352 for
 // 128), and a thread has R weights to make for 128 keys, not 64 for 64.
 //
 // m belongs to a row.  It is 2^12 below the row's largest weight when it is set, and a tile is taken by it as long as no
@@ -25,9 +25,11 @@
 // New tokens' tiles are bf16 with the queries as they were given: 64-column halves of 128 keys, and 64 keys' values, in a
 // ring stage each; weights as two bf16 parts.
 //
-// What bounds it: HBM for large batches (256 requests of 4 tokens over up to 8192 in blocks of 64, 2.27 GB, 382 to 391 us, 0.86
-// to 0.88 of the copy rate; a 16-bit cache 664 us), latency for one token over 777 (12 us with the join).  Queries as
-// rows, padded to 128 of them, took 603 us; three CTAs to an SM 416; every CTA with heads of its own choice 535.
+// What bounds it: HBM for large batches (256 requests of 4 tokens over up to 8192 in blocks of 64, 2.27 GB, 385 to 398 us, 0.84
+// to 0.87 of the copy rate; a 16-bit cache 664 us), the softmax warps' instructions with tiles of 32 rows (64 requests of 8 tokens, 4
+// query heads to a key head, over up to 8192: 182 us; 164 with two e4m3 parts, 7 instructions for two weights instead of
+// 12), latency for one token over 777 (14.5 us with the join).  With weights in two e4m3 parts, on the first of these:
+// queries as rows, padded to 128 of them, 603 us; three CTAs to an SM 416; every CTA with heads of its own choice 535; now 391.
 //
 // Masked places: a weight that must not count is set to 0, whatever its score is.  Values' rows that are not there
 // are zeroed in shared memory; new tokens' values that are not finite are taken out and added at the end.  Waits are bounded as in
@@ -564,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     wait(&bar[B::SCALES0 + scaled % kScaleRing], scaled / kScaleRing & 1);
                     const float *sc = scales + (scaled % kScaleRing) * 2 * kBoxes + (tid >> p.box_shift);
                     const float vs = sc[kBoxes];
-                    f = sc[0], shift = log2_of(vs), inv = reciprocal(vs);
+                    f = sc[0], shift = log2_of(vs), inv = reciprocal(vs);  // exact for powers of two, else off by 2^-22
                     ++scaled;
                 }
                 wait(&bar[B::S_FULL0 + (tile & 1)], (tile >> 1) & 1);

@@ -25,7 +25,7 @@
 // of it for the scores (both parts of the queries are read), 128 for the values' product, 128 for the copies and 192 for the
 // widening, 833 in all, of 1040 that pass; a tile of the 16-bit kernel 768.  The softmax warps issue 0.46 instructions a
 // cycle and scheduler (3 warps a scheduler, each a chain).  Measured on 4 prompts of 512 to 4096 tokens over up to 8192
-// (blocks of 64) / 24 trees of 33 to 64 over up to 16384 (blocks of 32): 961 / 240 us (a 16-bit cache: 721 / 184).
+// (blocks of 64) / 24 trees of 33 to 64 over up to 16384 (blocks of 32): 974 / 245 us (a 16-bit cache: 741 / 188).
 // Ways that were measured and not taken, with the time of this one then:
 //   constants of every 8 keys, whatever the blocks, not a kernel for each size of their common part   962 / 276 (961 / 240)
 //   one loop for cached and new tiles, of twice the code                                            1031 / 295 (962 / 276)

@@ -67,8 +67,8 @@ __device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
 // Which (request, block) an item is follows from closed forms: with a path, every request is given the most
 // blocks that max_path tokens can lie in; without, request r's items start at cu_seqlens[r] / b + 2 r.
 // What an item is takes four dependent reads, so a CTA of a large call has several, found side by side, a lane an item
-// (32768 tokens of 8 heads of 128 bf16 in blocks of 16: 67 us with one item a CTA, 36.9 now, 0.80 of the copy rate; it is
-// bound by instructions beside it.  256 paths of up to 5 tokens 6.2 us: latency).
+// (32768 tokens of 8 heads of 128 bf16 in blocks of 16: 67 us with one item a CTA, 37 to 39 now, 0.76 to 0.80 of the copy
+// rate; it is bound by instructions beside it.  256 paths of up to 5 tokens 8 us, again on the same 6.2: latency).
 
 constexpr int kThreads = 256;
 // pieces of 8 values that a thread holds: with 8, whole blocks of 16 rows are a warp's, which costs less an item, but a
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 //
 // A CTA has the rows of kReadTokens packed tokens, keys and values; a thread has kFlight pieces of kCodes codes on their
 // way at a time (16, or 8 where a head's size is no multiple of 16).  Bound by HBM: 16 prefixes of 500 to 8192 tokens of 8
-// heads of 128 to bf16, 427 MB, 61 us, the copy rate (8 codes a piece: 73 us).
+// heads of 128 to bf16, 346 MB, 62 us, 0.82 of the copy rate (8 codes a piece: 73 us).
 
 constexpr int kReadTokens = 8;
 constexpr int kFlight = 4;

@@ -6,8 +6,9 @@
 // token that is turned down in a tree.  Weights are whole multiples of 2^-44 in 64 bits, so that sums are exact, the
 // same in any order, and every CTA decides alike.  The row is summed in segments of 1024 entries, whose sums stay
 // in shared memory: the one that the drawn mark falls into is read again and walked through.
-// Bound by the bytes of the rows, the copy rate (256 chains of 1 + 3 over 65536 fp32 entries 19.8 us), or by latency
-// for a few requests (5 trees of 24 over 50021 entries 8.6 us: the walk by one warp, then the sum; 12.0 with the drafted
+// Bound by the bytes of the rows (256 chains of 1 + 3 over 65536 fp32 entries, 134 MB, 25 to 27 us, 0.73 to 0.8 of the copy
+// rate; again on the same rows, of which L2 holds a part, 19.8), or by latency for a few requests (5 trees of 24 over 50021
+// entries 10 to 12 us, again on the same rows 8.6: the walk by one warp, then the sum; 12.0 with the drafted
 // tokens read again where they are needed and the mark's segment walked through by one warp, and the chains 23.5).
 #include <cooperative_groups.h>
 
@@ -448,7 +449,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 4) kv_verify_k
 }
 
 template <typename T> cudaError_t launch(const kv_verify_args &a, cudaStream_t s) {
-    // CTAs of a request: as many as run at once, each with 2048 entries at least (256 chains of 65536 entries 19.8 us with 2,
+    // CTAs of a request: as many as run at once, each with 2048 entries at least (256 chains of 65536 entries, again on the same rows, 19.8 us with 2,
     // 21.7 with one, 24.4 with 4: the walk costs each the same)
     int ctas = 1;
     while (ctas < kMostCluster && (int64_t)a.num_seqs * ctas * 2 <= 4ll * device_sms() && a.vocab / (ctas * 2) >= 2048) ctas *= 2;
